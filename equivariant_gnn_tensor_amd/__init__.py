@@ -13,4 +13,8 @@ from ._binding import (  # noqa: F401
     etpc_layout_convert, etpc_radius_graph, etpc_radius_graph_workspace_size,
     etpc_degree_order, etpc_degree_order_workspace_size, RECV_ORDER_WINDOW, SEND_ORDER_WINDOW,
     etpc_spatial_order, etpc_spatial_order_workspace_size,
+    etpc_dropout, etpc_layer_norm, etpc_layer_norm_backward, etpc_layer_norm_workspace_size,
+    etpc_dropout_add_layer_norm, etpc_dropout_add_layer_norm_backward,
+    etpc_irreps_dims, etpc_irreps_dropout, etpc_irreps_norm, etpc_irreps_norm_backward,
+    etpc_irreps_norm_workspace_size,
 )

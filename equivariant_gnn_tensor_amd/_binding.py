@@ -9,6 +9,7 @@ raises ImportError: there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 from typing import Dict, List, Optional, Sequence, Tuple
@@ -66,6 +67,10 @@ class etpc_graph(C.Structure):
     ]
 
 
+class etpc_dropout_spec(C.Structure):
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64), ("offset_add", C.c_void_p)]
+
+
 SYMBOLS = (
     "etpc_plan_create", "etpc_plan_destroy", "etpc_plan_info", "etpc_plan_path", "etpc_plan_out_irrep",
     "etpc_plan_cg", "etpc_workspace_size", "etpc_csr_workspace_size", "etpc_csr_build", "etpc_graph_validate",
@@ -73,16 +78,20 @@ SYMBOLS = (
     "etpc_profile_enable", "etpc_profile_read", "etpc_radius_graph_workspace_size", "etpc_radius_graph",
     "etpc_layout_convert", "etpc_last_error", "etpc_degree_order_workspace_size", "etpc_degree_order",
     "etpc_degree_order_within", "etpc_spatial_order_workspace_size", "etpc_spatial_order",
+    "etpc_dropout", "etpc_layer_norm", "etpc_layer_norm_workspace_size", "etpc_layer_norm_backward",
+    "etpc_dropout_add_layer_norm", "etpc_dropout_add_layer_norm_backward", "etpc_irreps_dims", "etpc_irreps_dropout",
+    "etpc_irreps_norm", "etpc_irreps_norm_workspace_size", "etpc_irreps_norm_backward",
 )
-KINDS = ("csr", "fwd_traverse", "channel_gemm", "bwd_traverse", "node_gemm", "aux", "prep")
+KINDS = ("csr", "fwd_traverse", "channel_gemm", "bwd_traverse", "node_gemm", "aux", "prep", "nodewise")
 
 
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is not built (python equivariant_gnn_tensor_amd/build.py)")
     lib = C.CDLL(_LIB_PATH)
-    vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
+    vp, i32, i64, sz, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
     P = C.POINTER
+    ir, ds = P(etpc_irrep), P(etpc_dropout_spec)
     lib.etpc_last_error.restype = C.c_char_p
     lib.etpc_last_error.argtypes = []
     sig = {
@@ -110,6 +119,18 @@ def _load():
         "etpc_radius_graph_workspace_size": [i32, i64, P(sz)],
         "etpc_radius_graph": [i32, vp, C.c_float, P(C.c_float), i64, vp, vp, P(i64), vp, sz, vp],
         "etpc_layout_convert": [vp, i32, i32, i32, vp, vp, vp],
+        "etpc_dropout": [i64, i64, i32, vp, i64, ds, vp, i64, vp],
+        "etpc_layer_norm": [i64, i64, i32, vp, i64, vp, vp, f32, vp, i64, vp, vp, vp],
+        "etpc_layer_norm_workspace_size": [i64, i64, P(sz)],
+        "etpc_layer_norm_backward": [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp],
+        "etpc_dropout_add_layer_norm": [i64, i64, i32, vp, i64, vp, i64, ds, vp, vp, f32, vp, i64, vp, i64, vp, vp, vp],
+        "etpc_dropout_add_layer_norm_backward": [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, ds, vp, i64, vp,
+                                                 i64, vp, vp, vp, sz, vp],
+        "etpc_irreps_dims": [i32, ir, P(i64), P(i64), P(i64)],
+        "etpc_irreps_dropout": [i32, ir, i32, vp, ds, vp, vp],
+        "etpc_irreps_norm": [i32, ir, i32, vp, vp, vp, f32, vp, vp, vp],
+        "etpc_irreps_norm_workspace_size": [i32, ir, i32, P(sz)],
+        "etpc_irreps_norm_backward": [i32, ir, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -552,3 +573,287 @@ def etpc_profile_read(kind) -> Tuple[float, int]:
     ms, n = C.c_double(), C.c_int64()
     _check(lib.etpc_profile_read(k, C.byref(ms), C.byref(n)))
     return ms.value, n.value
+
+
+# ---------------------------------------------------------------- node-wise operators
+# Rows of f32, bf16 or f16 tensors: any shape [..., C] whose leading axes are one axis with
+# one stride (a view like x[:, a:b] qualifies); parameters and statistics are f32.
+_ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # etpc_dtype
+
+
+def _row_type(x: torch.Tensor) -> int:
+    try:
+        return _ROW_TYPES[x.dtype]
+    except KeyError:
+        raise TypeError(f"rows must be float32, bfloat16 or float16, got {x.dtype}") from None
+
+
+def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> Tuple[int, int, int, int]:
+    """(pointer, row stride, rows, columns) of a tensor, which has to match `like`."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if like is None:
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    elif t is not like:
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    shape, strides = t.shape, t.stride()
+    if not shape:
+        raise ValueError(f"{name} must have at least one axis")
+    cols = shape[-1]
+    if t.numel() == 0:
+        rows = 1
+        for n in shape[:-1]:
+            rows *= n
+        return t.data_ptr(), cols, rows, cols
+    if cols > 1 and strides[-1] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    rows, stride = 1, cols
+    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if n == 1:
+            continue
+        if rows == 1:
+            stride = st
+        elif st != rows * stride:
+            raise ValueError(f"{name}: the leading axes must be one axis of rows with one stride")
+        rows *= n
+    return t.data_ptr(), stride, rows, cols
+
+
+def _vector(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[int]:
+    """Pointer of a contiguous f32 tensor of n numbers (None passes)."""
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} numbers, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return _ptr(t, torch.float32)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output, allocated on the call's stream (see _workspace)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _drop_spec(p: float, seed: int, offset, device) -> etpc_dropout_spec:
+    """offset: a whole number, or a one-element int64 tensor on the GPU that is read when the
+    kernel runs (what a captured graph needs for a fresh mask in every replay)."""
+    m64 = (1 << 64) - 1
+    if isinstance(offset, torch.Tensor):
+        if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
+            raise ValueError(f"an offset tensor is one int64 number on {device}")
+        return etpc_dropout_spec(p, seed & m64, 0, offset.data_ptr())
+    return etpc_dropout_spec(p, seed & m64, offset & m64, None)
+
+
+def etpc_dropout(x, p: float, seed: int, offset=0, y=None, stream=None) -> torch.Tensor:
+    """y = x with elements dropped with probability p and the rest scaled by 1 / (1 - p), over
+    the rows x [..., C]; y may be x.  The gradient is the same call on y_bar."""
+    dtype = _row_type(x)
+    xp, xs, rows, cols = _rows("x", x)
+    if y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    yp, ys, _, _ = _rows("y", y, x)
+    _check(lib.etpc_dropout(rows, cols, dtype, xp, xs, C.byref(_drop_spec(p, seed, offset, x.device)), yp, ys,
+                            _stream(stream)))
+    return y
+
+
+def _norm_forward(x, residual, drop, w, b, eps, y, h, keep_h, stats, mean, rstd, stream):
+    dtype, dev = _row_type(x), x.device
+    xp, xs, rows, cols = _rows("x", x)
+    rp, rs = _rows("residual", residual, x)[:2] if residual is not None else (None, 0)
+    wp, bp = _vector("w", w, cols, dev), _vector("b", b, cols, dev)
+    if y is None:
+        y = _new(x.shape, x.dtype, dev, stream)
+    if h is None and keep_h:
+        h = _new(x.shape, x.dtype, dev, stream)
+    if stats:
+        lead = x.shape[:-1]
+        mean = _new(lead, torch.float32, dev, stream) if mean is None else mean
+        rstd = _new(lead, torch.float32, dev, stream) if rstd is None else rstd
+    yp, ys = _rows("y", y, x)[:2]
+    hp, hs = _rows("h", h, x)[:2] if h is not None else (None, 0)
+    mp, sp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev)
+    if keep_h:
+        st = lib.etpc_dropout_add_layer_norm(rows, cols, dtype, xp, xs, rp, rs, drop, wp, bp, eps, yp, ys, hp, hs, mp,
+                                             sp, _stream(stream))
+    else:
+        st = lib.etpc_layer_norm(rows, cols, dtype, xp, xs, wp, bp, eps, yp, ys, mp, sp, _stream(stream))
+    _check(st)
+    return y, h, mean, rstd
+
+
+def etpc_layer_norm(x, w=None, b=None, eps: float = 1e-5, y=None, mean=None, rstd=None, stats: bool = True,
+                    stream=None):
+    """(y, mean, rstd): y = (x - mean) rstd w + b over the rows x [..., C].  stats=False skips
+    the statistics (inference) and returns (y, None, None)."""
+    y, _, mean, rstd = _norm_forward(x, None, None, w, b, eps, y, None, False, stats, mean, rstd, stream)
+    return y, mean, rstd
+
+
+def etpc_layer_norm_workspace_size(n_rows: int, n_cols: int) -> int:
+    b = C.c_size_t()
+    _check(lib.etpc_layer_norm_workspace_size(n_rows, n_cols, C.byref(b)))
+    return b.value
+
+
+def _scratch(ws, nbytes: int, device, stream):
+    """(pointer, bytes, tensor to keep alive) of a caller's workspace or a new one."""
+    if ws is None:
+        ws, _ = _workspace(nbytes, device, stream) if stream is not None or nbytes <= 0 else (
+            torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes)
+        return (None, 0, None) if ws is None else (ws.data_ptr(), nbytes, ws)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous and on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _norm_backward(h, y_bar, mean, rstd, w, h_bar, drop, want, outs, ws, stream):
+    dtype, dev = _row_type(h), h.device
+    hp, hs, rows, cols = _rows("x" if drop is False else "h", h)
+    yp, ys = _rows("y_bar", y_bar, h)[:2]
+    bp, bs = _rows("h_bar", h_bar, h)[:2] if h_bar is not None else (None, 0)
+    mp, sp, wp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev), _vector("w", w, cols, dev)
+    if outs is None:
+        outs = tuple(None if name not in want else _new(h.shape, h.dtype, dev, stream) if name in ("x", "residual")
+                     else _new((cols,), torch.float32, dev, stream) for name in ("x", "residual", "w", "b"))
+    x_bar, r_bar, w_bar, b_bar = outs
+    xbp, xbs = _rows("x_bar", x_bar, h)[:2] if x_bar is not None else (None, 0)
+    rbp, rbs = _rows("residual_bar", r_bar, h)[:2] if r_bar is not None else (None, 0)
+    wbp, bbp = _vector("w_bar", w_bar, cols, dev), _vector("b_bar", b_bar, cols, dev)
+    need = etpc_layer_norm_workspace_size(rows, cols) if wbp is not None or bbp is not None else 0
+    wsp, wsn, _keep = _scratch(ws, need, dev, stream)
+    if drop is False:
+        st = lib.etpc_layer_norm_backward(rows, cols, dtype, hp, hs, yp, ys, mp, sp, wp, xbp, xbs, wbp, bbp, wsp, wsn,
+                                          _stream(stream))
+    else:
+        st = lib.etpc_dropout_add_layer_norm_backward(rows, cols, dtype, hp, hs, yp, ys, bp, bs, mp, sp, wp, drop, xbp,
+                                                      xbs, rbp, rbs, wbp, bbp, wsp, wsn, _stream(stream))
+    _check(st)
+    return outs
+
+
+def etpc_layer_norm_backward(x, y_bar, mean, rstd, w=None, want=("x", "w", "b"), outs=None, ws=None, stream=None):
+    """(x_bar, w_bar, b_bar) of <y_bar, y>; None for what `want` leaves out.  outs: three
+    caller-given tensors (or None to skip one)."""
+    if outs is not None:
+        outs = (outs[0], None, outs[1], outs[2])
+    x_bar, _, w_bar, b_bar = _norm_backward(x, y_bar, mean, rstd, w, None, False, want, outs, ws, stream)
+    return x_bar, w_bar, b_bar
+
+
+def etpc_dropout_add_layer_norm(x, residual, w=None, b=None, p: float = 0.0, seed: int = 0, offset=0,
+                                eps: float = 1e-5, y=None, h=None, mean=None, rstd=None, stats: bool = True,
+                                stream=None):
+    """(y, h, mean, rstd): h = residual + dropout(x) (residual may be None), y = layer_norm(h)."""
+    drop = C.byref(_drop_spec(p, seed, offset, x.device))
+    return _norm_forward(x, residual, drop, w, b, eps, y, h, True, stats, mean, rstd, stream)
+
+
+def etpc_dropout_add_layer_norm_backward(h, y_bar, mean, rstd, w=None, h_bar=None, p: float = 0.0, seed: int = 0,
+                                         offset=0, want=("x", "residual", "w", "b"), outs=None, ws=None, stream=None):
+    """(x_bar, residual_bar, w_bar, b_bar) of <y_bar, y> + <h_bar, h>; None for what `want`
+    leaves out.  p, seed and offset as in the forward call."""
+    drop = C.byref(_drop_spec(p, seed, offset, h.device))
+    return _norm_backward(h, y_bar, mean, rstd, w, h_bar, drop, want, outs, ws, stream)
+
+
+class _Irreps:
+    """Blocks and widths of an irreps list, as the C calls take them."""
+
+    def __init__(self, blocks):
+        self.n = len(blocks)
+        self.c = (etpc_irrep * max(1, self.n))(*[etpc_irrep(*t) for t in blocks])
+        dim, channels, biases = C.c_int64(), C.c_int64(), C.c_int64()
+        _check(lib.etpc_irreps_dims(self.n, self.c, C.byref(dim), C.byref(channels), C.byref(biases)))
+        self.dim, self.channels, self.biases = dim.value, channels.value, biases.value
+
+
+@functools.lru_cache(maxsize=256)
+def _irreps_of(key) -> _Irreps:
+    return _Irreps(parse_irreps(key))
+
+
+def _irreps(irreps) -> _Irreps:
+    return _irreps_of(irreps if isinstance(irreps, str) else tuple(tuple(t) for t in irreps))
+
+
+def etpc_irreps_dims(irreps) -> Dict[str, int]:
+    """Width of a feature row, number of channels (gains) and of 0e channels (biases)."""
+    ir = _irreps(irreps)
+    return dict(dim=ir.dim, channels=ir.channels, biases=ir.biases)
+
+
+def _features(name, t, ir: _Irreps, like=None) -> int:
+    if t.dim() != 2 or t.shape[1] != ir.dim:
+        raise ValueError(f"{name} must have shape (n_nodes, {ir.dim}), got {tuple(t.shape)}")
+    if like is not None:
+        _check_shape(name, t, tuple(like.shape), like.device)
+    elif t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return _ptr(t)
+
+
+def etpc_irreps_dropout(irreps, x, p: float, seed: int, offset=0, y=None, stream=None) -> torch.Tensor:
+    """Dropout of whole channels of ir_mul features x [N, dim]: the components of a (node,
+    channel) share their mask, so rotations commute with it; y may be x."""
+    ir = _irreps(irreps)
+    xp = _features("x", x, ir)
+    if y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    _check(lib.etpc_irreps_dropout(ir.n, ir.c, x.shape[0], xp, C.byref(_drop_spec(p, seed, offset, x.device)),
+                                   _features("y", y, ir, x), _stream(stream)))
+    return y
+
+
+def etpc_irreps_norm(irreps, x, w=None, b=None, eps: float = 1e-5, y=None, stats=None, keep_stats: bool = True,
+                     stream=None):
+    """(y, stats): the layer norm of ir_mul features that commutes with rotations and
+    reflections.  w: one gain per channel; b: one bias per 0e channel; stats [N, blocks, 2]
+    holds (mean, rstd) for the backward pass (None with keep_stats=False)."""
+    ir, dev = _irreps(irreps), x.device
+    xp = _features("x", x, ir)
+    n = x.shape[0]
+    if y is None:
+        y = _new(x.shape, x.dtype, dev, stream)
+    if stats is None and keep_stats:
+        stats = _new((n, ir.n, 2), torch.float32, dev, stream)
+    _check(lib.etpc_irreps_norm(ir.n, ir.c, n, xp, _vector("w", w, ir.channels, dev), _vector("b", b, ir.biases, dev),
+                                eps, _features("y", y, ir, x), _vector("stats", stats, 2 * n * ir.n, dev),
+                                _stream(stream)))
+    return y, stats
+
+
+def etpc_irreps_norm_workspace_size(irreps, n_nodes: int) -> int:
+    ir, b = _irreps(irreps), C.c_size_t()
+    _check(lib.etpc_irreps_norm_workspace_size(ir.n, ir.c, n_nodes, C.byref(b)))
+    return b.value
+
+
+def etpc_irreps_norm_backward(irreps, x, y_bar, stats, w=None, want=("x", "w", "b"), outs=None, ws=None, stream=None):
+    """(x_bar, w_bar, b_bar) of <y_bar, y>; None for what `want` leaves out."""
+    ir, dev = _irreps(irreps), x.device
+    xp, yp = _features("x", x, ir), _features("y_bar", y_bar, ir, x)
+    n = x.shape[0]
+    if outs is None:
+        outs = (_new(x.shape, x.dtype, dev, stream) if "x" in want else None,
+                _new((ir.channels,), torch.float32, dev, stream) if "w" in want else None,
+                _new((ir.biases,), torch.float32, dev, stream) if "b" in want else None)
+    x_bar, w_bar, b_bar = outs
+    xbp = _features("x_bar", x_bar, ir, x) if x_bar is not None else None
+    wbp, bbp = _vector("w_bar", w_bar, ir.channels, dev), _vector("b_bar", b_bar, ir.biases, dev)
+    need = etpc_irreps_norm_workspace_size(irreps, n) if w_bar is not None or b_bar is not None else 0
+    wsp, wsn, _keep = _scratch(ws, need, dev, stream)
+    _check(lib.etpc_irreps_norm_backward(ir.n, ir.c, n, xp, yp, _vector("stats", stats, 2 * n * ir.n, dev),
+                                         _vector("w", w, ir.channels, dev), xbp, wbp, bbp, wsp, wsn, _stream(stream)))
+    return outs

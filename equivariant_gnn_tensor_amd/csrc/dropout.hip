@@ -1,0 +1,112 @@
+// Dropout from a counter-based generator, over rows and over irreps features.
+//
+// y = kept ? x * scale : 0.  The mask is a function of (seed, offset, row, column) alone: it
+// is generated where it is used and never stored, and the gradient applies the same mask
+// again (the map is diagonal, hence its own adjoint).  One generator call serves eight
+// columns with 16 bits each, so a thread takes eight columns.
+#include <algorithm>
+
+#include "nodewise.hpp"
+#include "rows.hpp"
+
+namespace etpc {
+namespace {
+
+constexpr int kThreads = 256;
+
+// q = floor(a / d) for 0 <= a < 2^31 by a multiplication: RowMap's magic of the divisor d.
+__device__ inline uint32_t div_by(uint32_t a, const RowMap& m) { return (__umulhi(a, m.magic) + a) >> m.shift; }
+
+// More workgroups than this walk on (a launch holds less than 2^32 threads).
+constexpr int64_t kMaxGroups = int64_t{1} << 22;
+
+// Thread t of workgroup b takes vector b * 256 + t of the rows * vecs vectors.  The
+// workgroup divides its first index once in 64 bits; the threads divide what is left over.
+template <class T>
+__global__ __launch_bounds__(kThreads) void dropout_kernel(const T* x, int64_t xs, T* y, int64_t ys, int64_t total,
+                                                           int cols, RowMap vecs, DropArgs d) {
+  const uint64_t offset = d.threshold != 0 ? drop_offset(d) : 0;
+  for (uint64_t first = static_cast<uint64_t>(blockIdx.x) * kThreads; first + threadIdx.x < static_cast<uint64_t>(total);
+       first += static_cast<uint64_t>(gridDim.x) * kThreads) {
+    const uint64_t row0 = first / static_cast<uint32_t>(vecs.div);
+    const uint32_t left = static_cast<uint32_t>(first - row0 * static_cast<uint32_t>(vecs.div)) + threadIdx.x;
+    const uint32_t q = div_by(left, vecs);
+    const uint32_t vec = left - q * static_cast<uint32_t>(vecs.div);
+    const int64_t row = static_cast<int64_t>(row0 + q);
+    float v[8];
+    load8(x + row * xs, static_cast<int>(8 * vec), cols, v);
+    if (d.threshold != 0) drop8(v, philox(vec, static_cast<uint32_t>(row), offset, d.seed), d.threshold, d.scale);
+    store8(y + row * ys, static_cast<int>(8 * vec), cols, v);
+  }
+}
+
+// A thread takes eight channels of one block of one node, with all 2l+1 components: they
+// share one mask, so a kept channel turns under a rotation as before.
+template <int D>
+__device__ inline void drop_block(const float* x, float* y, const IrrepBlock& k, int c, const Philox& r,
+                                  const DropArgs& d) {
+  float v[D][8];
+#pragma unroll
+  for (int m = 0; m < D; ++m) load8(x + m * k.mul, c, k.mul, v[m]);
+#pragma unroll
+  for (int m = 0; m < D; ++m) {
+    if (d.threshold != 0) drop8(v[m], r, d.threshold, d.scale);
+    store8(y + m * k.mul, c, k.mul, v[m]);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void irreps_dropout_kernel(const IrrepTable t, const float* x, float* y,
+                                                                  int32_t rows, DropArgs d) {
+  const IrrepBlock k = t.blk[blockIdx.y];
+  const uint32_t groups = static_cast<uint32_t>(k.mul + 7) / 8;
+  const uint64_t offset = d.threshold != 0 ? drop_offset(d) : 0;
+  for (uint64_t id = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;;
+       id += static_cast<uint64_t>(gridDim.x) * kThreads) {
+    const uint64_t row = id / groups;
+    if (row >= static_cast<uint64_t>(rows)) return;
+    const int g = static_cast<int>(id - row * groups);
+    const Philox r = d.threshold != 0
+                         ? philox(static_cast<uint32_t>(k.group + g), static_cast<uint32_t>(row), offset, d.seed)
+                         : Philox{};
+    const int64_t at = static_cast<int64_t>(row) * t.dim + k.off;
+    if (k.l == 0) drop_block<1>(x + at, y + at, k, 8 * g, r, d);
+    else if (k.l == 1) drop_block<3>(x + at, y + at, k, 8 * g, r, d);
+    else if (k.l == 2) drop_block<5>(x + at, y + at, k, 8 * g, r, d);
+    else drop_block<7>(x + at, y + at, k, 8 * g, r, d);
+  }
+}
+
+unsigned groups_of(int64_t threads) {
+  return static_cast<unsigned>(std::min((threads + kThreads - 1) / kThreads, kMaxGroups));
+}
+
+template <class T>
+hipError_t rows_of(const void* x, int64_t xs, void* y, int64_t ys, int32_t rows, int32_t cols, const DropArgs& d,
+                   hipStream_t s) {
+  const int32_t vecs = (cols + 7) / 8;
+  const int64_t total = static_cast<int64_t>(rows) * vecs;
+  dropout_kernel<T><<<dim3(groups_of(total)), dim3(kThreads), 0, s>>>(
+      static_cast<const T*>(x), xs, static_cast<T*>(y), ys, total, cols, make_rowmap(0, 0, vecs), d);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const void* x, int64_t xs, void* y, int64_t ys, int32_t rows, int32_t cols, int dtype,
+                          const DropArgs& d, hipStream_t s) {
+  if (dtype == ETPC_F32) return rows_of<float>(x, xs, y, ys, rows, cols, d, s);
+  if (dtype == ETPC_BF16) return rows_of<Bf16>(x, xs, y, ys, rows, cols, d, s);
+  return rows_of<F16>(x, xs, y, ys, rows, cols, d, s);
+}
+
+hipError_t launch_irreps_dropout(const IrrepTable& t, const float* x, float* y, int32_t rows, const DropArgs& d,
+                                 hipStream_t s) {
+  int32_t most = 0;
+  for (int k = 0; k < t.n; ++k) most = std::max(most, (t.blk[k].mul + 7) / 8);
+  const int64_t total = static_cast<int64_t>(rows) * most;
+  irreps_dropout_kernel<<<dim3(groups_of(total), static_cast<unsigned>(t.n)),
+                          dim3(kThreads), 0, s>>>(t, x, y, rows, d);
+  return hipGetLastError();
+}
+
+}  // namespace etpc

@@ -323,6 +323,101 @@ etpc_status etpc_double_backward(etpc_plan plan, const etpc_graph* graph, const 
                                  float* z_bar_grad, float* x_grad, float* w_grad, float* pos_grad,
                                  void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------ node-wise operators
+ * What a network puts between two convolutions: layer norm, dropout, the residual join of
+ * the two, and the norm and dropout of irreps features.  They take no plan and no graph.
+ *
+ * Rows.  A matrix is n_rows rows of n_cols adjacent elements of one etpc_dtype; row r starts
+ * at pointer + r * stride elements, so a block of wider rows (the scalars inside ir_mul
+ * feature rows) is passed in place.  An input's stride is 0 (one row for all) or at least
+ * n_cols, an output's at least n_cols; pointers are aligned to the element, no more.
+ * Outputs do not overlap inputs or one another (etpc_dropout may work in place).  Gains,
+ * biases, statistics and the gradients of parameters are fp32 and contiguous whatever the
+ * dtype; sums are taken in fp32 and each result is rounded to the dtype once.
+ * n_rows < 2^31 and n_cols <= 2^30, else ETPC_ERR_OVERFLOW.  No rows is no work (parameter
+ * gradients are then zero). */
+typedef enum { ETPC_F32 = 0, ETPC_BF16 = 1, ETPC_F16 = 2 } etpc_dtype;
+
+/* Dropout with probability p in [0, 1], mask from a counter, never stored.  With
+ * T = rint(65536 p), element (row, c) is dropped when field c mod 8 of
+ * Philox4x32-10(counter = (c div 8, row, offset low, offset high), key = seed) is below T,
+ * the fields being the 16-bit halves of the four output words, low half first.  Kept
+ * elements are multiplied by 65536 / (65536 - T), the inverse of the exact probability of
+ * keeping; dropped ones become 0 even where they were infinite or NaN.  T = 0 keeps all and
+ * p = 1 drops all.  The mask depends on (seed, offset, row, c) only: a call that has to
+ * reuse a mask (the gradient) passes the same pair, a call that needs a fresh one another
+ * offset.  offset_add, when given, is read on the device at run time and added to offset,
+ * so a captured graph can advance it between replays. */
+typedef struct {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_add; /* [device] or NULL */
+} etpc_dropout_spec;
+
+/* y = dropout(x); x and y may be the same matrix.  The map is diagonal, so its gradient is
+ * the same call on y_bar. */
+etpc_status etpc_dropout(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride,
+                         const etpc_dropout_spec* drop, void* y, int64_t y_stride, hipStream_t stream);
+
+/* y = (x - mean) rstd w + b with mean and rstd = 1 / sqrt(var + eps) of each row (var: mean
+ * squared distance from the mean, taken in a second sum that cannot cancel).  w, b [n_cols]:
+ * NULL = ones, zeros.  mean, rstd [n_rows]: kept for the backward pass, or NULL.
+ * n_cols >= 1; eps >= 0 and finite. */
+etpc_status etpc_layer_norm(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride,
+                            const float* w, const float* b, float eps, void* y, int64_t y_stride, float* mean,
+                            float* rstd, hipStream_t stream);
+/* Workspace of both backward calls below: partial sums of the parameter gradients. */
+etpc_status etpc_layer_norm_workspace_size(int64_t n_rows, int64_t n_cols, size_t* bytes);
+/* Gradients of <y_bar, y>, from the forward pass's x, mean and rstd.  x_bar, w_bar, b_bar:
+ * NULL skips.  Sums over rows have a fixed order. */
+etpc_status etpc_layer_norm_backward(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride,
+                                     const void* y_bar, int64_t y_bar_stride, const float* mean, const float* rstd,
+                                     const float* w, void* x_bar, int64_t x_bar_stride, float* w_bar, float* b_bar,
+                                     void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* The join of a residual block in one pass: h = residual + dropout(x), y = layer_norm(h).
+ * residual, drop: NULL = none.  h: NULL = not kept (the backward pass reads it).  mean, rstd
+ * and y are those of h before it is rounded. */
+etpc_status etpc_dropout_add_layer_norm(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride,
+                                        const void* residual, int64_t residual_stride, const etpc_dropout_spec* drop,
+                                        const float* w, const float* b, float eps, void* y, int64_t y_stride, void* h,
+                                        int64_t h_stride, float* mean, float* rstd, hipStream_t stream);
+/* Gradients of <y_bar, y> + <h_bar, h> (h_bar NULL = zero): residual_bar is the gradient of
+ * h, x_bar its dropout.  Any output may be NULL. */
+etpc_status etpc_dropout_add_layer_norm_backward(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* h,
+                                                 int64_t h_stride, const void* y_bar, int64_t y_bar_stride,
+                                                 const void* h_bar, int64_t h_bar_stride, const float* mean,
+                                                 const float* rstd, const float* w, const etpc_dropout_spec* drop,
+                                                 void* x_bar, int64_t x_bar_stride, void* residual_bar,
+                                                 int64_t residual_bar_stride, float* w_bar, float* b_bar, void* ws,
+                                                 size_t ws_bytes, hipStream_t stream);
+
+/* Irreps features: contiguous fp32 ir_mul rows, x[n_nodes][dim], given by their blocks
+ * irreps[n_blocks] (host; at most 64, mul >= 1, l <= 3, parity +-1).
+ * dim = sum mul (2l+1); channels = sum mul (one gain each); biases = channels of the 0e
+ * blocks.  Output pointers may be NULL. */
+etpc_status etpc_irreps_dims(int32_t n_blocks, const etpc_irrep* irreps, int64_t* dim, int64_t* channels,
+                             int64_t* biases);
+/* Dropout of whole channels: the 2l+1 components of one (node, channel) share their mask,
+ * so the result turns with the input.  Counter (g, node): channel u of block k has
+ * g = u div 8 + the sum of ceil(mul / 8) over the blocks before, field u mod 8.  In place
+ * allowed; its own gradient, like etpc_dropout. */
+etpc_status etpc_irreps_dropout(int32_t n_blocks, const etpc_irrep* irreps, int32_t n_nodes, const float* x,
+                                const etpc_dropout_spec* drop, float* y, hipStream_t stream);
+/* Layer norm that commutes with rotations and reflections, block by block: an l = 0 block as
+ * etpc_layer_norm over its channels (bias for 0e only), an l > 0 block divided by
+ * sqrt(mean of its squares over channels and components + eps).  w [channels], b [biases]:
+ * NULL = ones, zeros.  stats [n_nodes][n_blocks][2] = (mean, rstd), mean 0 for l > 0; NULL =
+ * not kept. */
+etpc_status etpc_irreps_norm(int32_t n_blocks, const etpc_irrep* irreps, int32_t n_nodes, const float* x,
+                             const float* w, const float* b, float eps, float* y, float* stats, hipStream_t stream);
+etpc_status etpc_irreps_norm_workspace_size(int32_t n_blocks, const etpc_irrep* irreps, int32_t n_nodes,
+                                            size_t* bytes);
+etpc_status etpc_irreps_norm_backward(int32_t n_blocks, const etpc_irrep* irreps, int32_t n_nodes, const float* x,
+                                      const float* y_bar, const float* stats, const float* w, float* x_bar,
+                                      float* w_bar, float* b_bar, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Kernel timing (off by default), a measurement aid outside the compute path.  While
  * enabled, every kernel the library enqueues is bracketed by a pair of HIP events recorded
  * on its launch stream, grouped by kind.  etpc_profile_read synchronizes on the recorded
@@ -338,7 +433,8 @@ typedef enum {
   ETPC_KIND_NODE_GEMM = 4,    /* Xt = x W, x_bar = P W^T, W_bar = x^T P */
   ETPC_KIND_AUX = 5,          /* weight re-layout, fixed-order reductions, fills, pos_bar */
   ETPC_KIND_PREP = 6,         /* radius graph and layout conversion */
-  ETPC_KIND_COUNT = 7
+  ETPC_KIND_NODEWISE = 7,     /* layer norm, dropout, irreps norm */
+  ETPC_KIND_COUNT = 8
 } etpc_kind;
 etpc_status etpc_profile_enable(int32_t enable);
 etpc_status etpc_profile_read(int32_t kind, double* total_ms, int64_t* launches);

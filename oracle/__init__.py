@@ -22,6 +22,7 @@ Modules:
   csr     -- receiver and sender CSR views (stable)
   radius  -- radius graph of a point set by brute force (graph preparation)
   layout  -- mul_ir <-> ir_mul feature layouts at the boundary
+  nodewise -- dropout masks, layer norm, residual join, irreps norm
 
 Parity status: every function above is pinned by tests against something other
 than itself (closed forms, scipy/sympy routines, invariants, finite differences,
