@@ -177,8 +177,8 @@ def _ptr(t: Optional[torch.Tensor], dtype=torch.float32) -> Optional[int]:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # torch.cuda.current_stream().cuda_stream without the stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -582,35 +582,33 @@ _ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # etpc_dt
 
 
 def _row_type(x: torch.Tensor) -> int:
-    try:
-        return _ROW_TYPES[x.dtype]
-    except KeyError:
-        raise TypeError(f"rows must be float32, bfloat16 or float16, got {x.dtype}") from None
+    t = _ROW_TYPES.get(x.dtype)
+    if t is None:
+        raise TypeError(f"rows must be float32, bfloat16 or float16, got {x.dtype}")
+    return t
 
 
-def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> Tuple[int, int, int, int]:
-    """(pointer, row stride, rows, columns) of a tensor, which has to match `like`."""
+def _check_device(name: str, t: torch.Tensor):
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if like is None:
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    elif t is not like:
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    shape, strides = t.shape, t.stride()
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _rows(name: str, t: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(pointer, row stride, rows, columns) of a tensor."""
+    shape = t.shape
     if not shape:
         raise ValueError(f"{name} must have at least one axis")
     cols = shape[-1]
-    if t.numel() == 0:
+    if t.is_contiguous():
+        if cols:
+            return t.data_ptr(), cols, t.numel() // cols, cols
         rows = 1
         for n in shape[:-1]:
             rows *= n
         return t.data_ptr(), cols, rows, cols
+    strides = t.stride()
     if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
     rows, stride = 1, cols
@@ -625,6 +623,19 @@ def _rows(name: str, t: torch.Tensor, like: Optional[torch.Tensor] = None) -> Tu
     return t.data_ptr(), stride, rows, cols
 
 
+def _rows_like(name: str, t: Optional[torch.Tensor], like: torch.Tensor) -> Tuple[Optional[int], int]:
+    """(pointer, row stride) of a tensor that has to match `like`; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return _rows(name, t)[:2]
+
+
 def _vector(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[int]:
     """Pointer of a contiguous f32 tensor of n numbers (None passes)."""
     if t is None:
@@ -633,15 +644,23 @@ def _vector(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[in
         raise ValueError(f"{name} must hold {n} numbers, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return _ptr(t, torch.float32)
+    return _ptr(t)
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output, allocated on the call's stream (see _workspace)."""
+def _new(shape, device, stream) -> torch.Tensor:
+    """An f32 output, allocated on the call's stream (see _workspace)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=torch.float32, device=device)
     with torch.cuda.stream(_torch_stream(stream, device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=torch.float32, device=device)
+
+
+def _new_like(x: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous output of x's shape and type, allocated on the call's stream."""
+    if stream is None:
+        return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    with torch.cuda.stream(_torch_stream(stream, x.device)):
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _drop_spec(p: float, seed: int, offset, device) -> etpc_dropout_spec:
@@ -659,37 +678,52 @@ def etpc_dropout(x, p: float, seed: int, offset=0, y=None, stream=None) -> torch
     """y = x with elements dropped with probability p and the rest scaled by 1 / (1 - p), over
     the rows x [..., C]; y may be x.  The gradient is the same call on y_bar."""
     dtype = _row_type(x)
+    _check_device("x", x)
     xp, xs, rows, cols = _rows("x", x)
     if y is None:
-        y = _new(x.shape, x.dtype, x.device, stream)
-    yp, ys, _, _ = _rows("y", y, x)
-    _check(lib.etpc_dropout(rows, cols, dtype, xp, xs, C.byref(_drop_spec(p, seed, offset, x.device)), yp, ys,
-                            _stream(stream)))
+        y = _new_like(x, stream)
+        yp, ys = y.data_ptr(), cols
+    else:
+        yp, ys = _rows_like("y", y, x)
+    st = lib.etpc_dropout(rows, cols, dtype, xp, xs, _drop_spec(p, seed, offset, x.device), yp, ys, _stream(stream))
+    if st:
+        _check(st)
     return y
 
 
-def _norm_forward(x, residual, drop, w, b, eps, y, h, keep_h, stats, mean, rstd, stream):
+def _norm_forward(x, residual, drop, w, b, eps, y, h, join, stats, mean, rstd, stream):
     dtype, dev = _row_type(x), x.device
+    _check_device("x", x)
     xp, xs, rows, cols = _rows("x", x)
-    rp, rs = _rows("residual", residual, x)[:2] if residual is not None else (None, 0)
-    wp, bp = _vector("w", w, cols, dev), _vector("b", b, cols, dev)
     if y is None:
-        y = _new(x.shape, x.dtype, dev, stream)
-    if h is None and keep_h:
-        h = _new(x.shape, x.dtype, dev, stream)
-    if stats:
-        lead = x.shape[:-1]
-        mean = _new(lead, torch.float32, dev, stream) if mean is None else mean
-        rstd = _new(lead, torch.float32, dev, stream) if rstd is None else rstd
-    yp, ys = _rows("y", y, x)[:2]
-    hp, hs = _rows("h", h, x)[:2] if h is not None else (None, 0)
-    mp, sp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev)
-    if keep_h:
+        y = _new_like(x, stream)
+        yp, ys = y.data_ptr(), cols
+    else:
+        yp, ys = _rows_like("y", y, x)
+    if stats and mean is None:
+        mean = _new(rows if x.dim() == 2 else x.shape[:-1], dev, stream)
+        mp = mean.data_ptr()
+    else:
+        mp = _vector("mean", mean, rows, dev)
+    if stats and rstd is None:
+        rstd = _new(rows if x.dim() == 2 else x.shape[:-1], dev, stream)
+        sp = rstd.data_ptr()
+    else:
+        sp = _vector("rstd", rstd, rows, dev)
+    wp, bp = _vector("w", w, cols, dev), _vector("b", b, cols, dev)
+    if join:
+        rp, rs = _rows_like("residual", residual, x)
+        if h is None:
+            h = _new_like(x, stream)
+            hp, hs = h.data_ptr(), cols
+        else:
+            hp, hs = _rows_like("h", h, x)
         st = lib.etpc_dropout_add_layer_norm(rows, cols, dtype, xp, xs, rp, rs, drop, wp, bp, eps, yp, ys, hp, hs, mp,
                                              sp, _stream(stream))
     else:
         st = lib.etpc_layer_norm(rows, cols, dtype, xp, xs, wp, bp, eps, yp, ys, mp, sp, _stream(stream))
-    _check(st)
+    if st:
+        _check(st)
     return y, h, mean, rstd
 
 
@@ -703,52 +737,59 @@ def etpc_layer_norm(x, w=None, b=None, eps: float = 1e-5, y=None, mean=None, rst
 
 def etpc_layer_norm_workspace_size(n_rows: int, n_cols: int) -> int:
     b = C.c_size_t()
-    _check(lib.etpc_layer_norm_workspace_size(n_rows, n_cols, C.byref(b)))
+    _check(lib.etpc_layer_norm_workspace_size(n_rows, n_cols, b))
     return b.value
 
 
 def _scratch(ws, nbytes: int, device, stream):
     """(pointer, bytes, tensor to keep alive) of a caller's workspace or a new one."""
     if ws is None:
-        ws, _ = _workspace(nbytes, device, stream) if stream is not None or nbytes <= 0 else (
-            torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes)
-        return (None, 0, None) if ws is None else (ws.data_ptr(), nbytes, ws)
+        if nbytes <= 0:
+            return None, 0, None
+        ws = _new((nbytes + 3) // 4, device, stream)
+        return ws.data_ptr(), nbytes, ws
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"the workspace must be contiguous and on {device}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
-def _norm_backward(h, y_bar, mean, rstd, w, h_bar, drop, want, outs, ws, stream):
-    dtype, dev = _row_type(h), h.device
-    hp, hs, rows, cols = _rows("x" if drop is False else "h", h)
-    yp, ys = _rows("y_bar", y_bar, h)[:2]
-    bp, bs = _rows("h_bar", h_bar, h)[:2] if h_bar is not None else (None, 0)
-    mp, sp, wp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev), _vector("w", w, cols, dev)
-    if outs is None:
-        outs = tuple(None if name not in want else _new(h.shape, h.dtype, dev, stream) if name in ("x", "residual")
-                     else _new((cols,), torch.float32, dev, stream) for name in ("x", "residual", "w", "b"))
-    x_bar, r_bar, w_bar, b_bar = outs
-    xbp, xbs = _rows("x_bar", x_bar, h)[:2] if x_bar is not None else (None, 0)
-    rbp, rbs = _rows("residual_bar", r_bar, h)[:2] if r_bar is not None else (None, 0)
-    wbp, bbp = _vector("w_bar", w_bar, cols, dev), _vector("b_bar", b_bar, cols, dev)
-    need = etpc_layer_norm_workspace_size(rows, cols) if wbp is not None or bbp is not None else 0
-    wsp, wsn, _keep = _scratch(ws, need, dev, stream)
-    if drop is False:
-        st = lib.etpc_layer_norm_backward(rows, cols, dtype, hp, hs, yp, ys, mp, sp, wp, xbp, xbs, wbp, bbp, wsp, wsn,
-                                          _stream(stream))
-    else:
-        st = lib.etpc_dropout_add_layer_norm_backward(rows, cols, dtype, hp, hs, yp, ys, bp, bs, mp, sp, wp, drop, xbp,
-                                                      xbs, rbp, rbs, wbp, bbp, wsp, wsn, _stream(stream))
-    _check(st)
-    return outs
+def _bar_like(name, want, key, outs, i, like, cols, stream):
+    """(tensor, pointer, row stride) of a gradient shaped like the features."""
+    if outs is not None:
+        return (outs[i], *_rows_like(name, outs[i], like))
+    if key not in want:
+        return None, None, 0
+    t = _new_like(like, stream)
+    return t, t.data_ptr(), cols
+
+
+def _bar_vector(name, want, key, outs, i, n, dev, stream):
+    """(tensor, pointer) of a parameter's gradient."""
+    if outs is not None:
+        return outs[i], _vector(name, outs[i], n, dev)
+    if key not in want:
+        return None, None
+    t = _new(n, dev, stream)
+    return t, t.data_ptr()
 
 
 def etpc_layer_norm_backward(x, y_bar, mean, rstd, w=None, want=("x", "w", "b"), outs=None, ws=None, stream=None):
     """(x_bar, w_bar, b_bar) of <y_bar, y>; None for what `want` leaves out.  outs: three
     caller-given tensors (or None to skip one)."""
-    if outs is not None:
-        outs = (outs[0], None, outs[1], outs[2])
-    x_bar, _, w_bar, b_bar = _norm_backward(x, y_bar, mean, rstd, w, None, False, want, outs, ws, stream)
+    dtype, dev = _row_type(x), x.device
+    _check_device("x", x)
+    xp, xs, rows, cols = _rows("x", x)
+    yp, ys = _rows_like("y_bar", y_bar, x)
+    mp, sp, wp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev), _vector("w", w, cols, dev)
+    x_bar, xbp, xbs = _bar_like("x_bar", want, "x", outs, 0, x, cols, stream)
+    w_bar, wbp = _bar_vector("w_bar", want, "w", outs, 1, cols, dev, stream)
+    b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 2, cols, dev, stream)
+    need = etpc_layer_norm_workspace_size(rows, cols) if wbp is not None or bbp is not None else 0
+    wsp, wsn, _keep = _scratch(ws, need, dev, stream)
+    st = lib.etpc_layer_norm_backward(rows, cols, dtype, xp, xs, yp, ys, mp, sp, wp, xbp, xbs, wbp, bbp, wsp, wsn,
+                                      _stream(stream))
+    if st:
+        _check(st)
     return x_bar, w_bar, b_bar
 
 
@@ -756,7 +797,7 @@ def etpc_dropout_add_layer_norm(x, residual, w=None, b=None, p: float = 0.0, see
                                 eps: float = 1e-5, y=None, h=None, mean=None, rstd=None, stats: bool = True,
                                 stream=None):
     """(y, h, mean, rstd): h = residual + dropout(x) (residual may be None), y = layer_norm(h)."""
-    drop = C.byref(_drop_spec(p, seed, offset, x.device))
+    drop = _drop_spec(p, seed, offset, x.device)
     return _norm_forward(x, residual, drop, w, b, eps, y, h, True, stats, mean, rstd, stream)
 
 
@@ -764,8 +805,24 @@ def etpc_dropout_add_layer_norm_backward(h, y_bar, mean, rstd, w=None, h_bar=Non
                                          offset=0, want=("x", "residual", "w", "b"), outs=None, ws=None, stream=None):
     """(x_bar, residual_bar, w_bar, b_bar) of <y_bar, y> + <h_bar, h>; None for what `want`
     leaves out.  p, seed and offset as in the forward call."""
-    drop = C.byref(_drop_spec(p, seed, offset, h.device))
-    return _norm_backward(h, y_bar, mean, rstd, w, h_bar, drop, want, outs, ws, stream)
+    dtype, dev = _row_type(h), h.device
+    _check_device("h", h)
+    hp, hs, rows, cols = _rows("h", h)
+    yp, ys = _rows_like("y_bar", y_bar, h)
+    bp, bs = _rows_like("h_bar", h_bar, h)
+    mp, sp, wp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev), _vector("w", w, cols, dev)
+    x_bar, xbp, xbs = _bar_like("x_bar", want, "x", outs, 0, h, cols, stream)
+    r_bar, rbp, rbs = _bar_like("residual_bar", want, "residual", outs, 1, h, cols, stream)
+    w_bar, wbp = _bar_vector("w_bar", want, "w", outs, 2, cols, dev, stream)
+    b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 3, cols, dev, stream)
+    need = etpc_layer_norm_workspace_size(rows, cols) if wbp is not None or bbp is not None else 0
+    wsp, wsn, _keep = _scratch(ws, need, dev, stream)
+    st = lib.etpc_dropout_add_layer_norm_backward(rows, cols, dtype, hp, hs, yp, ys, bp, bs, mp, sp, wp,
+                                                  _drop_spec(p, seed, offset, dev), xbp, xbs, rbp, rbs, wbp, bbp, wsp,
+                                                  wsn, _stream(stream))
+    if st:
+        _check(st)
+    return x_bar, r_bar, w_bar, b_bar
 
 
 class _Irreps:
@@ -794,13 +851,17 @@ def etpc_irreps_dims(irreps) -> Dict[str, int]:
     return dict(dim=ir.dim, channels=ir.channels, biases=ir.biases)
 
 
-def _features(name, t, ir: _Irreps, like=None) -> int:
-    if t.dim() != 2 or t.shape[1] != ir.dim:
-        raise ValueError(f"{name} must have shape (n_nodes, {ir.dim}), got {tuple(t.shape)}")
-    if like is not None:
-        _check_shape(name, t, tuple(like.shape), like.device)
-    elif t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+def _features(name, t, ir: _Irreps, like=None) -> Optional[int]:
+    """Pointer of contiguous f32 feature rows (None passes where `like` is given)."""
+    if t is None and like is not None:
+        return None
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != ir.dim:
+        raise ValueError(f"{name} must have shape (n_nodes, {ir.dim}), got {tuple(shape)}")
+    if like is None:
+        _check_device(name, t)
+    elif shape != like.shape or t.device != like.device:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} on {like.device}, got {tuple(shape)} on {t.device}")
     return _ptr(t)
 
 
@@ -810,9 +871,13 @@ def etpc_irreps_dropout(irreps, x, p: float, seed: int, offset=0, y=None, stream
     ir = _irreps(irreps)
     xp = _features("x", x, ir)
     if y is None:
-        y = _new(x.shape, x.dtype, x.device, stream)
-    _check(lib.etpc_irreps_dropout(ir.n, ir.c, x.shape[0], xp, C.byref(_drop_spec(p, seed, offset, x.device)),
-                                   _features("y", y, ir, x), _stream(stream)))
+        y = _new_like(x, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _features("y", y, ir, x)
+    st = lib.etpc_irreps_dropout(ir.n, ir.c, x.shape[0], xp, _drop_spec(p, seed, offset, x.device), yp, _stream(stream))
+    if st:
+        _check(st)
     return y
 
 
@@ -825,18 +890,25 @@ def etpc_irreps_norm(irreps, x, w=None, b=None, eps: float = 1e-5, y=None, stats
     xp = _features("x", x, ir)
     n = x.shape[0]
     if y is None:
-        y = _new(x.shape, x.dtype, dev, stream)
+        y = _new_like(x, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _features("y", y, ir, x)
     if stats is None and keep_stats:
-        stats = _new((n, ir.n, 2), torch.float32, dev, stream)
-    _check(lib.etpc_irreps_norm(ir.n, ir.c, n, xp, _vector("w", w, ir.channels, dev), _vector("b", b, ir.biases, dev),
-                                eps, _features("y", y, ir, x), _vector("stats", stats, 2 * n * ir.n, dev),
-                                _stream(stream)))
+        stats = _new((n, ir.n, 2), dev, stream)
+        sp = stats.data_ptr()
+    else:
+        sp = _vector("stats", stats, 2 * n * ir.n, dev)
+    st = lib.etpc_irreps_norm(ir.n, ir.c, n, xp, _vector("w", w, ir.channels, dev), _vector("b", b, ir.biases, dev), eps,
+                              yp, sp, _stream(stream))
+    if st:
+        _check(st)
     return y, stats
 
 
 def etpc_irreps_norm_workspace_size(irreps, n_nodes: int) -> int:
     ir, b = _irreps(irreps), C.c_size_t()
-    _check(lib.etpc_irreps_norm_workspace_size(ir.n, ir.c, n_nodes, C.byref(b)))
+    _check(lib.etpc_irreps_norm_workspace_size(ir.n, ir.c, n_nodes, b))
     return b.value
 
 
@@ -845,15 +917,19 @@ def etpc_irreps_norm_backward(irreps, x, y_bar, stats, w=None, want=("x", "w", "
     ir, dev = _irreps(irreps), x.device
     xp, yp = _features("x", x, ir), _features("y_bar", y_bar, ir, x)
     n = x.shape[0]
-    if outs is None:
-        outs = (_new(x.shape, x.dtype, dev, stream) if "x" in want else None,
-                _new((ir.channels,), torch.float32, dev, stream) if "w" in want else None,
-                _new((ir.biases,), torch.float32, dev, stream) if "b" in want else None)
-    x_bar, w_bar, b_bar = outs
-    xbp = _features("x_bar", x_bar, ir, x) if x_bar is not None else None
-    wbp, bbp = _vector("w_bar", w_bar, ir.channels, dev), _vector("b_bar", b_bar, ir.biases, dev)
-    need = etpc_irreps_norm_workspace_size(irreps, n) if w_bar is not None or b_bar is not None else 0
+    if outs is not None:
+        x_bar, xbp = outs[0], _features("x_bar", outs[0], ir, x)
+    elif "x" in want:
+        x_bar = _new_like(x, stream)
+        xbp = x_bar.data_ptr()
+    else:
+        x_bar = xbp = None
+    w_bar, wbp = _bar_vector("w_bar", want, "w", outs, 1, ir.channels, dev, stream)
+    b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 2, ir.biases, dev, stream)
+    need = etpc_irreps_norm_workspace_size(irreps, n) if wbp is not None or bbp is not None else 0
     wsp, wsn, _keep = _scratch(ws, need, dev, stream)
-    _check(lib.etpc_irreps_norm_backward(ir.n, ir.c, n, xp, yp, _vector("stats", stats, 2 * n * ir.n, dev),
-                                         _vector("w", w, ir.channels, dev), xbp, wbp, bbp, wsp, wsn, _stream(stream)))
-    return outs
+    st = lib.etpc_irreps_norm_backward(ir.n, ir.c, n, xp, yp, _vector("stats", stats, 2 * n * ir.n, dev),
+                                       _vector("w", w, ir.channels, dev), xbp, wbp, bbp, wsp, wsn, _stream(stream))
+    if st:
+        _check(st)
+    return x_bar, w_bar, b_bar

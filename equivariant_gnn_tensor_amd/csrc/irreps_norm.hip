@@ -11,8 +11,11 @@
 // commutes with it; a mean over channels may only be taken out, and a constant added, where
 // the numbers are invariant.
 //
-// Memory bound, like the layer norm of rows.  The grid's y axis is the block, so every wave
-// works on segments of one length; a group of lanes owns a segment in registers.
+// Memory bound: each operand is read once and each result written once.  A group of lanes
+// owns a segment: lane j holds channels 4 j .. 4 j + 3 with all their components, so a
+// gain, a bias and the gradients' sums are four registers a lane whatever the degree, and
+// 64 channels fill 16 lanes exactly at every degree.  Workgroups are dealt to the blocks in
+// proportion to the blocks' widths, so that all have about the same bytes to move.
 #include <algorithm>
 
 #include "nodewise.hpp"
@@ -23,19 +26,19 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kVecs = 8;                  // vectors of four numbers a lane holds
-constexpr int kRegNumbers = 64 * 4 * kVecs;
+constexpr int kRegMul = 512;   // most channels a wave keeps in registers (two vectors a lane)
 
-// Lanes of a segment: a power of two up to the wave, by the number of four-vectors.
-__device__ inline int lanes_of(int vecs) {
-  int g = 4;
-  while (g < vecs && g < 64) g *= 2;
+// Lanes of a segment: a power of two that covers its channels by fours, at most a wave.
+__host__ __device__ inline int lanes_of(int mul) {
+  int g = 1;
+  while (4 * g < mul && g < 64) g *= 2;
   return g;
 }
 
-// The sum over aligned groups of g lanes (4..64), g uniform in the workgroup.
+// The sum over aligned groups of g lanes, g uniform in the workgroup.
 __device__ inline float sum_lanes(float v, int g) {
-  v = lane_sum<4>(v);
+  if (g >= 2) v += dpp_f<0xB1>(v);
+  if (g >= 4) v += dpp_f<0x4E>(v);
   if (g >= 8) v += dpp_f<0x141>(v);
   if (g >= 16) v += dpp_f<0x140>(v);
   if (g >= 32) v = add_lane16(v);
@@ -43,283 +46,429 @@ __device__ inline float sum_lanes(float v, int g) {
   return v;
 }
 
-__device__ inline void load4(const float* __restrict__ p, int e, int n, float (&v)[4]) {
-  if (e + 4 <= n) {
-    __builtin_memcpy(v, p + e, 16);
+__device__ inline void load4(const float* __restrict__ p, int c, int n, float (&v)[4]) {
+  if (c + 4 <= n) {
+    __builtin_memcpy(v, p + c, 16);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = e + k < n ? p[e + k] : 0.f;
+    for (int k = 0; k < 4; ++k) v[k] = c + k < n ? p[c + k] : 0.f;
   }
 }
-__device__ inline void store4(float* __restrict__ p, int e, int n, const float (&v)[4]) {
-  if (e + 4 <= n) {
-    __builtin_memcpy(p + e, v, 16);
+__device__ inline void store4(float* __restrict__ p, int c, int n, const float (&v)[4]) {
+  if (c + 4 <= n) {
+    __builtin_memcpy(p + c, v, 16);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (e + k < n) p[e + k] = v[k];
+      if (c + k < n) p[c + k] = v[k];
   }
 }
-
-// The gains (biases) of four adjacent numbers of a segment, channel of number e = e mod C.
-__device__ inline void channel4(const float* __restrict__ p, int e, int n, int mul, float missing, float (&v)[4]) {
-  int c = e % mul;
+__device__ inline void load4_or(const float* __restrict__ p, int c, int n, float missing, float (&v)[4]) {
+  if (p != nullptr) {
+    load4(p, c, n, v);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[k] = p != nullptr && e + k < n ? p[c] : missing;
-    c = c + 1 == mul ? 0 : c + 1;
+    for (int k = 0; k < 4; ++k) v[k] = missing;
   }
 }
 
-__global__ __launch_bounds__(kThreads) void irreps_norm_fwd_kernel(const IrrepTable t, const float* x, const float* w,
-                                                                   const float* b, float eps, float* y, float* stats,
-                                                                   int32_t rows) {
-  const IrrepBlock k = t.blk[blockIdx.y];
-  const int n = (2 * k.l + 1) * k.mul, vecs = (n + 3) / 4;
-  const int G = lanes_of(vecs), lane = threadIdx.x & (G - 1), per = kThreads / G;
-  const float inv_n = 1.f / static_cast<float>(n);
-  const float* gain = w != nullptr ? w + k.ch : nullptr;
-  const float* bias = b != nullptr && k.bias >= 0 ? b + k.bias : nullptr;
-  if (n > kRegNumbers) {   // longer segments are read once for each sum and once for y
-    const int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / 64;
-    for (int64_t row = wave; row < rows; row += static_cast<int64_t>(gridDim.x) * kWaves) {
-      const float* xr = x + row * t.dim + k.off;
+struct FwdArgs {
+  const float* x;
+  const float* w;
+  const float* b;
+  float* y;
+  float* stats;
+  float eps;
+  int32_t rows;
+};
+
+struct BwdArgs {
+  const float* x;
+  const float* y_bar;
+  const float* stats;
+  const float* w;
+  float* x_bar;
+  float* w_bar;
+  float* b_bar;
+  float* part;
+  int32_t rows;
+  bool whole;   // one workgroup a block: sums go straight to w_bar and b_bar
+};
+
+// Which block a workgroup belongs to.
+__device__ inline int block_of(const IrrepTable& t, int wg) {
+  int k = 0;
+  while (k + 1 < t.n && wg >= t.blk[k + 1].wg) ++k;
+  return k;
+}
+__device__ inline int groups_of(const IrrepTable& t, int k) { return (k + 1 < t.n ? t.blk[k + 1].wg : t.groups) - t.blk[k].wg; }
+
+// D = 2l+1 components, I vectors of four channels a lane, R nodes in flight a group.
+template <int D, int I, int R>
+__device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
+  const int mul = t.blk[k].mul, off = t.blk[k].off;
+  const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), per = kThreads / G;
+  const float inv_n = 1.f / static_cast<float>(D * mul);
+  float w[I][4], b[I][4];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    load4_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
+    load4_or(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, 4 * (lane + i * G), mul, 0.f, b[i]);
+  }
+  const int64_t step = static_cast<int64_t>(parts) * per;
+  for (int64_t first = static_cast<int64_t>(p) * per + threadIdx.x / G; first < a.rows; first += R * step) {
+    float v[R][D][I][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (first + r * step < a.rows)
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+            load4(a.x + (first + r * step) * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = first + r * step;
+      if (row >= a.rows) break;
       float s = 0.f, mean = 0.f;
-      if (k.l == 0) {
-        for (int e = 4 * lane; e < n; e += 256) {
-          float v[4];
-          load4(xr, e, n, v);
-          s += (v[0] + v[1]) + (v[2] + v[3]);
-        }
-        mean = sum_lanes(s, 64) / static_cast<float>(n);   // exact for a constant row
+      if (D == 1) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) s += (v[r][0][i][0] + v[r][0][i][1]) + (v[r][0][i][2] + v[r][0][i][3]);
+        mean = sum_lanes(s, G) / static_cast<float>(mul);   // exact for a constant row
         s = 0.f;
       }
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (D == 1) {
+              v[r][d][i][j] -= mean;
+              if (4 * (lane + i * G) + j < mul) s = fmaf(v[r][d][i][j], v[r][d][i][j], s);
+            } else {
+              s = fmaf(v[r][d][i][j], v[r][d][i][j], s);   // channels past the last hold 0
+            }
+      const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, G), inv_n, a.eps));
+      if (lane == 0 && a.stats != nullptr) {
+        a.stats[2 * (row * t.n + k)] = mean;
+        a.stats[2 * (row * t.n + k) + 1] = rstd;
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          float o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = fmaf(v[r][d][i][j] * rstd, w[i][j], b[i][j]);
+          store4(a.y + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
+        }
+    }
+  }
+}
+
+// Segments of more channels: a wave reads its segment once for each sum and once for y.
+__device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
+  const int mul = t.blk[k].mul, n = (2 * t.blk[k].l + 1) * mul, lane = threadIdx.x & 63;
+  const float inv_n = 1.f / static_cast<float>(n);
+  const float* w = a.w != nullptr ? a.w + t.blk[k].ch : nullptr;
+  const float* b = a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr;
+  for (int64_t row = static_cast<int64_t>(p) * kWaves + threadIdx.x / 64; row < a.rows;
+       row += static_cast<int64_t>(parts) * kWaves) {
+    const float* x = a.x + row * t.dim + t.blk[k].off;
+    float s = 0.f, mean = 0.f;
+    if (n == mul) {
       for (int e = 4 * lane; e < n; e += 256) {
         float v[4];
-        load4(xr, e, n, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (e + j < n) s = fmaf(v[j] - mean, v[j] - mean, s);
+        load4(x, e, n, v);
+        s += (v[0] + v[1]) + (v[2] + v[3]);
       }
-      const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, 64), inv_n, eps));
-      if (lane == 0 && stats != nullptr) {
-        stats[2 * (row * t.n + blockIdx.y)] = mean;
-        stats[2 * (row * t.n + blockIdx.y) + 1] = rstd;
-      }
-      for (int e = 4 * lane; e < n; e += 256) {
-        float v[4], g[4], c[4];
-        load4(xr, e, n, v);
-        channel4(gain, e, n, k.mul, 1.f, g);
-        channel4(bias, e, n, k.mul, 0.f, c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], c[j]);
-        store4(y + row * t.dim + k.off, e, n, v);
-      }
-    }
-    return;
-  }
-  float g[kVecs][4], c[kVecs][4];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    if (i * G < vecs) {
-      channel4(gain, 4 * (lane + i * G), n, k.mul, 1.f, g[i]);
-      channel4(bias, 4 * (lane + i * G), n, k.mul, 0.f, c[i]);
-    }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / G; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * per) {
-    const float* xr = x + row * t.dim + k.off;
-    float v[kVecs][4], s = 0.f, mean = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (i * G < vecs) load4(xr, 4 * (lane + i * G), n, v[i]);
-    if (k.l == 0) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (i * G < vecs) s += (v[i][0] + v[i][1]) + (v[i][2] + v[i][3]);
-      mean = sum_lanes(s, G) / static_cast<float>(n);
+      mean = sum_lanes(s, 64) / static_cast<float>(n);
       s = 0.f;
     }
+    for (int e = 4 * lane; e < n; e += 256) {
+      float v[4];
+      load4(x, e, n, v);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (i * G < vecs)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][j] -= mean;
-          if (4 * (lane + i * G) + j < n) s = fmaf(v[i][j], v[i][j], s);
-        }
-    const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, G), inv_n, eps));
-    if (lane == 0 && stats != nullptr) {
-      stats[2 * (row * t.n + blockIdx.y)] = mean;
-      stats[2 * (row * t.n + blockIdx.y) + 1] = rstd;
+      for (int j = 0; j < 4; ++j)
+        if (e + j < n) s = fmaf(v[j] - mean, v[j] - mean, s);
     }
+    const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, 64), inv_n, a.eps));
+    if (lane == 0 && a.stats != nullptr) {
+      a.stats[2 * (row * t.n + k)] = mean;
+      a.stats[2 * (row * t.n + k) + 1] = rstd;
+    }
+    for (int d = 0; d * mul < n; ++d)
+      for (int c = 4 * lane; c < mul; c += 256) {
+        float v[4], g[4], h[4];
+        load4(x + d * mul, c, mul, v);
+        load4_or(w, c, mul, 1.f, g);
+        load4_or(b, c, mul, 0.f, h);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (i * G < vecs) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[i][j], c[i][j]);
-        store4(y + row * t.dim + k.off, 4 * (lane + i * G), n, v[i]);
+        for (int j = 0; j < 4; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], h[j]);
+        store4(a.y + row * t.dim + t.blk[k].off + d * mul, c, mul, v);
       }
   }
 }
 
-// Column sums stay in registers while a group walks its nodes; at the end each wave in turn
-// adds its numbers to an LDS copy of the segment, and thread c sums the 2l+1 components of
-// channel c: every order is fixed.
-__global__ __launch_bounds__(kThreads) void irreps_norm_bwd_kernel(const IrrepTable t, const float* x,
-                                                                   const float* y_bar, const float* stats,
-                                                                   const float* w, float* x_bar, float* part,
-                                                                   float* w_bar, float* b_bar, int32_t rows) {
-  __shared__ float lds[2][kRegNumbers];
-  const IrrepBlock k = t.blk[blockIdx.y];
-  const int n = (2 * k.l + 1) * k.mul, vecs = (n + 3) / 4;
-  const int G = lanes_of(vecs), lane = threadIdx.x & (G - 1), per = kThreads / G;
-  const float inv_n = 1.f / static_cast<float>(n);
-  const float* gain = w != nullptr ? w + k.ch : nullptr;
-  const bool whole = gridDim.x == 1, sums = w_bar != nullptr || b_bar != nullptr;
-  float* wo = whole ? w_bar : part + static_cast<int64_t>(blockIdx.x) * (t.channels + t.biases);
-  float* bo = whole ? b_bar : wo + t.channels;
-  if (n > kRegNumbers) {   // longer segments are read twice, and once more for the channel sums
-    const int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / 64;
-    for (int64_t row = wave; row < rows && x_bar != nullptr; row += static_cast<int64_t>(gridDim.x) * kWaves) {
-      const float* xr = x + row * t.dim + k.off;
-      const float* yr = y_bar + row * t.dim + k.off;
-      const float mean = stats[2 * (row * t.n + blockIdx.y)], rstd = stats[2 * (row * t.n + blockIdx.y) + 1];
+template <int I>
+__global__ __launch_bounds__(kThreads) void irreps_norm_fwd_kernel(const IrrepTable t, const FwdArgs a) {
+  const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
+  if (I == 2 && t.blk[k].mul > kRegMul) return fwd_long(t, k, p, parts, a);
+  if (l == 0) fwd_block<1, I, 4>(t, k, p, parts, a);
+  else if (l == 1) fwd_block<3, I, 2>(t, k, p, parts, a);
+  else if (l == 2) fwd_block<5, I, 1>(t, k, p, parts, a);
+  else fwd_block<7, I, 1>(t, k, p, parts, a);
+}
+
+// Where a workgroup of the backward pass leaves its sums: gains first, then biases.
+__device__ inline void sum_outputs(const IrrepTable& t, int k, int p, const BwdArgs& a, float** wo, float** bo) {
+  const IrrepBlock& q = t.blk[k];
+  if (a.whole) {
+    *wo = a.w_bar != nullptr ? a.w_bar + q.ch : nullptr;
+    *bo = a.b_bar != nullptr && q.bias >= 0 ? a.b_bar + q.bias : nullptr;
+  } else {
+    *wo = a.part + q.part + static_cast<int64_t>(p) * (q.bias >= 0 ? 2 * q.mul : q.mul);
+    *bo = q.bias >= 0 ? *wo + q.mul : nullptr;
+  }
+}
+
+// A group keeps its channels' sums of y_bar xh and y_bar in registers while it walks its
+// nodes; lanes, then waves are added at the end in a fixed order.
+template <int D, int I, int R>
+__device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a, float* lds) {
+  const int mul = t.blk[k].mul, off = t.blk[k].off;
+  const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), per = kThreads / G;
+  const float inv_n = 1.f / static_cast<float>(D * mul);
+  float w[I][4], dw[I][4] = {}, db[I][4] = {};
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+    load4_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
+  const int64_t step = static_cast<int64_t>(parts) * per;
+  for (int64_t first = static_cast<int64_t>(p) * per + threadIdx.x / G; first < a.rows; first += R * step) {
+    float v[R][D][I][4], g[R][D][I][4], mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = first + r * step;
+      if (row < a.rows) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+          for (int i = 0; i < I; ++i) {
+            load4(a.x + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
+            load4(a.y_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, g[r][d][i]);
+          }
+        mean[r] = D == 1 ? a.stats[2 * (row * t.n + k)] : 0.f;
+        rstd[r] = a.stats[2 * (row * t.n + k) + 1];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = first + r * step;
+      if (row >= a.rows) break;
       float s0 = 0.f, s1 = 0.f;
-      for (int e = 4 * lane; e < n; e += 256) {
-        float v[4], d[4], g[4];
-        load4(xr, e, n, v);
-        load4(yr, e, n, d);
-        channel4(gain, e, n, k.mul, 1.f, g);
+      // channels past the last hold y_bar = 0 and add nothing
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s0 = fmaf(d[j], g[j], s0);
-          s1 = fmaf(d[j] * g[j], (v[j] - mean) * rstd, s1);
-        }
-      }
-      const float m0 = k.l == 0 ? sum_lanes(s0, 64) * inv_n : 0.f, m1 = sum_lanes(s1, 64) * inv_n;
-      for (int e = 4 * lane; e < n; e += 256) {
-        float v[4], d[4], g[4];
-        load4(xr, e, n, v);
-        load4(yr, e, n, d);
-        channel4(gain, e, n, k.mul, 1.f, g);
+      for (int d = 0; d < D; ++d)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = rstd * (fmaf(d[j], g[j], -m0) - (v[j] - mean) * rstd * m1);
-        store4(x_bar + row * t.dim + k.off, e, n, v);
-      }
-    }
-    if (!sums) return;
-    for (int c = threadIdx.x; c < k.mul; c += kThreads) {
-      float dw = 0.f, db = 0.f;
-      for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const float mean = stats[2 * (row * t.n + blockIdx.y)], rstd = stats[2 * (row * t.n + blockIdx.y) + 1];
-        for (int e = c; e < n; e += k.mul) {
-          const float d = y_bar[row * t.dim + k.off + e];
-          dw = fmaf(d, (x[row * t.dim + k.off + e] - mean) * rstd, dw);
-          db += d;
-        }
-      }
-      if (wo != nullptr) wo[k.ch + c] = dw;
-      if (bo != nullptr && k.bias >= 0) bo[k.bias + c] = db;
-    }
-    return;
-  }
-  float g[kVecs][4], dw[kVecs][4], db[kVecs][4];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    if (i * G < vecs) channel4(gain, 4 * (lane + i * G), n, k.mul, 1.f, g[i]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = 0.f;
-  }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / G; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * per) {
-    const float* xr = x + row * t.dim + k.off;
-    const float* yr = y_bar + row * t.dim + k.off;
-    float v[kVecs][4], d[kVecs][4], s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (i * G < vecs) {
-        load4(xr, 4 * (lane + i * G), n, v[i]);
-        load4(yr, 4 * (lane + i * G), n, d[i]);
-      }
-    const float mean = stats[2 * (row * t.n + blockIdx.y)], rstd = stats[2 * (row * t.n + blockIdx.y) + 1];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (i * G < vecs)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][j] = (v[i][j] - mean) * rstd;
-          dw[i][j] = fmaf(d[i][j], v[i][j], dw[i][j]);
-          db[i][j] += d[i][j];
-          d[i][j] *= g[i][j];
-          s0 += d[i][j];
-          s1 = fmaf(d[i][j], v[i][j], s1);
-        }
-    if (x_bar == nullptr) continue;
-    const float m0 = k.l == 0 ? sum_lanes(s0, G) * inv_n : 0.f, m1 = sum_lanes(s1, G) * inv_n;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (i * G < vecs) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = rstd * (d[i][j] - fmaf(v[i][j], m1, m0));
-        store4(x_bar + row * t.dim + k.off, 4 * (lane + i * G), n, v[i]);
-      }
-  }
-  if (!sums) return;
-  // the groups of a wave first: lane sums over equal positions
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    if (i * G < vecs)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        for (int o = G; o < 64; o *= 2) {
-          dw[i][j] += __shfl_xor(dw[i][j], o);
-          db[i][j] += __shfl_xor(db[i][j], o);
-        }
-  for (int q = 0; q < kWaves; ++q) {
-    if (static_cast<int>(threadIdx.x / 64) == q && (threadIdx.x & 63) < static_cast<unsigned>(G)) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (i * G < vecs)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int e = 4 * (lane + i * G) + j;
-            if (e < n) {
-              lds[0][e] = q == 0 ? dw[i][j] : lds[0][e] + dw[i][j];
-              lds[1][e] = q == 0 ? db[i][j] : lds[1][e] + db[i][j];
-            }
+            float& x = v[r][d][i][j];
+            float& y = g[r][d][i][j];
+            x = (x - mean[r]) * rstd[r];
+            dw[i][j] = fmaf(y, x, dw[i][j]);
+            if (D == 1) db[i][j] += y;
+            y *= w[i][j];
+            if (D == 1) s0 += y;
+            s1 = fmaf(y, x, s1);
           }
+      if (a.x_bar == nullptr) continue;
+      const float m0 = D == 1 ? sum_lanes(s0, G) * inv_n : 0.f, m1 = sum_lanes(s1, G) * inv_n;
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          float o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = rstd[r] * (g[r][d][i][j] - fmaf(v[r][d][i][j], m1, m0));
+          store4(a.x_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
+        }
     }
-    __syncthreads();
   }
-  for (int c = threadIdx.x; c < k.mul; c += kThreads) {
-    float sw = 0.f, sb = 0.f;
-    for (int e = c; e < n; e += k.mul) {
-      sw += lds[0][e];
-      sb += lds[1][e];
+  if (a.w_bar == nullptr && a.b_bar == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      for (int o = G; o < 64; o *= 2) {
+        dw[i][j] += __shfl_xor(dw[i][j], o);
+        if (D == 1) db[i][j] += __shfl_xor(db[i][j], o);
+      }
+      const int c = 4 * (lane + i * G) + j, wave = threadIdx.x / 64;
+      if ((threadIdx.x & 63) < static_cast<unsigned>(G) && c < mul) {
+        lds[wave * kRegMul + c] = dw[i][j];
+        if (D == 1) lds[(kWaves + wave) * kRegMul + c] = db[i][j];
+      }
     }
-    if (wo != nullptr) wo[k.ch + c] = sw;
-    if (bo != nullptr && k.bias >= 0) bo[k.bias + c] = sb;
+  __syncthreads();
+  float *wo, *bo;
+  sum_outputs(t, k, p, a, &wo, &bo);
+  for (int c = threadIdx.x; c < mul; c += kThreads) {
+    float sw = lds[c], sb = 0.f;
+#pragma unroll
+    for (int q = 1; q < kWaves; ++q) sw += lds[q * kRegMul + c];
+    if (wo != nullptr) wo[c] = sw;
+    if (D == 1 && bo != nullptr) {
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) sb += lds[(kWaves + q) * kRegMul + c];
+      bo[c] = sb;
+    }
   }
+}
+
+__device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a) {
+  const int mul = t.blk[k].mul, n = (2 * t.blk[k].l + 1) * mul, lane = threadIdx.x & 63;
+  const float inv_n = 1.f / static_cast<float>(n);
+  const float* w = a.w != nullptr ? a.w + t.blk[k].ch : nullptr;
+  for (int64_t row = static_cast<int64_t>(p) * kWaves + threadIdx.x / 64; row < a.rows && a.x_bar != nullptr;
+       row += static_cast<int64_t>(parts) * kWaves) {
+    const int64_t at = row * t.dim + t.blk[k].off;
+    const float mean = a.stats[2 * (row * t.n + k)], rstd = a.stats[2 * (row * t.n + k) + 1];
+    float s0 = 0.f, s1 = 0.f;
+    for (int d = 0; d * mul < n; ++d)
+      for (int c = 4 * lane; c < mul; c += 256) {
+        float v[4], y[4], g[4];
+        load4(a.x + at + d * mul, c, mul, v);
+        load4(a.y_bar + at + d * mul, c, mul, y);
+        load4_or(w, c, mul, 1.f, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s0 = fmaf(y[j], g[j], s0);
+          s1 = fmaf(y[j] * g[j], (v[j] - mean) * rstd, s1);
+        }
+      }
+    const float m0 = n == mul ? sum_lanes(s0, 64) * inv_n : 0.f, m1 = sum_lanes(s1, 64) * inv_n;
+    for (int d = 0; d * mul < n; ++d)
+      for (int c = 4 * lane; c < mul; c += 256) {
+        float v[4], y[4], g[4];
+        load4(a.x + at + d * mul, c, mul, v);
+        load4(a.y_bar + at + d * mul, c, mul, y);
+        load4_or(w, c, mul, 1.f, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = rstd * (fmaf(y[j], g[j], -m0) - (v[j] - mean) * rstd * m1);
+        store4(a.x_bar + at + d * mul, c, mul, v);
+      }
+  }
+  if (a.w_bar == nullptr && a.b_bar == nullptr) return;
+  float *wo, *bo;
+  sum_outputs(t, k, p, a, &wo, &bo);
+  for (int c = threadIdx.x; c < mul; c += kThreads) {
+    float dw = 0.f, db = 0.f;
+    for (int64_t row = p; row < a.rows; row += parts) {
+      const int64_t at = row * t.dim + t.blk[k].off;
+      const float mean = a.stats[2 * (row * t.n + k)], rstd = a.stats[2 * (row * t.n + k) + 1];
+      for (int e = c; e < n; e += mul) {
+        const float y = a.y_bar[at + e];
+        dw = fmaf(y, (a.x[at + e] - mean) * rstd, dw);
+        db += y;
+      }
+    }
+    if (wo != nullptr) wo[c] = dw;
+    if (bo != nullptr) bo[c] = db;
+  }
+}
+
+template <int I>
+__global__ __launch_bounds__(kThreads) void irreps_norm_bwd_kernel(const IrrepTable t, const BwdArgs a) {
+  __shared__ float lds[2 * kWaves * kRegMul];
+  const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
+  if (I == 2 && t.blk[k].mul > kRegMul) return bwd_long(t, k, p, parts, a);
+  if (l == 0) bwd_block<1, I, 4>(t, k, p, parts, a, lds);
+  else if (l == 1) bwd_block<3, I, 2>(t, k, p, parts, a, lds);
+  else if (l == 2) bwd_block<5, I, 1>(t, k, p, parts, a, lds);
+  else bwd_block<7, I, 1>(t, k, p, parts, a, lds);
+}
+
+// Second stage of the sums: a workgroup takes 16 adjacent columns of one block (gains, then
+// biases), 16 slices of its rows of `part` in order each, then the slices in order.
+constexpr int kCols = 16, kSlices = kThreads / kCols;
+
+__global__ __launch_bounds__(kThreads) void irreps_parts_kernel(const IrrepTable t, const BwdArgs a) {
+  __shared__ float lds[kSlices][kCols];
+  const IrrepBlock& q = t.blk[blockIdx.y];
+  const int width = q.bias >= 0 ? 2 * q.mul : q.mul, parts = groups_of(t, blockIdx.y);
+  const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
+  const int c = blockIdx.x * kCols + lane;
+  float s = 0.f;
+  if (c < width)
+    for (int p = slice; p < parts; p += kSlices) s += a.part[q.part + static_cast<int64_t>(p) * width + c];
+  lds[slice][lane] = s;
+  __syncthreads();
+  if (slice != 0 || c >= width) return;
+#pragma unroll
+  for (int i = 1; i < kSlices; ++i) s += lds[i][lane];
+  if (c < q.mul) {
+    if (a.w_bar != nullptr) a.w_bar[q.ch + c] = s;
+  } else if (a.b_bar != nullptr) {
+    a.b_bar[q.bias + c - q.mul] = s;
+  }
+}
+
+bool wide(const IrrepTable& t) {
+  for (int k = 0; k < t.n; ++k)
+    if (t.blk[k].mul > 256) return true;
+  return false;
 }
 
 }  // namespace
 
-// Four waves a workgroup, each at least one node; beyond 512 a block's waves fill the card.
-int irreps_norm_parts(int32_t rows) { return std::min(rows / kWaves + (rows % kWaves != 0), 512); }
+// Deals about `total` workgroups to the blocks by width, at least one each and no more than
+// its nodes fill, and lays out the rows of partial sums; returns the floats these need.
+int64_t irreps_deal(IrrepTable& t, int32_t rows, int total) {
+  int64_t floats = 0;
+  t.groups = 0;
+  for (int k = 0; k < t.n; ++k) {
+    IrrepBlock& q = t.blk[k];
+    const int per = kThreads / lanes_of(q.mul);
+    const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per;
+    const int64_t share = (static_cast<int64_t>(total) * (2 * q.l + 1) * q.mul + t.dim - 1) / t.dim;
+    const int64_t parts = std::max<int64_t>(1, std::min(need, share));
+    q.wg = t.groups;
+    q.part = floats;
+    t.groups += static_cast<int32_t>(parts);
+    floats += parts * (q.bias >= 0 ? 2 * q.mul : q.mul);
+  }
+  return t.groups > t.n ? floats : 0;
+}
 
-hipError_t launch_irreps_norm_fwd(const IrrepTable& t, const float* x, const float* w, const float* b, float eps,
-                                  float* y, float* stats, int32_t rows, hipStream_t s) {
-  const int groups = std::min(rows / kWaves + (rows % kWaves != 0), 2048);
-  irreps_norm_fwd_kernel<<<dim3(static_cast<unsigned>(groups), static_cast<unsigned>(t.n)), dim3(kThreads), 0, s>>>(
-      t, x, w, b, eps, y, stats, rows);
+hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w, const float* b, float eps, float* y,
+                                  float* stats, int32_t rows, hipStream_t s) {
+  irreps_deal(t, rows, 2048);
+  const FwdArgs a{x, w, b, y, stats, eps, rows};
+  const dim3 grid(static_cast<unsigned>(t.groups));
+  if (wide(t)) irreps_norm_fwd_kernel<2><<<grid, dim3(kThreads), 0, s>>>(t, a);
+  else irreps_norm_fwd_kernel<1><<<grid, dim3(kThreads), 0, s>>>(t, a);
   return hipGetLastError();
 }
 
-hipError_t launch_irreps_norm_bwd(const IrrepTable& t, const float* x, const float* y_bar, const float* stats,
+// Four workgroups a CU.
+int64_t irreps_norm_part_floats(IrrepTable& t, int32_t rows) { return irreps_deal(t, rows, 1024); }
+
+hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_bar, const float* stats,
                                   const float* w, float* x_bar, float* w_bar, float* b_bar, float* part, int32_t rows,
                                   hipStream_t s) {
-  irreps_norm_bwd_kernel<<<dim3(static_cast<unsigned>(irreps_norm_parts(rows)), static_cast<unsigned>(t.n)),
-                           dim3(kThreads), 0, s>>>(t, x, y_bar, stats, w, x_bar, part, w_bar, b_bar, rows);
+  const bool whole = irreps_norm_part_floats(t, rows) == 0;
+  const BwdArgs a{x, y_bar, stats, w, x_bar, w_bar, b_bar, part, rows, whole};
+  const dim3 grid(static_cast<unsigned>(t.groups));
+  if (wide(t)) irreps_norm_bwd_kernel<2><<<grid, dim3(kThreads), 0, s>>>(t, a);
+  else irreps_norm_bwd_kernel<1><<<grid, dim3(kThreads), 0, s>>>(t, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || whole || (w_bar == nullptr && b_bar == nullptr)) return e;
+  int64_t most = 0;
+  for (int k = 0; k < t.n; ++k) most = std::max<int64_t>(most, int64_t{t.blk[k].bias >= 0 ? 2 : 1} * t.blk[k].mul);
+  irreps_parts_kernel<<<dim3(static_cast<unsigned>((most + kCols - 1) / kCols), static_cast<unsigned>(t.n)),
+                        dim3(kThreads), 0, s>>>(t, a);
   return hipGetLastError();
 }
 

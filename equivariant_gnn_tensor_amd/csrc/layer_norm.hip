@@ -9,14 +9,14 @@ namespace {
 constexpr int kCols = 16, kSlices = 64;
 
 __global__ __launch_bounds__(kCols* kSlices) void parts_reduce_kernel(const float* __restrict__ part, int parts,
-                                                                      int cols, int total, float* w_bar,
-                                                                      float* b_bar) {
+                                                                      int cols, int64_t total,
+                                                                      float* w_bar, float* b_bar) {
   __shared__ float lds[kSlices][kCols];
   const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
-  const int c = blockIdx.x * kCols + lane;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kCols + lane;
   float s = 0.f;
   if (c < total)
-    for (int p = slice; p < parts; p += kSlices) s += part[static_cast<int64_t>(p) * total + c];
+    for (int p = slice; p < parts; p += kSlices) s += part[p * total + c];
   lds[slice][lane] = s;
   __syncthreads();
   if (slice != 0 || c >= total) return;
@@ -46,11 +46,10 @@ int norm_parts(int32_t rows, int32_t cols) {
   return cols > norm::kRegCols ? std::min(rows, 32) : norm::by_cols(cols, CountParts{rows});
 }
 
-hipError_t launch_parts_reduce(const float* part, int parts, int cols, int b_cols, float* w_bar, float* b_bar,
-                               hipStream_t s) {
-  const int64_t total = static_cast<int64_t>(cols) + b_cols;
+hipError_t launch_parts_reduce(const float* part, int parts, int cols, float* w_bar, float* b_bar, hipStream_t s) {
+  const int64_t total = 2 * static_cast<int64_t>(cols);
   parts_reduce_kernel<<<dim3(static_cast<unsigned>((total + kCols - 1) / kCols)), dim3(kCols * kSlices), 0, s>>>(
-      part, parts, cols, static_cast<int>(total), w_bar, b_bar);
+      part, parts, cols, total, w_bar, b_bar);
   return hipGetLastError();
 }
 

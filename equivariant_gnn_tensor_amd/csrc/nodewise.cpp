@@ -156,7 +156,7 @@ etpc_status norm_backward(int64_t rows, int64_t cols, int32_t dtype, const Mat& 
   a.hs = h.stride, a.ybs = y_bar.stride, a.hbs = h_bar.stride, a.xbs = x_bar.stride, a.rbs = res_bar.stride;
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_norm_bwd(a, dtype, s));
   if (sums && parts > 1)
-    ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_parts_reduce(a.part, parts, a.cols, a.cols, w_bar, b_bar, s));
+    ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_parts_reduce(a.part, parts, a.cols, w_bar, b_bar, s));
   return ETPC_OK;
 }
 
@@ -173,7 +173,7 @@ etpc_status make_table(int32_t n, const etpc_irrep* irreps, IrrepTable* t) {
     if (ir.parity != 1 && ir.parity != -1) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "parity must be 1 or -1");
     const bool bias = ir.l == 0 && ir.parity == 1;
     t->blk[k] = IrrepBlock{static_cast<int32_t>(dim), ir.mul, ir.l, static_cast<int32_t>(channels),
-                           bias ? static_cast<int32_t>(biases) : -1, static_cast<int32_t>(groups)};
+                           bias ? static_cast<int32_t>(biases) : -1, static_cast<int32_t>(groups), 0, 0};
     dim += static_cast<int64_t>(ir.mul) * (2 * ir.l + 1);
     channels += ir.mul;
     biases += bias ? ir.mul : 0;
@@ -303,7 +303,7 @@ etpc_status etpc_irreps_norm_workspace_size(int32_t n_blocks, const etpc_irrep* 
   IrrepTable t;
   ETPC_TRY(make_table(n_blocks, irreps, &t));
   if (n_nodes < 0) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "negative n_nodes");
-  *bytes = n_nodes > 0 ? parts_bytes(irreps_norm_parts(n_nodes), int64_t{t.channels} + t.biases) : 0;
+  *bytes = n_nodes > 0 && t.n > 0 ? static_cast<size_t>(irreps_norm_part_floats(t, n_nodes)) * sizeof(float) : 0;
   return ETPC_OK;
 }
 
@@ -326,14 +326,11 @@ etpc_status etpc_irreps_norm_backward(int32_t n_blocks, const etpc_irrep* irreps
   if (x_bar != nullptr) ETPC_TRY(check_mat(mo, n_nodes, t.dim, ETPC_F32, true));
   if (stats == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null stats");
   ETPC_TRY(check_apart({mo}, {mx, my}, n_nodes, t.dim, ETPC_F32));
-  const int parts = irreps_norm_parts(n_nodes);
   const bool sums = w_bar != nullptr || b_bar != nullptr;
-  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, parts_bytes(parts, int64_t{t.channels} + t.biases)));
+  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, static_cast<size_t>(irreps_norm_part_floats(t, n_nodes)) * sizeof(float)));
   if (!sums && x_bar == nullptr) return ETPC_OK;
   float* part = static_cast<float*>(ws);
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_irreps_norm_bwd(t, x, y_bar, stats, w, x_bar, w_bar, b_bar, part, n_nodes, s));
-  if (sums && parts > 1)
-    ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_parts_reduce(part, parts, t.channels, t.biases, w_bar, b_bar, s));
   return ETPC_OK;
 }
 

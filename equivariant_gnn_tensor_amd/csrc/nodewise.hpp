@@ -48,10 +48,9 @@ struct NormBwdArgs {
 int norm_parts(int32_t rows, int32_t cols);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, hipStream_t s);
 
-// out[k][c] = sum_{p < parts} part[p][k * cols + c] for k = 0 (w_bar) and 1 (b_bar) in a
-// fixed order; a null output is skipped.  b_cols columns for k = 1.
-hipError_t launch_parts_reduce(const float* part, int parts, int cols, int b_cols, float* w_bar, float* b_bar,
-                               hipStream_t s);
+// w_bar[c], b_bar[c] = sum_{p < parts} part[p][0][c], part[p][1][c] in a fixed order; a null
+// output is skipped.
+hipError_t launch_parts_reduce(const float* part, int parts, int cols, float* w_bar, float* b_bar, hipStream_t s);
 
 // ---------------------------------------------------------------- dropout over rows
 hipError_t launch_dropout(const void* x, int64_t xs, void* y, int64_t ys, int32_t rows, int32_t cols, int dtype,
@@ -60,20 +59,23 @@ hipError_t launch_dropout(const void* x, int64_t xs, void* y, int64_t ys, int32_
 // ---------------------------------------------------------------- irreps features
 constexpr int kMaxIrreps = 64;
 // Block k of a feature row: [2l+1][mul] floats at off.  ch / bias: its first channel among
-// the gains / biases (bias = -1: none).  group: its first group of eight channels.
+// the gains / biases (bias = -1: none).  group: its first group of eight channels.  wg, part:
+// its first workgroup and its first partial sum in the irreps norm (irreps_deal).
 struct IrrepBlock {
-  int32_t off, mul, l, ch, bias, group;
+  int32_t off, mul, l, ch, bias, group, wg;
+  int64_t part;
 };
 struct IrrepTable {
-  int32_t n, dim, channels, biases;
+  int32_t n, dim, channels, biases, groups;
   IrrepBlock blk[kMaxIrreps];
 };
 hipError_t launch_irreps_dropout(const IrrepTable& t, const float* x, float* y, int32_t rows, const DropArgs& d,
                                  hipStream_t s);
-hipError_t launch_irreps_norm_fwd(const IrrepTable& t, const float* x, const float* w, const float* b, float eps,
-                                  float* y, float* stats, int32_t rows, hipStream_t s);
-int irreps_norm_parts(int32_t rows);
-hipError_t launch_irreps_norm_bwd(const IrrepTable& t, const float* x, const float* y_bar, const float* stats,
+// These fill in the table's deal of workgroups.
+hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w, const float* b, float eps, float* y,
+                                  float* stats, int32_t rows, hipStream_t s);
+int64_t irreps_norm_part_floats(IrrepTable& t, int32_t rows);
+hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_bar, const float* stats,
                                   const float* w, float* x_bar, float* w_bar, float* b_bar, float* part, int32_t rows,
                                   hipStream_t s);
 
