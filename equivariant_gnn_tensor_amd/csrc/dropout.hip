@@ -22,7 +22,7 @@ constexpr int64_t kMaxGroups = int64_t{1} << 22;
 
 // Thread t of workgroup b takes vector b * 256 + t of the rows * vecs vectors.  The
 // workgroup divides its first index once in 64 bits; the threads divide what is left over.
-template <class T>
+template <class T, bool kEven>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(const T* x, int64_t xs, T* y, int64_t ys, int64_t total,
                                                            int cols, RowMap vecs, DropArgs d) {
   const uint64_t offset = d.threshold != 0 ? drop_offset(d) : 0;
@@ -34,27 +34,28 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const T* x, int64_t x
     const uint32_t vec = left - q * static_cast<uint32_t>(vecs.div);
     const int64_t row = static_cast<int64_t>(row0 + q);
     float v[8];
-    load8(x + row * xs, static_cast<int>(8 * vec), cols, v);
+    load<8, kEven>(x + row * xs, static_cast<int>(8 * vec), cols, v);
     if (d.threshold != 0) drop8(v, philox(vec, static_cast<uint32_t>(row), offset, d.seed), d.threshold, d.scale);
-    store8(y + row * ys, static_cast<int>(8 * vec), cols, v);
+    store<8, kEven>(y + row * ys, static_cast<int>(8 * vec), cols, v);
   }
 }
 
 // A thread takes eight channels of one block of one node, with all 2l+1 components: they
 // share one mask, so a kept channel turns under a rotation as before.
-template <int D>
+template <int D, bool kEven>
 __device__ inline void drop_block(const float* x, float* y, const IrrepBlock& k, int c, const Philox& r,
                                   const DropArgs& d) {
   float v[D][8];
 #pragma unroll
-  for (int m = 0; m < D; ++m) load8(x + m * k.mul, c, k.mul, v[m]);
+  for (int m = 0; m < D; ++m) load<8, kEven>(x + m * k.mul, c, k.mul, v[m]);
 #pragma unroll
   for (int m = 0; m < D; ++m) {
     if (d.threshold != 0) drop8(v[m], r, d.threshold, d.scale);
-    store8(y + m * k.mul, c, k.mul, v[m]);
+    store<8, kEven>(y + m * k.mul, c, k.mul, v[m]);
   }
 }
 
+template <bool kEven>
 __global__ __launch_bounds__(kThreads) void irreps_dropout_kernel(const IrrepTable t, const float* x, float* y,
                                                                   int32_t rows, DropArgs d) {
   const IrrepBlock k = t.blk[blockIdx.y];
@@ -69,10 +70,10 @@ __global__ __launch_bounds__(kThreads) void irreps_dropout_kernel(const IrrepTab
                          ? philox(static_cast<uint32_t>(k.group + g), static_cast<uint32_t>(row), offset, d.seed)
                          : Philox{};
     const int64_t at = static_cast<int64_t>(row) * t.dim + k.off;
-    if (k.l == 0) drop_block<1>(x + at, y + at, k, 8 * g, r, d);
-    else if (k.l == 1) drop_block<3>(x + at, y + at, k, 8 * g, r, d);
-    else if (k.l == 2) drop_block<5>(x + at, y + at, k, 8 * g, r, d);
-    else drop_block<7>(x + at, y + at, k, 8 * g, r, d);
+    if (k.l == 0) drop_block<1, kEven>(x + at, y + at, k, 8 * g, r, d);
+    else if (k.l == 1) drop_block<3, kEven>(x + at, y + at, k, 8 * g, r, d);
+    else if (k.l == 2) drop_block<5, kEven>(x + at, y + at, k, 8 * g, r, d);
+    else drop_block<7, kEven>(x + at, y + at, k, 8 * g, r, d);
   }
 }
 
@@ -85,8 +86,9 @@ hipError_t rows_of(const void* x, int64_t xs, void* y, int64_t ys, int32_t rows,
                    hipStream_t s) {
   const int32_t vecs = (cols + 7) / 8;
   const int64_t total = static_cast<int64_t>(rows) * vecs;
-  dropout_kernel<T><<<dim3(groups_of(total)), dim3(kThreads), 0, s>>>(
-      static_cast<const T*>(x), xs, static_cast<T*>(y), ys, total, cols, make_rowmap(0, 0, vecs), d);
+  const auto kernel = cols % 8 == 0 ? dropout_kernel<T, true> : dropout_kernel<T, false>;
+  kernel<<<dim3(groups_of(total)), dim3(kThreads), 0, s>>>(static_cast<const T*>(x), xs, static_cast<T*>(y), ys, total,
+                                                           cols, make_rowmap(0, 0, vecs), d);
   return hipGetLastError();
 }
 
@@ -102,10 +104,14 @@ hipError_t launch_dropout(const void* x, int64_t xs, void* y, int64_t ys, int32_
 hipError_t launch_irreps_dropout(const IrrepTable& t, const float* x, float* y, int32_t rows, const DropArgs& d,
                                  hipStream_t s) {
   int32_t most = 0;
-  for (int k = 0; k < t.n; ++k) most = std::max(most, (t.blk[k].mul + 7) / 8);
+  bool even = true;
+  for (int k = 0; k < t.n; ++k) {
+    most = std::max(most, (t.blk[k].mul + 7) / 8);
+    even = even && t.blk[k].mul % 8 == 0;
+  }
   const int64_t total = static_cast<int64_t>(rows) * most;
-  irreps_dropout_kernel<<<dim3(groups_of(total), static_cast<unsigned>(t.n)),
-                          dim3(kThreads), 0, s>>>(t, x, y, rows, d);
+  const auto kernel = even ? irreps_dropout_kernel<true> : irreps_dropout_kernel<false>;
+  kernel<<<dim3(groups_of(total), static_cast<unsigned>(t.n)), dim3(kThreads), 0, s>>>(t, x, y, rows, d);
   return hipGetLastError();
 }
 

@@ -46,26 +46,10 @@ __device__ inline float sum_lanes(float v, int g) {
   return v;
 }
 
-__device__ inline void load4(const float* __restrict__ p, int c, int n, float (&v)[4]) {
-  if (c + 4 <= n) {
-    __builtin_memcpy(v, p + c, 16);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = c + k < n ? p[c + k] : 0.f;
-  }
-}
-__device__ inline void store4(float* __restrict__ p, int c, int n, const float (&v)[4]) {
-  if (c + 4 <= n) {
-    __builtin_memcpy(p + c, v, 16);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (c + k < n) p[c + k] = v[k];
-  }
-}
+template <bool kEven>
 __device__ inline void load4_or(const float* __restrict__ p, int c, int n, float missing, float (&v)[4]) {
   if (p != nullptr) {
-    load4(p, c, n, v);
+    load<4, kEven>(p, c, n, v);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = missing;
@@ -104,7 +88,7 @@ __device__ inline int block_of(const IrrepTable& t, int wg) {
 __device__ inline int groups_of(const IrrepTable& t, int k) { return (k + 1 < t.n ? t.blk[k + 1].wg : t.groups) - t.blk[k].wg; }
 
 // D = 2l+1 components, I vectors of four channels a lane, R nodes in flight a group.
-template <int D, int I, int R>
+template <int D, int I, int R, bool kEven>
 __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
   const int mul = t.blk[k].mul, off = t.blk[k].off;
   const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), per = kThreads / G;
@@ -112,8 +96,8 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
   float w[I][4], b[I][4];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    load4_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
-    load4_or(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, 4 * (lane + i * G), mul, 0.f, b[i]);
+    load4_or<kEven>(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
+    load4_or<kEven>(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, 4 * (lane + i * G), mul, 0.f, b[i]);
   }
   const int64_t step = static_cast<int64_t>(parts) * per;
   for (int64_t first = static_cast<int64_t>(p) * per + threadIdx.x / G; first < a.rows; first += R * step) {
@@ -125,7 +109,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
         for (int d = 0; d < D; ++d)
 #pragma unroll
           for (int i = 0; i < I; ++i)
-            load4(a.x + (first + r * step) * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
+            load<4, kEven>(a.x + (first + r * step) * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t row = first + r * step;
@@ -145,7 +129,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
           for (int j = 0; j < 4; ++j)
             if (D == 1) {
               v[r][d][i][j] -= mean;
-              if (4 * (lane + i * G) + j < mul) s = fmaf(v[r][d][i][j], v[r][d][i][j], s);
+              if ((kEven ? 4 * (lane + i * G) : 4 * (lane + i * G) + j) < mul) s = fmaf(v[r][d][i][j], v[r][d][i][j], s);
             } else {
               s = fmaf(v[r][d][i][j], v[r][d][i][j], s);   // channels past the last hold 0
             }
@@ -161,13 +145,14 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
           float o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = fmaf(v[r][d][i][j] * rstd, w[i][j], b[i][j]);
-          store4(a.y + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
+          store<4, kEven>(a.y + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
         }
     }
   }
 }
 
 // Segments of more channels: a wave reads its segment once for each sum and once for y.
+template <bool kEven>
 __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
   const int mul = t.blk[k].mul, n = (2 * t.blk[k].l + 1) * mul, lane = threadIdx.x & 63;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -180,7 +165,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     if (n == mul) {
       for (int e = 4 * lane; e < n; e += 256) {
         float v[4];
-        load4(x, e, n, v);
+        load<4, kEven>(x, e, n, v);
         s += (v[0] + v[1]) + (v[2] + v[3]);
       }
       mean = sum_lanes(s, 64) / static_cast<float>(n);
@@ -188,7 +173,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     }
     for (int e = 4 * lane; e < n; e += 256) {
       float v[4];
-      load4(x, e, n, v);
+      load<4, kEven>(x, e, n, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (e + j < n) s = fmaf(v[j] - mean, v[j] - mean, s);
@@ -201,24 +186,24 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     for (int d = 0; d * mul < n; ++d)
       for (int c = 4 * lane; c < mul; c += 256) {
         float v[4], g[4], h[4];
-        load4(x + d * mul, c, mul, v);
-        load4_or(w, c, mul, 1.f, g);
-        load4_or(b, c, mul, 0.f, h);
+        load<4, kEven>(x + d * mul, c, mul, v);
+        load4_or<kEven>(w, c, mul, 1.f, g);
+        load4_or<kEven>(b, c, mul, 0.f, h);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], h[j]);
-        store4(a.y + row * t.dim + t.blk[k].off + d * mul, c, mul, v);
+        store<4, kEven>(a.y + row * t.dim + t.blk[k].off + d * mul, c, mul, v);
       }
   }
 }
 
-template <int I>
+template <int I, bool kEven>
 __global__ __launch_bounds__(kThreads) void irreps_norm_fwd_kernel(const IrrepTable t, const FwdArgs a) {
   const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
-  if (I == 2 && t.blk[k].mul > kRegMul) return fwd_long(t, k, p, parts, a);
-  if (l == 0) fwd_block<1, I, 4>(t, k, p, parts, a);
-  else if (l == 1) fwd_block<3, I, 2>(t, k, p, parts, a);
-  else if (l == 2) fwd_block<5, I, 1>(t, k, p, parts, a);
-  else fwd_block<7, I, 1>(t, k, p, parts, a);
+  if (I == 2 && t.blk[k].mul > kRegMul) return fwd_long<kEven>(t, k, p, parts, a);
+  if (l == 0) fwd_block<1, I, 4, kEven>(t, k, p, parts, a);
+  else if (l == 1) fwd_block<3, I, 2, kEven>(t, k, p, parts, a);
+  else if (l == 2) fwd_block<5, I, 1, kEven>(t, k, p, parts, a);
+  else fwd_block<7, I, 1, kEven>(t, k, p, parts, a);
 }
 
 // Where a workgroup of the backward pass leaves its sums: gains first, then biases.
@@ -235,7 +220,7 @@ __device__ inline void sum_outputs(const IrrepTable& t, int k, int p, const BwdA
 
 // A group keeps its channels' sums of y_bar xh and y_bar in registers while it walks its
 // nodes; lanes, then waves are added at the end in a fixed order.
-template <int D, int I, int R>
+template <int D, int I, int R, bool kEven>
 __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a, float* lds) {
   const int mul = t.blk[k].mul, off = t.blk[k].off;
   const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), per = kThreads / G;
@@ -243,7 +228,7 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
   float w[I][4], dw[I][4] = {}, db[I][4] = {};
 #pragma unroll
   for (int i = 0; i < I; ++i)
-    load4_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
+    load4_or<kEven>(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
   const int64_t step = static_cast<int64_t>(parts) * per;
   for (int64_t first = static_cast<int64_t>(p) * per + threadIdx.x / G; first < a.rows; first += R * step) {
     float v[R][D][I][4], g[R][D][I][4], mean[R], rstd[R];
@@ -255,8 +240,8 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
         for (int d = 0; d < D; ++d)
 #pragma unroll
           for (int i = 0; i < I; ++i) {
-            load4(a.x + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
-            load4(a.y_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, g[r][d][i]);
+            load<4, kEven>(a.x + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
+            load<4, kEven>(a.y_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, g[r][d][i]);
           }
         mean[r] = D == 1 ? a.stats[2 * (row * t.n + k)] : 0.f;
         rstd[r] = a.stats[2 * (row * t.n + k) + 1];
@@ -292,7 +277,7 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
           float o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = rstd[r] * (g[r][d][i][j] - fmaf(v[r][d][i][j], m1, m0));
-          store4(a.x_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
+          store<4, kEven>(a.x_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
         }
     }
   }
@@ -327,6 +312,7 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
   }
 }
 
+template <bool kEven>
 __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a) {
   const int mul = t.blk[k].mul, n = (2 * t.blk[k].l + 1) * mul, lane = threadIdx.x & 63;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -339,9 +325,9 @@ __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, co
     for (int d = 0; d * mul < n; ++d)
       for (int c = 4 * lane; c < mul; c += 256) {
         float v[4], y[4], g[4];
-        load4(a.x + at + d * mul, c, mul, v);
-        load4(a.y_bar + at + d * mul, c, mul, y);
-        load4_or(w, c, mul, 1.f, g);
+        load<4, kEven>(a.x + at + d * mul, c, mul, v);
+        load<4, kEven>(a.y_bar + at + d * mul, c, mul, y);
+        load4_or<kEven>(w, c, mul, 1.f, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           s0 = fmaf(y[j], g[j], s0);
@@ -352,12 +338,12 @@ __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, co
     for (int d = 0; d * mul < n; ++d)
       for (int c = 4 * lane; c < mul; c += 256) {
         float v[4], y[4], g[4];
-        load4(a.x + at + d * mul, c, mul, v);
-        load4(a.y_bar + at + d * mul, c, mul, y);
-        load4_or(w, c, mul, 1.f, g);
+        load<4, kEven>(a.x + at + d * mul, c, mul, v);
+        load<4, kEven>(a.y_bar + at + d * mul, c, mul, y);
+        load4_or<kEven>(w, c, mul, 1.f, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = rstd * (fmaf(y[j], g[j], -m0) - (v[j] - mean) * rstd * m1);
-        store4(a.x_bar + at + d * mul, c, mul, v);
+        store<4, kEven>(a.x_bar + at + d * mul, c, mul, v);
       }
   }
   if (a.w_bar == nullptr && a.b_bar == nullptr) return;
@@ -379,15 +365,15 @@ __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, co
   }
 }
 
-template <int I>
+template <int I, bool kEven>
 __global__ __launch_bounds__(kThreads) void irreps_norm_bwd_kernel(const IrrepTable t, const BwdArgs a) {
   __shared__ float lds[2 * kWaves * kRegMul];
   const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
-  if (I == 2 && t.blk[k].mul > kRegMul) return bwd_long(t, k, p, parts, a);
-  if (l == 0) bwd_block<1, I, 4>(t, k, p, parts, a, lds);
-  else if (l == 1) bwd_block<3, I, 2>(t, k, p, parts, a, lds);
-  else if (l == 2) bwd_block<5, I, 1>(t, k, p, parts, a, lds);
-  else bwd_block<7, I, 1>(t, k, p, parts, a, lds);
+  if (I == 2 && t.blk[k].mul > kRegMul) return bwd_long<kEven>(t, k, p, parts, a);
+  if (l == 0) bwd_block<1, I, 4, kEven>(t, k, p, parts, a, lds);
+  else if (l == 1) bwd_block<3, I, 2, kEven>(t, k, p, parts, a, lds);
+  else if (l == 2) bwd_block<5, I, 1, kEven>(t, k, p, parts, a, lds);
+  else bwd_block<7, I, 1, kEven>(t, k, p, parts, a, lds);
 }
 
 // Second stage of the sums: a workgroup takes 16 adjacent columns of one block (gains, then
@@ -415,10 +401,16 @@ __global__ __launch_bounds__(kThreads) void irreps_parts_kernel(const IrrepTable
   }
 }
 
-bool wide(const IrrepTable& t) {
-  for (int k = 0; k < t.n; ++k)
-    if (t.blk[k].mul > 256) return true;
-  return false;
+// The kernel for a table: blocks past 256 channels take two vectors a lane, and only
+// channel counts that are no multiple of four need the code for ends inside a vector.
+template <class K>
+K pick(const IrrepTable& t, K narrow, K narrow_ragged, K wide, K wide_ragged) {
+  bool even = true, is_wide = false;
+  for (int k = 0; k < t.n; ++k) {
+    even = even && t.blk[k].mul % 4 == 0;
+    is_wide = is_wide || t.blk[k].mul > 256;
+  }
+  return is_wide ? (even ? wide : wide_ragged) : (even ? narrow : narrow_ragged);
 }
 
 }  // namespace
@@ -446,9 +438,9 @@ hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w,
                                   float* stats, int32_t rows, hipStream_t s) {
   irreps_deal(t, rows, 2048);
   const FwdArgs a{x, w, b, y, stats, eps, rows};
-  const dim3 grid(static_cast<unsigned>(t.groups));
-  if (wide(t)) irreps_norm_fwd_kernel<2><<<grid, dim3(kThreads), 0, s>>>(t, a);
-  else irreps_norm_fwd_kernel<1><<<grid, dim3(kThreads), 0, s>>>(t, a);
+  const auto kernel = pick(t, irreps_norm_fwd_kernel<1, true>, irreps_norm_fwd_kernel<1, false>,
+                           irreps_norm_fwd_kernel<2, true>, irreps_norm_fwd_kernel<2, false>);
+  kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   return hipGetLastError();
 }
 
@@ -460,9 +452,9 @@ hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_
                                   hipStream_t s) {
   const bool whole = irreps_norm_part_floats(t, rows) == 0;
   const BwdArgs a{x, y_bar, stats, w, x_bar, w_bar, b_bar, part, rows, whole};
-  const dim3 grid(static_cast<unsigned>(t.groups));
-  if (wide(t)) irreps_norm_bwd_kernel<2><<<grid, dim3(kThreads), 0, s>>>(t, a);
-  else irreps_norm_bwd_kernel<1><<<grid, dim3(kThreads), 0, s>>>(t, a);
+  const auto kernel = pick(t, irreps_norm_bwd_kernel<1, true>, irreps_norm_bwd_kernel<1, false>,
+                           irreps_norm_bwd_kernel<2, true>, irreps_norm_bwd_kernel<2, false>);
+  kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole || (w_bar == nullptr && b_bar == nullptr)) return e;
   int64_t most = 0;

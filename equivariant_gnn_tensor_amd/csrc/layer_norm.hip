@@ -15,8 +15,17 @@ __global__ __launch_bounds__(kCols* kSlices) void parts_reduce_kernel(const floa
   const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kCols + lane;
   float s = 0.f;
-  if (c < total)
-    for (int p = slice; p < parts; p += kSlices) s += part[p * total + c];
+  if (c < total) {
+    int p = slice;
+    for (; p + 7 * kSlices < parts; p += 8 * kSlices) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = part[static_cast<int64_t>(p + i * kSlices) * total + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; p < parts; p += kSlices) s += part[p * total + c];
+  }
   lds[slice][lane] = s;
   __syncthreads();
   if (slice != 0 || c >= total) return;
@@ -34,7 +43,7 @@ struct CountParts {
   template <int G, int V>
   int operator()() const {
     constexpr int per = norm::threads_of<G>() / G;
-    constexpr int most = G > 256 ? 256 : G > 64 || V > 1 ? 512 : 1024;
+    constexpr int most = G == 1024 ? 256 : 256 * 8 / (norm::threads_of<G>() / 64);
     return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(rows) + per - 1) / per, most));
   }
 };
@@ -43,7 +52,7 @@ struct CountParts {
 
 // Workgroups of the backward pass, each of which leaves one row of partial sums.
 int norm_parts(int32_t rows, int32_t cols) {
-  return cols > norm::kRegCols ? std::min(rows, 32) : norm::by_cols(cols, CountParts{rows});
+  return cols > norm::kRegCols ? std::min(rows, 32) : norm::by_cols_bwd(cols, CountParts{rows});
 }
 
 hipError_t launch_parts_reduce(const float* part, int parts, int cols, float* w_bar, float* b_bar, hipStream_t s) {

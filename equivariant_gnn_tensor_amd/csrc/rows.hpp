@@ -1,4 +1,4 @@
-// Building blocks of the row kernels: eight-element loads and stores of any alignment in
+// Building blocks of the row kernels: vector loads and stores of any alignment in
 // fp32, bf16 and fp16, and sums over groups of lanes.
 #pragma once
 
@@ -7,42 +7,80 @@
 
 namespace etpc {
 
+template <class T, int N>
+using VecN = T __attribute__((ext_vector_type(N)));
 template <class T>
-using Vec8 = T __attribute__((ext_vector_type(8)));
-using Float8 = Vec8<float>;
+using Vec8 = VecN<T, 8>;
 
 // Element types of the row operators (etpc_dtype).
 using Bf16 = __bf16;
 using F16 = _Float16;
 
-// Eight elements of a row from column c on; columns at and past n read as 0.  The address
-// only has to be aligned to the element: unaligned vector accesses are native here, so
-// odd row lengths and strides run the same code as even ones.
-template <class T>
-__device__ inline void load8(const T* __restrict__ p, int c, int n, float (&v)[8]) {
-  if (c + 8 <= n) {
-    Vec8<T> t;
-    __builtin_memcpy(&t, p + c, sizeof(t));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(t[k]);
+// N = 4 or 8 elements of a row of n from column c on (a multiple of N), in two steps.
+// fetch issues one vector load and waits for nothing: the last vector of a row that ends
+// inside it is read as the row's last N elements.  settle, at the point of use, moves those
+// down into place and clears what lies past the end (columns at and past n are 0).
+// Element-wise loads of the row's end cost more than the whole rest of it (bf16 rows of
+// 2047: 226 us against 63 for 2048, layer norm backward of 32768 rows).  The address only
+// has to be aligned to the element: unaligned vector accesses are native here.  kEven: n is
+// a multiple of N, so nothing ends inside a vector (and the code for it costs no registers).
+template <int N, bool kEven, class T>
+__device__ inline VecN<T, N> fetch(const T* __restrict__ p, int c, int n) {
+  VecN<T, N> t = {};
+  if (kEven) {
+    if (c < n) __builtin_memcpy(&t, p + c, sizeof(t));
+  } else if (n >= N) {
+    if (c < n) __builtin_memcpy(&t, p + min(c, n - N), sizeof(t));
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = c + k < n ? static_cast<float>(p[c + k]) : 0.f;
+    for (int k = 0; k < N; ++k)
+      if (c + k < n) t[k] = p[c + k];
+  }
+  return t;
+}
+
+template <int N, bool kEven, class T>
+__device__ inline void settle(const VecN<T, N>& t, int c, int n, float (&v)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = static_cast<float>(t[k]);
+  if (!kEven && n >= N && c + N > n && c < n) {
+    const int down = c + N - n;   // 1 .. N - 1
+#pragma unroll
+    for (int by = 1; by < N; by *= 2)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = (down & by) ? (k + by < N ? v[k + by] : 0.f) : v[k];
   }
 }
 
-// Rounds to the element type here, once (to nearest, ties to even).
-template <class T>
-__device__ inline void store8(T* __restrict__ p, int c, int n, const float (&v)[8]) {
-  if (c + 8 <= n) {
-    Vec8<T> t;
+template <int N, bool kEven, class T>
+__device__ inline void load(const T* __restrict__ p, int c, int n, float (&v)[N]) {
+  settle<N, kEven, T>(fetch<N, kEven>(p, c, n), c, n, v);
+}
+
+// Rounds to the element type here, once (to nearest, ties to even).  The end of a row goes
+// out as at most three stores, of four, two and one elements.
+template <int N, bool kEven, class T>
+__device__ inline void store(T* __restrict__ p, int c, int n, const float (&v)[N]) {
+  VecN<T, N> t;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = static_cast<T>(v[k]);
+  for (int k = 0; k < N; ++k) t[k] = static_cast<T>(v[k]);
+  if (kEven ? c < n : c + N <= n) {
     __builtin_memcpy(p + c, &t, sizeof(t));
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < n) p[c + k] = static_cast<T>(v[k]);
+  } else if (!kEven && c < n) {
+    const int left = n - c;   // 1 .. N - 1
+    if (N == 8 && (left & 4)) {
+      const VecN<T, 4> u = {t[0], t[1], t[2], t[3]};
+      __builtin_memcpy(p + c, &u, sizeof(u));
+    }
+    if (left & 2) {
+      const bool high = N == 8 && (left & 4);
+      const VecN<T, 2> u = {high ? t[N - 4] : t[0], high ? t[N - 3] : t[1]};
+      __builtin_memcpy(p + c + (left & 4), &u, sizeof(u));
+    }
+    if (left & 1) {
+      const T low = (left & 2) ? t[2] : t[0], high = (left & 2) ? t[N - 2] : t[N - 4];
+      p[n - 1] = N == 8 && (left & 4) ? high : low;
+    }
   }
 }
 
