@@ -38,21 +38,31 @@ __global__ __launch_bounds__(kCols* kSlices) void parts_reduce_kernel(const floa
   }
 }
 
+// Workgroups of the backward pass, each of which leaves one row of partial sums.  By waves a
+// CU: 8 for fp32 rows; 16-bit rows of the join carry half the bytes a wave and want 12
+// (65408 x 1024 bf16: 142 us with 8, 131 with 12); 16-bit rows that leave a quarter of
+// their threads idle want 16 (50000 x 577 bf16: 103 us with 8, 77 with 16).  Three rows a
+// group at least, once there are 128 workgroups: fewer sums to add up afterwards (1000 x
+// 1024 fp32: 15.2 us with one row, 10.0 with three).
 struct CountParts {
-  int32_t rows;
+  int32_t rows, cols;
+  bool wide, join;   // 32-bit elements; the join
   template <int G, int V>
   int operator()() const {
-    constexpr int per = norm::threads_of<G>() / G;
-    constexpr int most = G == 1024 ? 256 : 256 * 8 / (norm::threads_of<G>() / 64);
-    return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(rows) + per - 1) / per, most));
+    constexpr int threads = norm::bwd_threads<G>(), per = threads / G;
+    const bool idle = G > 64 && 4 * ((static_cast<int64_t>(cols) + 7) / 8) <= 3 * G * V;
+    const int waves = (idle && !wide) || G == 1024 ? 16 : join && !wide ? 12 : 8;
+    const int64_t most = 256 * waves / (threads / 64);
+    const int64_t units = (static_cast<int64_t>(rows) + per - 1) / per;
+    return static_cast<int>(std::min(units, std::max<int64_t>(128, std::min((units + 2) / 3, most))));
   }
 };
 
 }  // namespace
 
-// Workgroups of the backward pass, each of which leaves one row of partial sums.
-int norm_parts(int32_t rows, int32_t cols) {
-  return cols > norm::kRegCols ? std::min(rows, 32) : norm::by_cols_bwd(cols, CountParts{rows});
+int norm_parts_most(int32_t rows, int32_t cols) {
+  if (cols > norm::kRegCols) return std::min(rows, 32);
+  return norm::bwd_shape(cols, CountParts{rows, cols, false, true});
 }
 
 hipError_t launch_parts_reduce(const float* part, int parts, int cols, float* w_bar, float* b_bar, hipStream_t s) {
@@ -64,6 +74,11 @@ hipError_t launch_parts_reduce(const float* part, int parts, int cols, float* w_
 
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, hipStream_t s) {
   return dtype == ETPC_F32 ? norm::fwd_f32(a, s) : dtype == ETPC_BF16 ? norm::fwd_bf16(a, s) : norm::fwd_f16(a, s);
+}
+
+int norm_parts(const NormBwdArgs& a, int dtype) {
+  if (a.cols > norm::kRegCols) return std::min(a.rows, 32);
+  return norm::bwd_shape(a.cols, CountParts{a.rows, a.cols, dtype == ETPC_F32, norm::bwd_join(a)});
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, hipStream_t s) {

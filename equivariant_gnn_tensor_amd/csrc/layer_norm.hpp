@@ -23,118 +23,197 @@ namespace etpc {
 namespace norm {
 
 constexpr int kThreads = 256;
-constexpr int kRegCols = 16384;   // longest row kept in registers: 512 threads of 32 columns
+constexpr int kRegCols = 16384;   // longest row kept in registers
 
+// Threads of a workgroup: the forward pass shares one between rows of up to a wave, the
+// backward pass also between two rows of two waves (fewer rows of partial sums).
 template <int G>
-constexpr int threads_of() {
+constexpr int fwd_threads() {
   return G > 64 ? G : kThreads;
 }
+template <int G>
+constexpr int bwd_threads() {
+  return G > kThreads ? G : kThreads;
+}
 
-template <class T, int G, int V, bool kEven>
-__global__ __launch_bounds__(threads_of<G>()) void fwd_kernel(const NormFwdArgs a) {
-  constexpr int kRows = threads_of<G>() / G;
+// Both by value, so that the arrays they come from stay in registers.
+__device__ inline uint32_t pick(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
+
+// Where a thread's vector i lies in a row of n columns.  A vector that would start or end
+// past the row is moved back to the row's last eight columns: every access is one full
+// vector inside the row, with no branch around it, and what it holds and writes there is
+// bit for bit what the columns' owners hold and write.  Only sums tell the copies apart:
+// element k counts from `skip` on (8: a copy as a whole).  Rows shorter than a vector (one
+// thread each) are read and written by elements.
+template <int G, int V, bool kEven>
+struct Span {
+  int n, at[V], skip[V];
+  __device__ inline Span(int lane, int cols) : n(cols) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = 8 * (lane + i * G);
+      at[i] = tiny() ? 0 : min(c, n - 8);
+      skip[i] = tiny() ? 0 : min(c - at[i], 8);
+    }
+  }
+  __device__ inline bool tiny() const { return G == 1 && !kEven && n < 8; }
+  __device__ inline bool counts(int i, int k) const {
+    return kEven ? skip[i] == 0 : k >= skip[i] && (G > 1 || k < n);
+  }
+  template <class T>
+  __device__ inline Vec8<T> fetch(const T* __restrict__ row, int i) const {
+    Vec8<T> t = {};
+    if (tiny()) {
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (k < n) t[k] = row[k];
+    } else {
+      __builtin_memcpy(&t, row + static_cast<unsigned>(at[i]), sizeof(t));
+    }
+    return t;
+  }
+  template <class T>
+  __device__ inline void load(const T* __restrict__ row, int i, float (&v)[8]) const {
+    const Vec8<T> t = fetch(row, i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(t[k]);
+  }
+  template <class T>
+  __device__ inline void load_or(const T* __restrict__ row, int i, float missing, float (&v)[8]) const {
+    if (row != nullptr) {
+      load(row, i, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = missing;
+    }
+  }
+  // Rounds to the element type here, once (to nearest, ties to even).
+  template <class T>
+  __device__ inline void store(T* __restrict__ row, int i, const float (&v)[8]) const {
+    Vec8<T> t;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = static_cast<T>(v[k]);
+    if (tiny()) {
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (k < n) row[k] = t[k];
+    } else {
+      __builtin_memcpy(row + static_cast<unsigned>(at[i]), &t, sizeof(t));
+    }
+  }
+  // The mask of a vector that was moved back takes its fields from two generator calls.
+  __device__ inline void drop(float (&v)[8], int i, int64_t row, uint64_t offset, const DropArgs& d) const {
+    Philox r = philox(static_cast<uint32_t>(at[i]) / 8, static_cast<uint32_t>(row), offset, d.seed);
+    const int by = kEven ? 0 : at[i] % 8;
+    if (by != 0) {
+      const Philox q = philox(static_cast<uint32_t>(at[i]) / 8 + 1, static_cast<uint32_t>(row), offset, d.seed);
+      const uint32_t w[8] = {r.w[0], r.w[1], r.w[2], r.w[3], q.w[0], q.w[1], q.w[2], q.w[3]};
+      uint32_t by4[6], by2[5];
+#pragma unroll
+      for (int k = 0; k < 6; ++k) by4[k] = pick(by & 4, w[k + 2], w[k]);
+#pragma unroll
+      for (int k = 0; k < 5; ++k) by2[k] = pick(by & 2, by4[k + 1], by4[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.w[k] = pick(by & 1, (by2[k] >> 16) | (by2[k + 1] << 16), by2[k]);
+    }
+    drop8(v, r, d.threshold, d.scale);
+  }
+};
+
+// The row of a thread's group among the kRows of its workgroup; rows of whole waves get it in
+// a scalar register.
+template <int G>
+__device__ inline int group_index() {
+  const int group = threadIdx.x / G;
+  return G >= 64 ? __builtin_amdgcn_readfirstlane(group) : group;
+}
+
+// One vector a thread was measured against two and four (forward pass, 64 MB in): 16-bit
+// rows need 32 to 64 bytes a thread in flight to reach the copy rate, 32-bit rows 32 to 64
+// too, which is half the vectors.
+template <class T, int G, int V, bool kEven, bool kJoin>
+__global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs a) {
+  constexpr int kRows = fwd_threads<G>() / G;
   __shared__ float lds[G > 64 ? 2 * G / 64 : 1];
-  const int lane = threadIdx.x % G, n = a.cols;
-  const float inv_n = 1.f / static_cast<float>(n);
-  const bool drop = a.drop.threshold != 0;
+  const Span<G, V, kEven> span(threadIdx.x % G, a.cols);
+  const float inv_n = 1.f / static_cast<float>(a.cols);
+  const bool drop = kJoin && a.drop.threshold != 0;
   const uint64_t offset = drop ? drop_offset(a.drop) : 0;
   int half = 0;
   float w[V][8], b[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = 8 * (lane + i * G);
-    if (a.w != nullptr) load<8, kEven>(a.w, c, n, w[i]);
-    if (a.b != nullptr) load<8, kEven>(a.b, c, n, b[i]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (a.w == nullptr) w[i][k] = 1.f;
-      if (a.b == nullptr) b[i][k] = 0.f;
-    }
+    span.load_or(a.w, i, 1.f, w[i]);
+    span.load_or(a.b, i, 0.f, b[i]);
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * kRows) {
-    const T* x = static_cast<const T*>(a.x) + row * a.xs;
-    float v[V][8];
+  // Adjacent rows go to adjacent groups: the rows in flight are one window of memory (equal
+  // shares of adjacent rows measured 5 to 15 % slower).
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group_index<G>(); row < a.rows; row += step) {
+    float v[V][8], s[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < V; ++i) load<8, kEven>(x, 8 * (lane + i * G), n, v[i]);
-    if (drop)
+    for (int i = 0; i < V; ++i) span.load(static_cast<const T*>(a.x) + row * a.xs, i, v[i]);
+    if (kJoin) {
+      Vec8<T> res[V];
+      if (a.res != nullptr)
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        drop8(v[i], philox(lane + i * G, static_cast<uint32_t>(row), offset, a.drop.seed), a.drop.threshold,
-              a.drop.scale);
-    if (a.res != nullptr) {
-      const T* res = static_cast<const T*>(a.res) + row * a.ress;
+        for (int i = 0; i < V; ++i) res[i] = span.fetch(static_cast<const T*>(a.res) + row * a.ress, i);
+      if (drop)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float t[8];
-        load<8, kEven>(res, 8 * (lane + i * G), n, t);
+        for (int i = 0; i < V; ++i) span.drop(v[i], i, row, offset, a.drop);
+      if (a.res != nullptr)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] += t[k];
-      }
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] += static_cast<float>(res[i][k]);
+      if (a.h != nullptr)
+#pragma unroll
+        for (int i = 0; i < V; ++i) span.store(static_cast<T*>(a.h) + row * a.hs, i, v[i]);
     }
-    if (a.h != nullptr) {
-      T* h = static_cast<T*>(a.h) + row * a.hs;
-#pragma unroll
-      for (int i = 0; i < V; ++i) store<8, kEven>(h, 8 * (lane + i * G), n, v[i]);
-    }
-    float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[0] += v[i][k];
-    group_sum<G>(s, lds, half);
-    const float mean = s[0] / static_cast<float>(n);   // exact for a constant row, unlike s * (1 / n)
+      for (int k = 0; k < 8; ++k) s[0] += span.counts(i, k) ? v[i][k] : 0.f;
+    group_sum<G, kRows>(s, lds, half);
+    const float mean = s[0] / static_cast<float>(a.cols);   // exact for a constant row, unlike s * (1 / n)
     s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         v[i][k] -= mean;
-        if ((kEven ? 8 * (lane + i * G) : 8 * (lane + i * G) + k) < n) s[0] = fmaf(v[i][k], v[i][k], s[0]);
+        const float c = span.counts(i, k) ? v[i][k] : 0.f;
+        s[0] = fmaf(c, c, s[0]);
       }
-    group_sum<G>(s, lds, half);
+    group_sum<G, kRows>(s, lds, half);
     const float rstd = 1.f / sqrtf(fmaf(s[0], inv_n, a.eps));
-    if (lane == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
-    }
-    T* y = static_cast<T*>(a.y) + row * a.ys;
+    if (a.mean != nullptr) a.mean[row] = mean;   // every thread of the group, the same bits
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[i][k] = fmaf(v[i][k] * rstd, w[i][k], b[i][k]);
-      store<8, kEven>(y, 8 * (lane + i * G), n, v[i]);
+      span.store(static_cast<T*>(a.y) + row * a.ys, i, v[i]);
     }
-  }
-}
-
-// Writes the gradient of one vector of columns, d + h_bar already added by the caller.
-template <class T, bool kEven>
-__device__ inline void store_bars(const NormBwdArgs& a, int64_t row, int c, float (&d)[8], bool drop, uint64_t offset) {
-  if (a.res_bar != nullptr) store<8, kEven>(static_cast<T*>(a.res_bar) + row * a.rbs, c, a.cols, d);
-  if (a.x_bar != nullptr) {
-    if (drop)
-      drop8(d, philox(c / 8, static_cast<uint32_t>(row), offset, a.drop.seed), a.drop.threshold, a.drop.scale);
-    store<8, kEven>(static_cast<T*>(a.x_bar) + row * a.xbs, c, a.cols, d);
   }
 }
 
 // What the backward pass reads of one row, a thread's share.
-template <class T, int G, int V, bool kEven>
+template <class T, int G, int V, bool kEven, bool kJoin>
 struct Operands {
-  Vec8<T> h[V], y_bar[V], h_bar[V];
+  Vec8<T> h[V], y_bar[V], h_bar[kJoin ? V : 1];
   float mean, rstd;
-  __device__ inline void read(const NormBwdArgs& a, int64_t row, int lane) {
+  __device__ inline void read(const NormBwdArgs& a, const Span<G, V, kEven>& span, int64_t row) {
+    if (kJoin && a.h_bar != nullptr)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = 8 * (lane + i * G);
-      h[i] = fetch<8, kEven>(static_cast<const T*>(a.h) + row * a.hs, c, a.cols);
-      y_bar[i] = fetch<8, kEven>(static_cast<const T*>(a.y_bar) + row * a.ybs, c, a.cols);
-      if (a.h_bar != nullptr) h_bar[i] = fetch<8, kEven>(static_cast<const T*>(a.h_bar) + row * a.hbs, c, a.cols);
-      else h_bar[i] = Vec8<T>{};
-    }
+      for (int i = 0; i < V; ++i) h_bar[i] = span.fetch(static_cast<const T*>(a.h_bar) + row * a.hbs, i);
     mean = a.mean[row];
     rstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      h[i] = span.fetch(static_cast<const T*>(a.h) + row * a.hs, i);
+      y_bar[i] = span.fetch(static_cast<const T*>(a.y_bar) + row * a.ybs, i);
+    }
   }
 };
 
@@ -145,69 +224,80 @@ struct Operands {
 // than more registers a thread (8192 x 4096 fp16: 512 threads of one vector 54.6 us, 256 of
 // two 81.4), the prefetch then gave 44.9.  Rows past 8192 columns need two vectors for 1024
 // threads, whose sums then live in LDS (each thread its own places).
-template <class T, int G, int V, bool kEven>
-__global__ __launch_bounds__(threads_of<G>()) void bwd_kernel(const NormBwdArgs a) {
-  constexpr int kRows = threads_of<G>() / G;
+template <class T, int G, int V, bool kEven, bool kJoin>
+__global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs a) {
+  constexpr int kRows = bwd_threads<G>() / G;
+  constexpr bool kBarrier = G > 64 && kRows > 1;   // rows that share a barrier take it together
   constexpr bool kLdsSums = V > 1, kAhead = V * sizeof(T) <= 4;   // two f32 vectors of the next row would spill
-  constexpr int kReduce = G > 64 ? 4 * G / 64 : 0;
+  constexpr int kReduce = G > 64 ? 4 * bwd_threads<G>() / 64 : 0;
   constexpr int kSums = kLdsSums ? 16 * V * G : kRows > 1 ? 16 * kThreads : 0;
   __shared__ float lds[kReduce + kSums];
   const int lane = threadIdx.x % G, group = threadIdx.x / G, n = a.cols;
+  const Span<G, V, kEven> span(lane, n);
   const float inv_n = 1.f / static_cast<float>(n);
-  const bool drop = a.drop.threshold != 0, grads = a.x_bar != nullptr || a.res_bar != nullptr;
+  const bool drop = kJoin && a.drop.threshold != 0, grads = a.x_bar != nullptr || (kJoin && a.res_bar != nullptr);
   const uint64_t offset = drop ? drop_offset(a.drop) : 0;
   int half = 0;
   float w[V][8], dw[kLdsSums ? 1 : V][8], db[kLdsSums ? 1 : V][8];
   float* own = lds + kReduce + threadIdx.x;   // with kLdsSums: sum k of vector i at own[(16 i + k) G]
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (a.w != nullptr) load<8, kEven>(a.w, 8 * (lane + i * G), n, w[i]);
+    span.load_or(a.w, i, 1.f, w[i]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (a.w == nullptr) w[i][k] = 1.f;
       if (kLdsSums) own[(16 * i + k) * G] = own[(16 * i + 8 + k) * G] = 0.f;
       else dw[i][k] = db[i][k] = 0.f;
     }
   }
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group_index<G>();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
-  Operands<T, G, V, kEven> next;
-  if (kAhead && row < a.rows) next.read(a, row, lane);
-  for (; row < a.rows; row += step) {
-    if (!kAhead) next.read(a, row, lane);
-    const Operands<T, G, V, kEven> now = next;
-    if (kAhead && row + step < a.rows) next.read(a, row + step, lane);
+  Operands<T, G, V, kEven, kJoin> next;
+  if (kAhead && row < a.rows) next.read(a, span, row);
+  for (; kBarrier ? row - group_index<G>() < a.rows : row < a.rows; row += step) {
+    if (kBarrier && row >= a.rows) {   // the last round may have a row for the first group only
+      float none[2] = {0.f, 0.f};
+      if (grads) group_sum<G, kRows>(none, lds, half);
+      continue;
+    }
+    if (!kAhead) next.read(a, span, row);
+    const Operands<T, G, V, kEven, kJoin> now = next;
+    if (kAhead) next.read(a, span, row + step < a.rows ? row + step : row);
     float v[V][8], g[V][8], s[2] = {0.f, 0.f};
-    // Columns past the row's end hold y_bar = 0, so they add nothing to any sum.
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      settle<8, kEven, T>(now.h[i], 8 * (lane + i * G), n, v[i]);
-      settle<8, kEven, T>(now.y_bar[i], 8 * (lane + i * G), n, g[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        v[i][k] = (v[i][k] - now.mean) * now.rstd;
+        const float y = static_cast<float>(now.y_bar[i][k]);
+        v[i][k] = (static_cast<float>(now.h[i][k]) - now.mean) * now.rstd;
         if (kLdsSums) {
-          own[(16 * i + k) * G] = fmaf(g[i][k], v[i][k], own[(16 * i + k) * G]);
-          own[(16 * i + 8 + k) * G] += g[i][k];
+          own[(16 * i + k) * G] = fmaf(y, v[i][k], own[(16 * i + k) * G]);
+          own[(16 * i + 8 + k) * G] += y;
         } else {
-          dw[i][k] = fmaf(g[i][k], v[i][k], dw[i][k]);
-          db[i][k] += g[i][k];
+          dw[i][k] = fmaf(y, v[i][k], dw[i][k]);
+          db[i][k] += y;
         }
-        g[i][k] *= w[i][k];
-        s[0] += g[i][k];
-        s[1] = fmaf(g[i][k], v[i][k], s[1]);
+        g[i][k] = y * w[i][k];
+        const float c = span.counts(i, k) ? g[i][k] : 0.f;
+        s[0] += c;
+        s[1] = fmaf(c, v[i][k], s[1]);
       }
     }
     if (!grads) continue;
-    group_sum<G>(s, lds, half);
+    group_sum<G, kRows>(s, lds, half);
     const float m0 = s[0] * inv_n, m1 = s[1] * inv_n;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float t[8];
-      settle<8, kEven, T>(now.h_bar[i], 8 * (lane + i * G), n, t);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) t[k] += now.rstd * (g[i][k] - fmaf(v[i][k], m1, m0));
-      store_bars<T, kEven>(a, row, 8 * (lane + i * G), t, drop, offset);
+      for (int k = 0; k < 8; ++k) {
+        t[k] = now.rstd * (g[i][k] - fmaf(v[i][k], m1, m0));
+        if (kJoin && a.h_bar != nullptr) t[k] += static_cast<float>(now.h_bar[i][k]);
+      }
+      if (kJoin) {
+        if (a.res_bar != nullptr) span.store(static_cast<T*>(a.res_bar) + row * a.rbs, i, t);
+        if (drop) span.drop(t, i, row, offset, a.drop);
+      }
+      if (!kJoin || a.x_bar != nullptr) span.store(static_cast<T*>(a.x_bar) + row * a.xbs, i, t);
     }
   }
   if (a.w_bar == nullptr && a.b_bar == nullptr) return;
@@ -223,8 +313,8 @@ __global__ __launch_bounds__(threads_of<G>()) void bwd_kernel(const NormBwdArgs 
           dw[0][k] = own[(16 * i + k) * G];
           db[0][k] = own[(16 * i + 8 + k) * G];
         }
-      if (wo != nullptr) store<8, kEven>(wo, 8 * (lane + i * G), n, dw[kLdsSums ? 0 : i]);
-      if (bo != nullptr) store<8, kEven>(bo, 8 * (lane + i * G), n, db[kLdsSums ? 0 : i]);
+      if (wo != nullptr) span.store(wo, i, dw[kLdsSums ? 0 : i]);
+      if (bo != nullptr) span.store(bo, i, db[kLdsSums ? 0 : i]);
     }
     return;
   }
@@ -235,12 +325,13 @@ __global__ __launch_bounds__(threads_of<G>()) void bwd_kernel(const NormBwdArgs 
   }
   __syncthreads();
   for (int j = threadIdx.x; j < 16 * G; j += kThreads) {
-    const int which = j / (8 * G), e = j % (8 * G), c = 8 * (e % G) + e / G;
+    const int which = j / (8 * G), e = j % (8 * G);
+    const Span<G, 1, kEven> of(e % G, n);
     float t = 0.f;
 #pragma unroll
     for (int q = 0; q < kRows; ++q) t += lds[kReduce + which * 8 * kThreads + q * 8 * G + e];
     float* out = which ? bo : wo;
-    if (c < n && out != nullptr) out[c] = t;
+    if (of.counts(0, e / G) && out != nullptr) out[of.at[0] + e / G] = t;
   }
 }
 
@@ -280,7 +371,7 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
       for (int k = 0; k < 8; ++k) t += v[k];
       s[0] += t;
     }
-    group_sum<kLong>(s, lds, half);
+    group_sum<kLong, 1>(s, lds, half);
     const float mean = s[0] / static_cast<float>(n);   // exact for a constant row, unlike s * (1 / n)
     s[0] = 0.f;
     for (int64_t c = 8 * threadIdx.x; c < n; c += 8 * kLong) {
@@ -291,7 +382,7 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
         if (c + k < n) t = fmaf(v[k] - mean, v[k] - mean, t);
       s[0] += t;
     }
-    group_sum<kLong>(s, lds, half);
+    group_sum<kLong, 1>(s, lds, half);
     const float rstd = 1.f / sqrtf(fmaf(s[0], inv_n, a.eps));
     if (threadIdx.x == 0) {
       if (a.mean != nullptr) a.mean[row] = mean;
@@ -308,6 +399,17 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
         v[k] = fmaf((v[k] - mean) * rstd, a.w != nullptr ? w[k] : 1.f, a.b != nullptr ? b[k] : 0.f);
       store<8, false>(static_cast<T*>(a.y) + row * a.ys, c, n, v);
     }
+  }
+}
+
+// Writes the gradient of one vector of columns.
+template <class T>
+__device__ inline void store_bars(const NormBwdArgs& a, int64_t row, int c, float (&d)[8], bool drop, uint64_t offset) {
+  if (a.res_bar != nullptr) store<8, false>(static_cast<T*>(a.res_bar) + row * a.rbs, c, a.cols, d);
+  if (a.x_bar != nullptr) {
+    if (drop)
+      drop8(d, philox(c / 8, static_cast<uint32_t>(row), offset, a.drop.seed), a.drop.threshold, a.drop.scale);
+    store<8, false>(static_cast<T*>(a.x_bar) + row * a.xbs, c, a.cols, d);
   }
 }
 
@@ -339,7 +441,7 @@ __global__ __launch_bounds__(kLong) void bwd_long_kernel(const NormBwdArgs a) {
       s[0] += t0;
       s[1] += t1;
     }
-    group_sum<kLong>(s, lds, half);
+    group_sum<kLong, 1>(s, lds, half);
     const float m0 = s[0] * inv_n, m1 = s[1] * inv_n;
     for (int64_t cc = 8 * threadIdx.x; cc < n; cc += 8 * kLong) {
       const int c = static_cast<int>(cc);
@@ -354,7 +456,7 @@ __global__ __launch_bounds__(kLong) void bwd_long_kernel(const NormBwdArgs a) {
         const float d = rstd * (g[k] - fmaf((v[k] - mean) * rstd, m1, m0));
         t[k] = a.h_bar != nullptr ? t[k] + d : d;
       }
-      store_bars<T, false>(a, row, c, t, drop, offset);
+      store_bars<T>(a, row, c, t, drop, offset);
     }
   }
 }
@@ -386,11 +488,36 @@ __global__ __launch_bounds__(kThreads) void bwd_long_cols_kernel(const NormBwdAr
 }
 
 // ---------------------------------------------------------------- launch shapes
-// Threads per row and vectors of eight columns per thread, from the row length alone: the
-// smallest group that holds the row, up to one wave with one vector; then more vectors
-// (rows to 2048 columns stay within one wave: no barrier), then several waves.
+// Threads per row and vectors of eight columns per thread, from the row length and the
+// element size: the smallest group that holds the row.
+template <int kSize, class F>
+auto fwd_shape(int32_t cols, F&& f) {
+  if (cols <= 8) return f.template operator()<1, 1>();
+  if (cols <= 16) return f.template operator()<2, 1>();
+  if (cols <= 32) return f.template operator()<4, 1>();
+  if (cols <= 64) return f.template operator()<8, 1>();
+  if constexpr (kSize == 2) {
+    if (cols <= 128) return f.template operator()<8, 2>();
+    if (cols <= 256) return f.template operator()<16, 2>();
+    if (cols <= 512) return f.template operator()<32, 2>();
+    if (cols <= 1024) return f.template operator()<64, 2>();
+    if (cols <= 2048) return f.template operator()<64, 4>();
+    if (cols <= 4096) return f.template operator()<128, 4>();
+    if (cols <= 8192) return f.template operator()<256, 4>();
+    return f.template operator()<512, 4>();
+  }
+  if (cols <= 128) return f.template operator()<16, 1>();
+  if (cols <= 256) return f.template operator()<32, 1>();
+  if (cols <= 512) return f.template operator()<64, 1>();
+  if (cols <= 1024) return f.template operator()<64, 2>();
+  if (cols <= 2048) return f.template operator()<128, 2>();
+  if (cols <= 4096) return f.template operator()<256, 2>();
+  if (cols <= 8192) return f.template operator()<512, 2>();
+  return f.template operator()<1024, 2>();
+}
+
 template <class F>
-auto by_cols_bwd(int32_t cols, F&& f) {
+auto bwd_shape(int32_t cols, F&& f) {
   if (cols <= 8) return f.template operator()<1, 1>();
   if (cols <= 16) return f.template operator()<2, 1>();
   if (cols <= 32) return f.template operator()<4, 1>();
@@ -405,70 +532,76 @@ auto by_cols_bwd(int32_t cols, F&& f) {
   return f.template operator()<1024, 2>();
 }
 
-template <class F>
-auto by_cols(int32_t cols, F&& f) {
-  if (cols <= 8) return f.template operator()<1, 1>();
-  if (cols <= 16) return f.template operator()<2, 1>();
-  if (cols <= 32) return f.template operator()<4, 1>();
-  if (cols <= 64) return f.template operator()<8, 1>();
-  if (cols <= 128) return f.template operator()<16, 1>();
-  if (cols <= 256) return f.template operator()<32, 1>();
-  if (cols <= 512) return f.template operator()<64, 1>();
-  if (cols <= 1024) return f.template operator()<64, 2>();
-  if (cols <= 2048) return f.template operator()<64, 4>();
-  if (cols <= 4096) return f.template operator()<256, 2>();
-  if (cols <= 8192) return f.template operator()<256, 4>();
-  return f.template operator()<512, 4>();
-}
+// Workgroups of the forward pass: 64 waves a CU, twice what fits, so that a CU whose rows
+// are done takes more (5 % over 32 at 64 MB in).
+constexpr int kFwdWaves = 64 * 256;
 
-constexpr int kFwdGroups = 2048;
-
-template <class T, bool kEven>
+template <class T, bool kEven, bool kJoin>
 struct LaunchFwd {
   const NormFwdArgs& a;
   hipStream_t s;
   template <int G, int V>
   hipError_t operator()() const {
-    constexpr int threads = threads_of<G>(), rows = threads / G;
-    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, kFwdGroups);
-    fwd_kernel<T, G, V, kEven><<<dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s>>>(a);
+    constexpr int threads = fwd_threads<G>(), rows = threads / G;
+    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, kFwdWaves / (threads / 64));
+    fwd_kernel<T, G, V, kEven, kJoin><<<dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
   }
 };
 
-template <class T, bool kEven>
+template <class T, bool kEven, bool kJoin>
 struct LaunchBwd {
   const NormBwdArgs& a;
   hipStream_t s;
   template <int G, int V>
   hipError_t operator()() const {
-    bwd_kernel<T, G, V, kEven><<<dim3(static_cast<unsigned>(norm_parts(a.rows, a.cols))), dim3(threads_of<G>()), 0, s>>>(a);
+    bwd_kernel<T, G, V, kEven, kJoin>
+        <<<dim3(static_cast<unsigned>(a.parts)), dim3(bwd_threads<G>()), 0, s>>>(a);
     return hipGetLastError();
   }
 };
 
+template <class T, bool kJoin>
+hipError_t reg_fwd(const NormFwdArgs& a, hipStream_t s) {
+  return a.cols % 8 == 0 ? fwd_shape<sizeof(T)>(a.cols, LaunchFwd<T, true, kJoin>{a, s})
+                         : fwd_shape<sizeof(T)>(a.cols, LaunchFwd<T, false, kJoin>{a, s});
+}
+inline bool bwd_join(const NormBwdArgs& a) {
+  return a.x_bar == nullptr || a.res_bar != nullptr || a.h_bar != nullptr || a.drop.threshold != 0;
+}
+
+template <class T, bool kJoin>
+hipError_t reg_bwd(const NormBwdArgs& a, hipStream_t s) {
+  return a.cols % 8 == 0 ? bwd_shape(a.cols, LaunchBwd<T, true, kJoin>{a, s})
+                         : bwd_shape(a.cols, LaunchBwd<T, false, kJoin>{a, s});
+}
+
+// The plain layer norm has kernels of its own: nothing in their loops depends on what the
+// caller left out.
 template <class T>
 hipError_t launch_fwd(const NormFwdArgs& a, hipStream_t s) {
-  if (a.cols <= kRegCols)
-    return a.cols % 8 == 0 ? by_cols(a.cols, LaunchFwd<T, true>{a, s}) : by_cols(a.cols, LaunchFwd<T, false>{a, s});
-  fwd_long_kernel<T><<<dim3(static_cast<unsigned>(std::min(a.rows, kFwdGroups))), dim3(kLong), 0, s>>>(a);
+  if (a.cols <= kRegCols) {
+    const bool join = a.res != nullptr || a.h != nullptr || a.drop.threshold != 0;
+    return join ? reg_fwd<T, true>(a, s) : reg_fwd<T, false>(a, s);
+  }
+  fwd_long_kernel<T><<<dim3(static_cast<unsigned>(std::min(a.rows, 2048))), dim3(kLong), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t s) {
-  if (a.cols <= kRegCols)
-    return a.cols % 8 == 0 ? by_cols_bwd(a.cols, LaunchBwd<T, true>{a, s})
-                           : by_cols_bwd(a.cols, LaunchBwd<T, false>{a, s});
+  if (a.cols <= kRegCols) {
+    return bwd_join(a) ? reg_bwd<T, true>(a, s) : reg_bwd<T, false>(a, s);
+  }
   if (a.x_bar != nullptr || a.res_bar != nullptr) {
-    bwd_long_kernel<T><<<dim3(static_cast<unsigned>(std::min(a.rows, kFwdGroups))), dim3(kLong), 0, s>>>(a);
+    bwd_long_kernel<T><<<dim3(static_cast<unsigned>(std::min(a.rows, 2048))), dim3(kLong), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.w_bar == nullptr && a.b_bar == nullptr) return hipSuccess;
   const int64_t vecs = (static_cast<int64_t>(a.cols) + 7) / 8;
   bwd_long_cols_kernel<T><<<dim3(static_cast<unsigned>((vecs + kThreads - 1) / kThreads),
-                                static_cast<unsigned>(norm_parts(a.rows, a.cols))),
+                                static_cast<unsigned>(a.parts)),
                            dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }

@@ -146,17 +146,17 @@ etpc_status norm_backward(int64_t rows, int64_t cols, int32_t dtype, const Mat& 
   if (mean == nullptr || rstd == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null mean or rstd");
   ETPC_TRY(check_apart({x_bar, res_bar}, {h, y_bar, h_bar}, rows, cols, dtype));
   a.rows = static_cast<int32_t>(rows), a.cols = static_cast<int32_t>(cols);
-  const int parts = norm_parts(a.rows, a.cols);
   const bool sums = w_bar != nullptr || b_bar != nullptr;
-  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, parts_bytes(parts, 2 * cols)));
+  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, parts_bytes(norm_parts_most(a.rows, a.cols), 2 * cols)));
   if (!sums && x_bar.p == nullptr && res_bar.p == nullptr) return ETPC_OK;
   a.h = h.p, a.y_bar = y_bar.p, a.h_bar = h_bar.p, a.mean = mean, a.rstd = rstd, a.w = w;
   a.x_bar = const_cast<void*>(x_bar.p), a.res_bar = const_cast<void*>(res_bar.p), a.w_bar = w_bar, a.b_bar = b_bar;
   a.part = static_cast<float*>(ws);
   a.hs = h.stride, a.ybs = y_bar.stride, a.hbs = h_bar.stride, a.xbs = x_bar.stride, a.rbs = res_bar.stride;
+  a.parts = norm_parts(a, dtype);
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_norm_bwd(a, dtype, s));
-  if (sums && parts > 1)
-    ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_parts_reduce(a.part, parts, a.cols, w_bar, b_bar, s));
+  if (sums && a.parts > 1)
+    ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_parts_reduce(a.part, a.parts, a.cols, w_bar, b_bar, s));
   return ETPC_OK;
 }
 
@@ -223,7 +223,7 @@ etpc_status etpc_layer_norm_workspace_size(int64_t n_rows, int64_t n_cols, size_
   if (bytes == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null output");
   ETPC_TRY(check_sizes(n_rows, n_cols, ETPC_F32));
   *bytes = n_rows > 0 && n_cols > 0
-               ? parts_bytes(norm_parts(static_cast<int32_t>(n_rows), static_cast<int32_t>(n_cols)), 2 * n_cols)
+               ? parts_bytes(norm_parts_most(static_cast<int32_t>(n_rows), static_cast<int32_t>(n_cols)), 2 * n_cols)
                : 0;
   return ETPC_OK;
 }

@@ -27,8 +27,8 @@ struct NormFwdArgs {
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, hipStream_t s);
 
 // d = h_bar + (gradient of <y_bar, y> with respect to h); res_bar = d, x_bar = dropout(d),
-// w_bar = sum_rows y_bar xhat, b_bar = sum_rows y_bar, the last two through `part`:
-// norm_parts(rows, cols) rows of [2][cols] floats (none needed when that is 1).
+// w_bar = sum_rows y_bar xhat, b_bar = sum_rows y_bar, the last two through `part`: `parts`
+// rows of [2][cols] floats (none needed when that is 1).
 struct NormBwdArgs {
   const void* h;
   const void* y_bar;
@@ -42,10 +42,13 @@ struct NormBwdArgs {
   float* b_bar;         // or null
   float* part;
   int64_t hs, ybs, hbs, xbs, rbs;
-  int32_t rows, cols;
+  int32_t rows, cols, parts;
   DropArgs drop;
 };
-int norm_parts(int32_t rows, int32_t cols);
+// Workgroups of the backward pass for these arguments (not yet in a.parts), and the most that
+// any element type and any of the optional operands give at this size.
+int norm_parts(const NormBwdArgs& a, int dtype);
+int norm_parts_most(int32_t rows, int32_t cols);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, hipStream_t s);
 
 // w_bar[c], b_bar[c] = sum_{p < parts} part[p][0][c], part[p][1][c] in a fixed order; a null

@@ -108,20 +108,20 @@ __device__ inline float lane_sum(float v) {
   return v;
 }
 
-// Sums of N values over a group of G threads: lanes of one wave (G <= 64), or the whole
-// workgroup of G threads through `lds` ([2][N][G / 64] floats, halves used in turn so one
-// barrier a call is enough).
-template <int G, int N>
+// Sums of N values over each group of G threads: lanes of one wave (G <= 64), or whole waves
+// of the workgroup through `lds` ([2][kGroups][N][G / 64] floats, halves used in turn so
+// one barrier a call is enough; every thread of the workgroup has to call).
+template <int G, int kGroups, int N>
 __device__ inline void group_sum(float (&v)[N], float* lds, int& half) {
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = lane_sum<(G < 64 ? G : 64)>(v[j]);
   if (G > 64) {
     constexpr int W = G / 64;
-    float* buf = lds + half * N * W;
+    float* buf = lds + (half * kGroups + (kGroups > 1 ? threadIdx.x / G : 0)) * N * W;
     half ^= 1;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int j = 0; j < N; ++j) buf[j * W + threadIdx.x / 64] = v[j];
+      for (int j = 0; j < N; ++j) buf[j * W + (kGroups > 1 ? threadIdx.x / 64 % W : threadIdx.x / 64)] = v[j];
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < N; ++j) {
