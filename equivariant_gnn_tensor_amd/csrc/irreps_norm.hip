@@ -46,15 +46,67 @@ __device__ inline float sum_lanes(float v, int g) {
   return v;
 }
 
-template <bool kEven>
-__device__ inline void load4_or(const float* __restrict__ p, int c, int n, float missing, float (&v)[4]) {
-  if (p != nullptr) {
-    load<4, kEven>(p, c, n, v);
-  } else {
+// Where a lane's vector i lies among the channels of a component.  A vector that would start
+// or end past the last channel is moved back to the last four: every access is one full
+// vector inside the segment, and what it holds and writes there is bit for bit what the
+// channels' owners hold and write.  Only sums tell the copies apart: element j counts from
+// `skip` on.  Blocks of fewer than four channels (one lane each) go by elements.
+template <int I, bool kEven>
+struct Span {
+  int mul, at[I], skip[I];
+  __device__ inline Span(int lane, int lanes, int channels) : mul(channels) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = missing;
+    for (int i = 0; i < I; ++i) {
+      const int c = 4 * (lane + i * lanes);
+      at[i] = tiny() ? 0 : min(c, mul - 4);
+      skip[i] = tiny() ? 4 * min(i, 1) : min(c - at[i], 4);
+    }
   }
-}
+  __device__ inline bool tiny() const { return !kEven && mul < 4; }
+  __device__ inline bool counts(int i, int j) const {
+    return kEven ? skip[i] == 0 : j >= skip[i] && j < mul;
+  }
+  // base is uniform, `offset` what the lane adds to it (floats)
+  __device__ inline void load(const float* __restrict__ base, uint32_t offset, int i, float (&v)[4]) const {
+    if (tiny()) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = j < mul ? base[offset + j] : 0.f;
+    } else {
+      __builtin_memcpy(v, base + (offset + static_cast<uint32_t>(at[i])), 16);
+    }
+  }
+  __device__ inline void load_or(const float* __restrict__ base, int i, float missing, float (&v)[4]) const {
+    if (base != nullptr) {
+      load(base, 0, i, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = missing;
+    }
+  }
+  __device__ inline void store(float* __restrict__ base, uint32_t offset, int i, const float (&v)[4]) const {
+    if (tiny()) {
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < mul) base[offset + j] = v[j];
+    } else {
+      __builtin_memcpy(base + (offset + static_cast<uint32_t>(at[i])), v, 16);
+    }
+  }
+};
+
+// A group's nodes: first + r step + group for the unrolled r.  Past the last node it reads
+// the last one again (and writes nothing).
+struct Node {
+  int64_t base;      // uniform: the workgroup's first node of this round
+  uint32_t offset;   // what the group adds to it
+  bool live;
+  __device__ inline Node(int64_t at, int group, int32_t rows) {
+    base = at < rows ? at : rows - 1;
+    const int64_t left = rows - 1 - base;
+    live = at < rows && group <= left;
+    offset = live ? group : static_cast<uint32_t>(left < group ? left : group);
+  }
+};
 
 struct FwdArgs {
   const float* x;
@@ -90,34 +142,37 @@ __device__ inline int groups_of(const IrrepTable& t, int k) { return (k + 1 < t.
 // D = 2l+1 components, I vectors of four channels a lane, R nodes in flight a group.
 template <int D, int I, int R, bool kEven>
 __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
-  const int mul = t.blk[k].mul, off = t.blk[k].off;
-  const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), per = kThreads / G;
+  const int mul = t.blk[k].mul;
+  const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), group = threadIdx.x / G, per = kThreads / G;
   const float inv_n = 1.f / static_cast<float>(D * mul);
+  const Span<I, kEven> span(lane, G, mul);
   float w[I][4], b[I][4];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    load4_or<kEven>(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
-    load4_or<kEven>(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, 4 * (lane + i * G), mul, 0.f, b[i]);
+    span.load_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, i, 1.f, w[i]);
+    span.load_or(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, i, 0.f, b[i]);
   }
   const int64_t step = static_cast<int64_t>(parts) * per;
-  for (int64_t first = static_cast<int64_t>(p) * per + threadIdx.x / G; first < a.rows; first += R * step) {
+  for (int64_t first = static_cast<int64_t>(p) * per; first < a.rows; first += R * step) {
     float v[R][D][I][4];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (first + r * step < a.rows)
+    for (int r = 0; r < R; ++r) {
+      const Node q(first + r * step, group, a.rows);
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+      for (int d = 0; d < D; ++d)
 #pragma unroll
-          for (int i = 0; i < I; ++i)
-            load<4, kEven>(a.x + (first + r * step) * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
+        for (int i = 0; i < I; ++i)
+          span.load(a.x + (q.base * t.dim + t.blk[k].off + d * mul), q.offset * t.dim, i, v[r][d][i]);
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t row = first + r * step;
-      if (row >= a.rows) break;
+      const Node q(first + r * step, group, a.rows);
       float s = 0.f, mean = 0.f;
       if (D == 1) {
 #pragma unroll
-        for (int i = 0; i < I; ++i) s += (v[r][0][i][0] + v[r][0][i][1]) + (v[r][0][i][2] + v[r][0][i][3]);
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s += span.counts(i, j) ? v[r][0][i][j] : 0.f;
         mean = sum_lanes(s, G) / static_cast<float>(mul);   // exact for a constant row
         s = 0.f;
       }
@@ -126,17 +181,17 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (D == 1) {
-              v[r][d][i][j] -= mean;
-              if ((kEven ? 4 * (lane + i * G) : 4 * (lane + i * G) + j) < mul) s = fmaf(v[r][d][i][j], v[r][d][i][j], s);
-            } else {
-              s = fmaf(v[r][d][i][j], v[r][d][i][j], s);   // channels past the last hold 0
-            }
+          for (int j = 0; j < 4; ++j) {
+            if (D == 1) v[r][d][i][j] -= mean;
+            const float c = span.counts(i, j) ? v[r][d][i][j] : 0.f;
+            s = fmaf(c, c, s);
+          }
       const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, G), inv_n, a.eps));
-      if (lane == 0 && a.stats != nullptr) {
-        a.stats[2 * (row * t.n + k)] = mean;
-        a.stats[2 * (row * t.n + k) + 1] = rstd;
+      if (!q.live) continue;
+      if (a.stats != nullptr) {   // every lane of the group, the same bits
+        float* st = a.stats + 2 * (q.base * t.n + k);
+        st[2 * q.offset * t.n] = mean;
+        st[2 * q.offset * t.n + 1] = rstd;
       }
 #pragma unroll
       for (int d = 0; d < D; ++d)
@@ -145,14 +200,22 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
           float o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = fmaf(v[r][d][i][j] * rstd, w[i][j], b[i][j]);
-          store<4, kEven>(a.y + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
+          span.store(a.y + (q.base * t.dim + t.blk[k].off + d * mul), q.offset * t.dim, i, o);
         }
     }
   }
 }
 
+__device__ inline void load4_or(const float* __restrict__ p, int c, int n, float missing, float (&v)[4]) {
+  if (p != nullptr) {
+    load<4, false>(p, c, n, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = missing;
+  }
+}
+
 // Segments of more channels: a wave reads its segment once for each sum and once for y.
-template <bool kEven>
 __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
   const int mul = t.blk[k].mul, n = (2 * t.blk[k].l + 1) * mul, lane = threadIdx.x & 63;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -165,7 +228,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     if (n == mul) {
       for (int e = 4 * lane; e < n; e += 256) {
         float v[4];
-        load<4, kEven>(x, e, n, v);
+        load<4, false>(x, e, n, v);
         s += (v[0] + v[1]) + (v[2] + v[3]);
       }
       mean = sum_lanes(s, 64) / static_cast<float>(n);
@@ -173,7 +236,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     }
     for (int e = 4 * lane; e < n; e += 256) {
       float v[4];
-      load<4, kEven>(x, e, n, v);
+      load<4, false>(x, e, n, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (e + j < n) s = fmaf(v[j] - mean, v[j] - mean, s);
@@ -186,12 +249,12 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     for (int d = 0; d * mul < n; ++d)
       for (int c = 4 * lane; c < mul; c += 256) {
         float v[4], g[4], h[4];
-        load<4, kEven>(x + d * mul, c, mul, v);
-        load4_or<kEven>(w, c, mul, 1.f, g);
-        load4_or<kEven>(b, c, mul, 0.f, h);
+        load<4, false>(x + d * mul, c, mul, v);
+        load4_or(w, c, mul, 1.f, g);
+        load4_or(b, c, mul, 0.f, h);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], h[j]);
-        store<4, kEven>(a.y + row * t.dim + t.blk[k].off + d * mul, c, mul, v);
+        store<4, false>(a.y + row * t.dim + t.blk[k].off + d * mul, c, mul, v);
       }
   }
 }
@@ -199,7 +262,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
 template <int I, bool kEven>
 __global__ __launch_bounds__(kThreads) void irreps_norm_fwd_kernel(const IrrepTable t, const FwdArgs a) {
   const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
-  if (I == 2 && t.blk[k].mul > kRegMul) return fwd_long<kEven>(t, k, p, parts, a);
+  if (I == 2 && t.blk[k].mul > kRegMul) return fwd_long(t, k, p, parts, a);
   if (l == 0) fwd_block<1, I, 4, kEven>(t, k, p, parts, a);
   else if (l == 1) fwd_block<3, I, 2, kEven>(t, k, p, parts, a);
   else if (l == 2) fwd_block<5, I, 1, kEven>(t, k, p, parts, a);
@@ -222,37 +285,35 @@ __device__ inline void sum_outputs(const IrrepTable& t, int k, int p, const BwdA
 // nodes; lanes, then waves are added at the end in a fixed order.
 template <int D, int I, int R, bool kEven>
 __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a, float* lds) {
-  const int mul = t.blk[k].mul, off = t.blk[k].off;
-  const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), per = kThreads / G;
+  const int mul = t.blk[k].mul;
+  const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), group = threadIdx.x / G, per = kThreads / G;
   const float inv_n = 1.f / static_cast<float>(D * mul);
+  const Span<I, kEven> span(lane, G, mul);
   float w[I][4], dw[I][4] = {}, db[I][4] = {};
 #pragma unroll
-  for (int i = 0; i < I; ++i)
-    load4_or<kEven>(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, 4 * (lane + i * G), mul, 1.f, w[i]);
+  for (int i = 0; i < I; ++i) span.load_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, i, 1.f, w[i]);
   const int64_t step = static_cast<int64_t>(parts) * per;
-  for (int64_t first = static_cast<int64_t>(p) * per + threadIdx.x / G; first < a.rows; first += R * step) {
+  for (int64_t first = static_cast<int64_t>(p) * per; first < a.rows; first += R * step) {
     float v[R][D][I][4], g[R][D][I][4], mean[R], rstd[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t row = first + r * step;
-      if (row < a.rows) {
+      const Node q(first + r * step, group, a.rows);
+      const float* st = a.stats + 2 * (q.base * t.n + k);
+      mean[r] = D == 1 ? st[2 * q.offset * t.n] : 0.f;
+      rstd[r] = st[2 * q.offset * t.n + 1];
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+      for (int d = 0; d < D; ++d)
 #pragma unroll
-          for (int i = 0; i < I; ++i) {
-            load<4, kEven>(a.x + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, v[r][d][i]);
-            load<4, kEven>(a.y_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, g[r][d][i]);
-          }
-        mean[r] = D == 1 ? a.stats[2 * (row * t.n + k)] : 0.f;
-        rstd[r] = a.stats[2 * (row * t.n + k) + 1];
-      }
+        for (int i = 0; i < I; ++i) {
+          const int64_t base = q.base * t.dim + t.blk[k].off + d * mul;
+          span.load(a.x + base, q.offset * t.dim, i, v[r][d][i]);
+          span.load(a.y_bar + base, q.offset * t.dim, i, g[r][d][i]);
+        }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t row = first + r * step;
-      if (row >= a.rows) break;
+      const Node q(first + r * step, group, a.rows);
       float s0 = 0.f, s1 = 0.f;
-      // channels past the last hold y_bar = 0 and add nothing
 #pragma unroll
       for (int d = 0; d < D; ++d)
 #pragma unroll
@@ -261,15 +322,19 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
           for (int j = 0; j < 4; ++j) {
             float& x = v[r][d][i][j];
             float& y = g[r][d][i][j];
-            x = (x - mean[r]) * rstd[r];
-            dw[i][j] = fmaf(y, x, dw[i][j]);
-            if (D == 1) db[i][j] += y;
+            x = (D == 1 ? x - mean[r] : x) * rstd[r];
+            if (q.live) {
+              dw[i][j] = fmaf(y, x, dw[i][j]);
+              if (D == 1) db[i][j] += y;
+            }
             y *= w[i][j];
-            if (D == 1) s0 += y;
-            s1 = fmaf(y, x, s1);
+            const float c = span.counts(i, j) ? y : 0.f;
+            if (D == 1) s0 += c;
+            s1 = fmaf(c, x, s1);
           }
       if (a.x_bar == nullptr) continue;
       const float m0 = D == 1 ? sum_lanes(s0, G) * inv_n : 0.f, m1 = sum_lanes(s1, G) * inv_n;
+      if (!q.live) continue;
 #pragma unroll
       for (int d = 0; d < D; ++d)
 #pragma unroll
@@ -277,7 +342,7 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
           float o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = rstd[r] * (g[r][d][i][j] - fmaf(v[r][d][i][j], m1, m0));
-          store<4, kEven>(a.x_bar + row * t.dim + off + d * mul, 4 * (lane + i * G), mul, o);
+          span.store(a.x_bar + (q.base * t.dim + t.blk[k].off + d * mul), q.offset * t.dim, i, o);
         }
     }
   }
@@ -290,8 +355,9 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
         dw[i][j] += __shfl_xor(dw[i][j], o);
         if (D == 1) db[i][j] += __shfl_xor(db[i][j], o);
       }
-      const int c = 4 * (lane + i * G) + j, wave = threadIdx.x / 64;
-      if ((threadIdx.x & 63) < static_cast<unsigned>(G) && c < mul) {
+      const int wave = threadIdx.x / 64;
+      if ((threadIdx.x & 63) < static_cast<unsigned>(G) && span.counts(i, j)) {
+        const int c = span.at[i] + j;
         lds[wave * kRegMul + c] = dw[i][j];
         if (D == 1) lds[(kWaves + wave) * kRegMul + c] = db[i][j];
       }
@@ -312,7 +378,6 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
   }
 }
 
-template <bool kEven>
 __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a) {
   const int mul = t.blk[k].mul, n = (2 * t.blk[k].l + 1) * mul, lane = threadIdx.x & 63;
   const float inv_n = 1.f / static_cast<float>(n);
@@ -325,9 +390,9 @@ __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, co
     for (int d = 0; d * mul < n; ++d)
       for (int c = 4 * lane; c < mul; c += 256) {
         float v[4], y[4], g[4];
-        load<4, kEven>(a.x + at + d * mul, c, mul, v);
-        load<4, kEven>(a.y_bar + at + d * mul, c, mul, y);
-        load4_or<kEven>(w, c, mul, 1.f, g);
+        load<4, false>(a.x + at + d * mul, c, mul, v);
+        load<4, false>(a.y_bar + at + d * mul, c, mul, y);
+        load4_or(w, c, mul, 1.f, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           s0 = fmaf(y[j], g[j], s0);
@@ -338,12 +403,12 @@ __device__ inline void bwd_long(const IrrepTable& t, int k, int p, int parts, co
     for (int d = 0; d * mul < n; ++d)
       for (int c = 4 * lane; c < mul; c += 256) {
         float v[4], y[4], g[4];
-        load<4, kEven>(a.x + at + d * mul, c, mul, v);
-        load<4, kEven>(a.y_bar + at + d * mul, c, mul, y);
-        load4_or<kEven>(w, c, mul, 1.f, g);
+        load<4, false>(a.x + at + d * mul, c, mul, v);
+        load<4, false>(a.y_bar + at + d * mul, c, mul, y);
+        load4_or(w, c, mul, 1.f, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = rstd * (fmaf(y[j], g[j], -m0) - (v[j] - mean) * rstd * m1);
-        store<4, kEven>(a.x_bar + at + d * mul, c, mul, v);
+        store<4, false>(a.x_bar + at + d * mul, c, mul, v);
       }
   }
   if (a.w_bar == nullptr && a.b_bar == nullptr) return;
@@ -369,7 +434,7 @@ template <int I, bool kEven>
 __global__ __launch_bounds__(kThreads) void irreps_norm_bwd_kernel(const IrrepTable t, const BwdArgs a) {
   __shared__ float lds[2 * kWaves * kRegMul];
   const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
-  if (I == 2 && t.blk[k].mul > kRegMul) return bwd_long<kEven>(t, k, p, parts, a);
+  if (I == 2 && t.blk[k].mul > kRegMul) return bwd_long(t, k, p, parts, a);
   if (l == 0) bwd_block<1, I, 4, kEven>(t, k, p, parts, a, lds);
   else if (l == 1) bwd_block<3, I, 2, kEven>(t, k, p, parts, a, lds);
   else if (l == 2) bwd_block<5, I, 1, kEven>(t, k, p, parts, a, lds);
@@ -377,23 +442,22 @@ __global__ __launch_bounds__(kThreads) void irreps_norm_bwd_kernel(const IrrepTa
 }
 
 // Second stage of the sums: a workgroup takes 16 adjacent columns of one block (gains, then
-// biases), 16 slices of its rows of `part` in order each, then the slices in order.
-constexpr int kCols = 16, kSlices = kThreads / kCols;
+// biases), 64 slices of its rows of `part` in order each (eight loads in flight), then the
+// slices in order.
+constexpr int kCols = 16, kSlices = 64;
 
-__global__ __launch_bounds__(kThreads) void irreps_parts_kernel(const IrrepTable t, const BwdArgs a) {
+__global__ __launch_bounds__(kCols* kSlices) void irreps_parts_kernel(const IrrepTable t, const BwdArgs a) {
   __shared__ float lds[kSlices][kCols];
   const IrrepBlock& q = t.blk[blockIdx.y];
   const int width = q.bias >= 0 ? 2 * q.mul : q.mul, parts = groups_of(t, blockIdx.y);
   const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
   const int c = blockIdx.x * kCols + lane;
-  float s = 0.f;
-  if (c < width)
-    for (int p = slice; p < parts; p += kSlices) s += a.part[q.part + static_cast<int64_t>(p) * width + c];
-  lds[slice][lane] = s;
+  lds[slice][lane] = c < width ? sum_slice<kSlices>(a.part + q.part + c, width, slice, parts) : 0.f;
   __syncthreads();
   if (slice != 0 || c >= width) return;
-#pragma unroll
-  for (int i = 1; i < kSlices; ++i) s += lds[i][lane];
+  float s = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < kSlices; ++i) s += lds[i][lane];
   if (c < q.mul) {
     if (a.w_bar != nullptr) a.w_bar[q.ch + c] = s;
   } else if (a.b_bar != nullptr) {
@@ -401,30 +465,39 @@ __global__ __launch_bounds__(kThreads) void irreps_parts_kernel(const IrrepTable
   }
 }
 
-// The kernel for a table: blocks past 256 channels take two vectors a lane, and only
-// channel counts that are no multiple of four need the code for ends inside a vector.
-template <class K>
-K pick(const IrrepTable& t, K narrow, K narrow_ragged, K wide, K wide_ragged) {
-  bool even = true, is_wide = false;
-  for (int k = 0; k < t.n; ++k) {
-    even = even && t.blk[k].mul % 4 == 0;
-    is_wide = is_wide || t.blk[k].mul > 256;
-  }
-  return is_wide ? (even ? wide : wide_ragged) : (even ? narrow : narrow_ragged);
+// Blocks past 256 channels take two vectors a lane, and only channel counts that are no
+// multiple of four need the code for ends inside a vector.
+bool is_wide(const IrrepTable& t) {
+  return std::any_of(t.blk, t.blk + t.n, [](const IrrepBlock& b) { return b.mul > 256; });
+}
+bool is_even(const IrrepTable& t) {
+  return std::all_of(t.blk, t.blk + t.n, [](const IrrepBlock& b) { return b.mul % 4 == 0; });
 }
 
 }  // namespace
 
-// Deals about `total` workgroups to the blocks by width, at least one each and no more than
-// its nodes fill, and lays out the rows of partial sums; returns the floats these need.
+// Workgroups, resident all at once.  Fewer than fit measured best where a row is 4096 bytes
+// (65408 nodes of 64x0e+64x1o+64x2e+64x3o: forward 116 us with 1024, 129 with 1536, 134 with
+// 2048; backward 163 with 512, 168 with 768, 183 with 896, 179 with 1024); other rows differ
+// by a few per cent between these.
+constexpr int kFwdGroups = 1024, kBwdGroups = 768, kBwdGroupsWide = 512;
+
+// Nodes a group has in flight, by degree.
+constexpr int kInFlight[kMaxL + 1] = {4, 2, 1, 1};
+
+// Deals about `total` workgroups to the blocks so that all blocks walk the nodes at one pace:
+// the rows in flight are one window of memory.  At least one workgroup each and no more than
+// the nodes fill.  Lays out the rows of partial sums too; returns the floats these need.
 int64_t irreps_deal(IrrepTable& t, int32_t rows, int total) {
+  double weight = 0.0;
+  for (int k = 0; k < t.n; ++k) weight += static_cast<double>(lanes_of(t.blk[k].mul)) / kInFlight[t.blk[k].l];
   int64_t floats = 0;
   t.groups = 0;
   for (int k = 0; k < t.n; ++k) {
     IrrepBlock& q = t.blk[k];
-    const int per = kThreads / lanes_of(q.mul);
+    const int lanes = lanes_of(q.mul), per = kThreads / lanes;
     const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per;
-    const int64_t share = (static_cast<int64_t>(total) * (2 * q.l + 1) * q.mul + t.dim - 1) / t.dim;
+    const int64_t share = static_cast<int64_t>(total * lanes / (kInFlight[q.l] * weight) + 0.5);
     const int64_t parts = std::max<int64_t>(1, std::min(need, share));
     q.wg = t.groups;
     q.part = floats;
@@ -436,31 +509,32 @@ int64_t irreps_deal(IrrepTable& t, int32_t rows, int total) {
 
 hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w, const float* b, float eps, float* y,
                                   float* stats, int32_t rows, hipStream_t s) {
-  irreps_deal(t, rows, 2048);
+  irreps_deal(t, rows, kFwdGroups);
   const FwdArgs a{x, w, b, y, stats, eps, rows};
-  const auto kernel = pick(t, irreps_norm_fwd_kernel<1, true>, irreps_norm_fwd_kernel<1, false>,
-                           irreps_norm_fwd_kernel<2, true>, irreps_norm_fwd_kernel<2, false>);
+  const auto kernel = is_wide(t) ? (is_even(t) ? irreps_norm_fwd_kernel<2, true> : irreps_norm_fwd_kernel<2, false>)
+                                 : (is_even(t) ? irreps_norm_fwd_kernel<1, true> : irreps_norm_fwd_kernel<1, false>);
   kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   return hipGetLastError();
 }
 
-// Four workgroups a CU.
-int64_t irreps_norm_part_floats(IrrepTable& t, int32_t rows) { return irreps_deal(t, rows, 1024); }
+int64_t irreps_norm_part_floats(IrrepTable& t, int32_t rows) {
+  return irreps_deal(t, rows, is_wide(t) ? kBwdGroupsWide : kBwdGroups);
+}
 
 hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_bar, const float* stats,
                                   const float* w, float* x_bar, float* w_bar, float* b_bar, float* part, int32_t rows,
                                   hipStream_t s) {
   const bool whole = irreps_norm_part_floats(t, rows) == 0;
   const BwdArgs a{x, y_bar, stats, w, x_bar, w_bar, b_bar, part, rows, whole};
-  const auto kernel = pick(t, irreps_norm_bwd_kernel<1, true>, irreps_norm_bwd_kernel<1, false>,
-                           irreps_norm_bwd_kernel<2, true>, irreps_norm_bwd_kernel<2, false>);
+  const auto kernel = is_wide(t) ? (is_even(t) ? irreps_norm_bwd_kernel<2, true> : irreps_norm_bwd_kernel<2, false>)
+                                 : (is_even(t) ? irreps_norm_bwd_kernel<1, true> : irreps_norm_bwd_kernel<1, false>);
   kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole || (w_bar == nullptr && b_bar == nullptr)) return e;
   int64_t most = 0;
   for (int k = 0; k < t.n; ++k) most = std::max<int64_t>(most, int64_t{t.blk[k].bias >= 0 ? 2 : 1} * t.blk[k].mul);
   irreps_parts_kernel<<<dim3(static_cast<unsigned>((most + kCols - 1) / kCols), static_cast<unsigned>(t.n)),
-                        dim3(kThreads), 0, s>>>(t, a);
+                        dim3(kCols * kSlices), 0, s>>>(t, a);
   return hipGetLastError();
 }
 

@@ -14,23 +14,12 @@ __global__ __launch_bounds__(kCols* kSlices) void parts_reduce_kernel(const floa
   __shared__ float lds[kSlices][kCols];
   const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kCols + lane;
-  float s = 0.f;
-  if (c < total) {
-    int p = slice;
-    for (; p + 7 * kSlices < parts; p += 8 * kSlices) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = part[static_cast<int64_t>(p + i * kSlices) * total + c];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
-    }
-    for (; p < parts; p += kSlices) s += part[p * total + c];
-  }
-  lds[slice][lane] = s;
+  lds[slice][lane] = c < total ? sum_slice<kSlices>(part + c, total, slice, parts) : 0.f;
   __syncthreads();
   if (slice != 0 || c >= total) return;
+  float s = 0.f;
 #pragma unroll 8
-  for (int q = 1; q < kSlices; ++q) s += lds[q][lane];
+  for (int q = 0; q < kSlices; ++q) s += lds[q][lane];
   if (c < cols) {
     if (w_bar != nullptr) w_bar[c] = s;
   } else if (b_bar != nullptr) {

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxCols = int64_t{1} << 30;
+constexpr int64_t kMaxDim = int64_t{1} << 20;
 
 struct Mat {
   const char* name;
@@ -178,7 +179,8 @@ etpc_status make_table(int32_t n, const etpc_irrep* irreps, IrrepTable* t) {
     channels += ir.mul;
     biases += bias ? ir.mul : 0;
     groups += (ir.mul + int64_t{7}) / 8;
-    if (dim > kMaxCols) ETPC_FAIL(ETPC_ERR_OVERFLOW, "feature rows must be at most 2^30 wide");
+    // a workgroup's 256 rows are addressed by 32-bit byte offsets
+    if (dim > kMaxDim) ETPC_FAIL(ETPC_ERR_OVERFLOW, "feature rows must be at most 2^20 wide");
   }
   t->dim = static_cast<int32_t>(dim);
   t->channels = static_cast<int32_t>(channels);

@@ -133,4 +133,22 @@ __device__ inline void group_sum(float (&v)[N], float* lds, int& half) {
   }
 }
 
+// p[slice width] + p[(slice + kSlices) width] + ... over the first `parts` rows, in order, with
+// eight loads in flight.
+template <int kSlices>
+__device__ inline float sum_slice(const float* __restrict__ p, int64_t width, int slice, int parts) {
+  float s = 0.f;
+  int q = slice;
+  for (; q + 7 * kSlices < parts; q += 8 * kSlices) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[(q + i * kSlices) * width];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
+  }
+#pragma unroll 4
+  for (; q < parts; q += kSlices) s += p[q * width];
+  return s;
+}
+
 }  // namespace etpc

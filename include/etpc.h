@@ -394,7 +394,7 @@ etpc_status etpc_dropout_add_layer_norm_backward(int64_t n_rows, int64_t n_cols,
                                                  size_t ws_bytes, hipStream_t stream);
 
 /* Irreps features: contiguous fp32 ir_mul rows, x[n_nodes][dim], given by their blocks
- * irreps[n_blocks] (host; at most 64, mul >= 1, l <= 3, parity +-1).
+ * irreps[n_blocks] (host; at most 64, mul >= 1, l <= 3, parity +-1; dim <= 2^20).
  * dim = sum mul (2l+1); channels = sum mul (one gain each); biases = channels of the 0e
  * blocks.  Output pointers may be NULL. */
 etpc_status etpc_irreps_dims(int32_t n_blocks, const etpc_irrep* irreps, int64_t* dim, int64_t* channels,
