@@ -4,6 +4,11 @@
 // is generated where it is used and never stored, and the gradient applies the same mask
 // again (the map is diagonal, hence its own adjoint).  One generator call serves eight
 // columns with 16 bits each, so a thread takes eight columns.
+//
+// Memory bound at the rate of a large copy: 65408 x 1024 bf16 in 47 us, 5.7 TB/s.  Sixteen bits
+// a column are what makes it so: a call is twenty 32 x 32 -> 64 bit products, each of which
+// takes four cycles of a lane, about as long for eight bf16 columns as their 32 bytes.
+// p is rounded to a multiple of 2^-16 and the scale belongs to the rounded p.
 #include <algorithm>
 
 #include "nodewise.hpp"

@@ -14,8 +14,9 @@
 // Memory bound: each operand is read once and each result written once.  A group of lanes
 // owns a segment: lane j holds channels 4 j .. 4 j + 3 with all their components, so a
 // gain, a bias and the gradients' sums are four registers a lane whatever the degree, and
-// 64 channels fill 16 lanes exactly at every degree.  Workgroups are dealt to the blocks in
-// proportion to the blocks' widths, so that all have about the same bytes to move.
+// 64 channels fill 16 lanes exactly at every degree (against lanes that span the segment:
+// backward of 65408 nodes of 64x0e+64x1o+64x2e 233 us -> 107).  That case reaches 90 us now,
+// 5.0 TB/s, sums included; forward 50 us, 6.0 TB/s.
 #include <algorithm>
 
 #include "nodewise.hpp"

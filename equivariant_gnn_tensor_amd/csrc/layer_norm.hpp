@@ -128,9 +128,10 @@ __device__ inline int group_index() {
   return G >= 64 ? __builtin_amdgcn_readfirstlane(group) : group;
 }
 
-// One vector a thread was measured against two and four (forward pass, 64 MB in): 16-bit
-// rows need 32 to 64 bytes a thread in flight to reach the copy rate, 32-bit rows 32 to 64
-// too, which is half the vectors.
+// Read and write one row after another, no prefetch: waves enough are in flight, and fetching
+// a row ahead measured slower (65536 x 512 bf16 24.8 us without, 28 to 30 with).
+// What it reaches (reads and writes): 65536 x 512 bf16 21.9 us, 6.1 TB/s; 8192 x 2048 fp32
+// 22.9 us, 5.9 TB/s; join 65408 x 1024 bf16 98.6 us, 5.4 TB/s, the rate of a large copy.
 template <class T, int G, int V, bool kEven, bool kJoin>
 __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs a) {
   constexpr int kRows = fwd_threads<G>() / G;
@@ -224,6 +225,9 @@ struct Operands {
 // than more registers a thread (8192 x 4096 fp16: 512 threads of one vector 54.6 us, 256 of
 // two 81.4), the prefetch then gave 44.9.  Rows past 8192 columns need two vectors for 1024
 // threads, whose sums then live in LDS (each thread its own places).
+// What it reaches, sums included: 8192 x 4096 fp16 41.3 us, 4.9 TB/s; 65536 x 512 bf16
+// 37.6 us, 5.4 TB/s; join 65408 x 1024 bf16 133 us, 5.0 TB/s.  bf16 rows that start at an
+// odd element are read a third slower (32768 x 2047: 103 us against 80).
 template <class T, int G, int V, bool kEven, bool kJoin>
 __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs a) {
   constexpr int kRows = bwd_threads<G>() / G;
@@ -489,7 +493,9 @@ __global__ __launch_bounds__(kThreads) void bwd_long_cols_kernel(const NormBwdAr
 
 // ---------------------------------------------------------------- launch shapes
 // Threads per row and vectors of eight columns per thread, from the row length and the
-// element size: the smallest group that holds the row.
+// element size: the smallest group that holds the row.  Forward, a thread wants 32 to 64
+// bytes in flight: two to four vectors of 16-bit rows (16384 x 2048 bf16: 22.3 us with four,
+// 28 to 30 with one), one or two of fp32 rows (8192 x 2048: 22.9 us with two, 27.3 with four).
 template <int kSize, class F>
 auto fwd_shape(int32_t cols, F&& f) {
   if (cols <= 8) return f.template operator()<1, 1>();
@@ -532,9 +538,14 @@ auto bwd_shape(int32_t cols, F&& f) {
   return f.template operator()<1024, 2>();
 }
 
-// Workgroups of the forward pass: 64 waves a CU, twice what fits, so that a CU whose rows
-// are done takes more (5 % over 32 at 64 MB in).
-constexpr int kFwdWaves = 64 * 256;
+// Workgroups of the forward pass by waves a CU: 64, twice what fits, so that a CU whose rows
+// are done takes more (16384 x 1024 fp32: 24.0 us with 32, 22.0 with 64); 32 where a wave
+// holds eight rows or more and loading gains and biases again costs more (100000 x 64 fp32:
+// 9.9 us with 32, 10.7 with 64).
+template <int G>
+constexpr int fwd_waves() {
+  return 256 * (G <= 8 ? 32 : 64);
+}
 
 template <class T, bool kEven, bool kJoin>
 struct LaunchFwd {
@@ -543,7 +554,7 @@ struct LaunchFwd {
   template <int G, int V>
   hipError_t operator()() const {
     constexpr int threads = fwd_threads<G>(), rows = threads / G;
-    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, kFwdWaves / (threads / 64));
+    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, fwd_waves<G>() / (threads / 64));
     fwd_kernel<T, G, V, kEven, kJoin><<<dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
   }
