@@ -588,11 +588,15 @@ def _row_type(x: torch.Tensor) -> int:
     return t
 
 
-def _check_device(name: str, t: torch.Tensor):
+def _check_device(name: str, t: torch.Tensor, stream) -> int:
+    """The stream handle of a call on t (the current stream of the current device, on which t
+    has to be, or the caller's)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if t.get_device() != torch.cuda.current_device():
+    index = t.get_device()
+    if index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
 def _rows(name: str, t: torch.Tensor) -> Tuple[int, int, int, int]:
@@ -611,6 +615,8 @@ def _rows(name: str, t: torch.Tensor) -> Tuple[int, int, int, int]:
     strides = t.stride()
     if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
+    if len(shape) == 2:   # one row may have any stride
+        return t.data_ptr(), strides[0] if shape[0] > 1 else cols, shape[0], cols
     rows, stride = 1, cols
     for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
@@ -644,7 +650,9 @@ def _vector(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[in
         raise ValueError(f"{name} must hold {n} numbers, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return _ptr(t)
+    if t.dtype is not torch.float32 or not t.is_contiguous():
+        return _ptr(t)   # raises
+    return t.data_ptr()
 
 
 def _new(shape, device, stream) -> torch.Tensor:
@@ -678,14 +686,14 @@ def etpc_dropout(x, p: float, seed: int, offset=0, y=None, stream=None) -> torch
     """y = x with elements dropped with probability p and the rest scaled by 1 / (1 - p), over
     the rows x [..., C]; y may be x.  The gradient is the same call on y_bar."""
     dtype = _row_type(x)
-    _check_device("x", x)
+    handle = _check_device("x", x, stream)
     xp, xs, rows, cols = _rows("x", x)
     if y is None:
         y = _new_like(x, stream)
         yp, ys = y.data_ptr(), cols
     else:
         yp, ys = _rows_like("y", y, x)
-    st = lib.etpc_dropout(rows, cols, dtype, xp, xs, _drop_spec(p, seed, offset, x.device), yp, ys, _stream(stream))
+    st = lib.etpc_dropout(rows, cols, dtype, xp, xs, _drop_spec(p, seed, offset, x.device), yp, ys, handle)
     if st:
         _check(st)
     return y
@@ -693,7 +701,7 @@ def etpc_dropout(x, p: float, seed: int, offset=0, y=None, stream=None) -> torch
 
 def _norm_forward(x, residual, drop, w, b, eps, y, h, join, stats, mean, rstd, stream):
     dtype, dev = _row_type(x), x.device
-    _check_device("x", x)
+    handle = _check_device("x", x, stream)
     xp, xs, rows, cols = _rows("x", x)
     if y is None:
         y = _new_like(x, stream)
@@ -719,9 +727,9 @@ def _norm_forward(x, residual, drop, w, b, eps, y, h, join, stats, mean, rstd, s
         else:
             hp, hs = _rows_like("h", h, x)
         st = lib.etpc_dropout_add_layer_norm(rows, cols, dtype, xp, xs, rp, rs, drop, wp, bp, eps, yp, ys, hp, hs, mp,
-                                             sp, _stream(stream))
+                                             sp, handle)
     else:
-        st = lib.etpc_layer_norm(rows, cols, dtype, xp, xs, wp, bp, eps, yp, ys, mp, sp, _stream(stream))
+        st = lib.etpc_layer_norm(rows, cols, dtype, xp, xs, wp, bp, eps, yp, ys, mp, sp, handle)
     if st:
         _check(st)
     return y, h, mean, rstd
@@ -739,6 +747,11 @@ def etpc_layer_norm_workspace_size(n_rows: int, n_cols: int) -> int:
     b = C.c_size_t()
     _check(lib.etpc_layer_norm_workspace_size(n_rows, n_cols, b))
     return b.value
+
+
+@functools.lru_cache(maxsize=512)
+def _norm_ws(n_rows: int, n_cols: int) -> int:
+    return etpc_layer_norm_workspace_size(n_rows, n_cols)
 
 
 def _scratch(ws, nbytes: int, device, stream):
@@ -777,17 +790,17 @@ def etpc_layer_norm_backward(x, y_bar, mean, rstd, w=None, want=("x", "w", "b"),
     """(x_bar, w_bar, b_bar) of <y_bar, y>; None for what `want` leaves out.  outs: three
     caller-given tensors (or None to skip one)."""
     dtype, dev = _row_type(x), x.device
-    _check_device("x", x)
+    handle = _check_device("x", x, stream)
     xp, xs, rows, cols = _rows("x", x)
     yp, ys = _rows_like("y_bar", y_bar, x)
     mp, sp, wp = _vector("mean", mean, rows, dev), _vector("rstd", rstd, rows, dev), _vector("w", w, cols, dev)
     x_bar, xbp, xbs = _bar_like("x_bar", want, "x", outs, 0, x, cols, stream)
     w_bar, wbp = _bar_vector("w_bar", want, "w", outs, 1, cols, dev, stream)
     b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 2, cols, dev, stream)
-    need = etpc_layer_norm_workspace_size(rows, cols) if wbp is not None or bbp is not None else 0
+    need = _norm_ws(rows, cols) if wbp is not None or bbp is not None else 0
     wsp, wsn, _keep = _scratch(ws, need, dev, stream)
     st = lib.etpc_layer_norm_backward(rows, cols, dtype, xp, xs, yp, ys, mp, sp, wp, xbp, xbs, wbp, bbp, wsp, wsn,
-                                      _stream(stream))
+                                      handle)
     if st:
         _check(st)
     return x_bar, w_bar, b_bar
@@ -806,7 +819,7 @@ def etpc_dropout_add_layer_norm_backward(h, y_bar, mean, rstd, w=None, h_bar=Non
     """(x_bar, residual_bar, w_bar, b_bar) of <y_bar, y> + <h_bar, h>; None for what `want`
     leaves out.  p, seed and offset as in the forward call."""
     dtype, dev = _row_type(h), h.device
-    _check_device("h", h)
+    handle = _check_device("h", h, stream)
     hp, hs, rows, cols = _rows("h", h)
     yp, ys = _rows_like("y_bar", y_bar, h)
     bp, bs = _rows_like("h_bar", h_bar, h)
@@ -815,11 +828,11 @@ def etpc_dropout_add_layer_norm_backward(h, y_bar, mean, rstd, w=None, h_bar=Non
     r_bar, rbp, rbs = _bar_like("residual_bar", want, "residual", outs, 1, h, cols, stream)
     w_bar, wbp = _bar_vector("w_bar", want, "w", outs, 2, cols, dev, stream)
     b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 3, cols, dev, stream)
-    need = etpc_layer_norm_workspace_size(rows, cols) if wbp is not None or bbp is not None else 0
+    need = _norm_ws(rows, cols) if wbp is not None or bbp is not None else 0
     wsp, wsn, _keep = _scratch(ws, need, dev, stream)
     st = lib.etpc_dropout_add_layer_norm_backward(rows, cols, dtype, hp, hs, yp, ys, bp, bs, mp, sp, wp,
                                                   _drop_spec(p, seed, offset, dev), xbp, xbs, rbp, rbs, wbp, bbp, wsp,
-                                                  wsn, _stream(stream))
+                                                  wsn, handle)
     if st:
         _check(st)
     return x_bar, r_bar, w_bar, b_bar
@@ -858,9 +871,7 @@ def _features(name, t, ir: _Irreps, like=None) -> Optional[int]:
     shape = t.shape
     if len(shape) != 2 or shape[1] != ir.dim:
         raise ValueError(f"{name} must have shape (n_nodes, {ir.dim}), got {tuple(shape)}")
-    if like is None:
-        _check_device(name, t)
-    elif shape != like.shape or t.device != like.device:
+    if like is not None and (shape != like.shape or t.device != like.device):
         raise ValueError(f"{name} must have shape {tuple(like.shape)} on {like.device}, got {tuple(shape)} on {t.device}")
     return _ptr(t)
 
@@ -869,13 +880,13 @@ def etpc_irreps_dropout(irreps, x, p: float, seed: int, offset=0, y=None, stream
     """Dropout of whole channels of ir_mul features x [N, dim]: the components of a (node,
     channel) share their mask, so rotations commute with it; y may be x."""
     ir = _irreps(irreps)
-    xp = _features("x", x, ir)
+    xp, handle = _features("x", x, ir), _check_device("x", x, stream)
     if y is None:
         y = _new_like(x, stream)
         yp = y.data_ptr()
     else:
         yp = _features("y", y, ir, x)
-    st = lib.etpc_irreps_dropout(ir.n, ir.c, x.shape[0], xp, _drop_spec(p, seed, offset, x.device), yp, _stream(stream))
+    st = lib.etpc_irreps_dropout(ir.n, ir.c, x.shape[0], xp, _drop_spec(p, seed, offset, x.device), yp, handle)
     if st:
         _check(st)
     return y
@@ -887,7 +898,7 @@ def etpc_irreps_norm(irreps, x, w=None, b=None, eps: float = 1e-5, y=None, stats
     reflections.  w: one gain per channel; b: one bias per 0e channel; stats [N, blocks, 2]
     holds (mean, rstd) for the backward pass (None with keep_stats=False)."""
     ir, dev = _irreps(irreps), x.device
-    xp = _features("x", x, ir)
+    xp, handle = _features("x", x, ir), _check_device("x", x, stream)
     n = x.shape[0]
     if y is None:
         y = _new_like(x, stream)
@@ -900,14 +911,19 @@ def etpc_irreps_norm(irreps, x, w=None, b=None, eps: float = 1e-5, y=None, stats
     else:
         sp = _vector("stats", stats, 2 * n * ir.n, dev)
     st = lib.etpc_irreps_norm(ir.n, ir.c, n, xp, _vector("w", w, ir.channels, dev), _vector("b", b, ir.biases, dev), eps,
-                              yp, sp, _stream(stream))
+                              yp, sp, handle)
     if st:
         _check(st)
     return y, stats
 
 
 def etpc_irreps_norm_workspace_size(irreps, n_nodes: int) -> int:
-    ir, b = _irreps(irreps), C.c_size_t()
+    return _irreps_ws(_irreps(irreps), n_nodes)
+
+
+@functools.lru_cache(maxsize=512)
+def _irreps_ws(ir: _Irreps, n_nodes: int) -> int:
+    b = C.c_size_t()
     _check(lib.etpc_irreps_norm_workspace_size(ir.n, ir.c, n_nodes, b))
     return b.value
 
@@ -916,6 +932,7 @@ def etpc_irreps_norm_backward(irreps, x, y_bar, stats, w=None, want=("x", "w", "
     """(x_bar, w_bar, b_bar) of <y_bar, y>; None for what `want` leaves out."""
     ir, dev = _irreps(irreps), x.device
     xp, yp = _features("x", x, ir), _features("y_bar", y_bar, ir, x)
+    handle = _check_device("x", x, stream)
     n = x.shape[0]
     if outs is not None:
         x_bar, xbp = outs[0], _features("x_bar", outs[0], ir, x)
@@ -926,10 +943,10 @@ def etpc_irreps_norm_backward(irreps, x, y_bar, stats, w=None, want=("x", "w", "
         x_bar = xbp = None
     w_bar, wbp = _bar_vector("w_bar", want, "w", outs, 1, ir.channels, dev, stream)
     b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 2, ir.biases, dev, stream)
-    need = etpc_irreps_norm_workspace_size(irreps, n) if wbp is not None or bbp is not None else 0
+    need = _irreps_ws(ir, n) if wbp is not None or bbp is not None else 0
     wsp, wsn, _keep = _scratch(ws, need, dev, stream)
     st = lib.etpc_irreps_norm_backward(ir.n, ir.c, n, xp, yp, _vector("stats", stats, 2 * n * ir.n, dev),
-                                       _vector("w", w, ir.channels, dev), xbp, wbp, bbp, wsp, wsn, _stream(stream))
+                                       _vector("w", w, ir.channels, dev), xbp, wbp, bbp, wsp, wsn, handle)
     if st:
         _check(st)
     return x_bar, w_bar, b_bar
