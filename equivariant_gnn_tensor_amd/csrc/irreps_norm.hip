@@ -36,6 +36,19 @@ __host__ __device__ inline int lanes_of(int mul) {
   return g;
 }
 
+// Narrow blocks are read flat: lanes span the whole segment, four adjacent numbers each, and
+// the components of a channel meet only in the gradients' sums at the end.  Channel by
+// channel, lanes would read runs shorter than a cache line.  Below 24 channels backward
+// (27542 nodes of 192x0e+8x2e+53x0e+32x1e+8x3o+6x1e 64 us -> 42; 36350 of 10x2o+48x3o+16x1e
+// 62 -> 49, with 16 the bound 57), below 16 forward (25985 nodes of 88x0o+8x3o+8x1o+24x3o+
+// 24x2o+88x0e 37.7 -> 32.8, 60000 of 16x0e+16x1o+16x2e 14.7, with 24 the bound 16.8).
+constexpr int kFwdFlat = 16, kBwdFlat = 24;
+__host__ __device__ inline bool is_flat(const IrrepBlock& b, int below) { return b.l == 0 || b.mul < below; }
+// What the lanes of a group span: numbers of the segment, or channels.
+__host__ __device__ inline int span_of(const IrrepBlock& b, int below) {
+  return is_flat(b, below) ? (2 * b.l + 1) * b.mul : b.mul;
+}
+
 // The sum over aligned groups of g lanes, g uniform in the workgroup.
 __device__ inline float sum_lanes(float v, int g) {
   if (g >= 2) v += dpp_f<0xB1>(v);
@@ -140,19 +153,34 @@ __device__ inline int block_of(const IrrepTable& t, int wg) {
 }
 __device__ inline int groups_of(const IrrepTable& t, int k) { return (k + 1 < t.n ? t.blk[k + 1].wg : t.groups) - t.blk[k].wg; }
 
-// D = 2l+1 components, I vectors of four channels a lane, R nodes in flight a group.
+// The gains (or biases) of a lane's numbers: channel of number e of a flat segment = e mod C.
+template <int D, int I, bool kEven>
+__device__ inline void channel_values(const float* p, const Span<I, kEven>& span, const IrrepBlock& b, float missing,
+                                      float (&v)[I][4]) {
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    if (D > 1 || b.l == 0) {
+      span.load_or(p, i, missing, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[i][j] = p != nullptr && span.at[i] + j < span.mul ? p[(span.at[i] + j) % b.mul] : missing;
+    }
+  }
+}
+
+// D components of I vectors a lane (D = 1: a flat segment, of any degree), R nodes in flight a
+// group.
 template <int D, int I, int R, bool kEven>
 __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, const FwdArgs& a) {
-  const int mul = t.blk[k].mul;
+  const int mul = span_of(t.blk[k], kFwdFlat);
+  const bool center = t.blk[k].l == 0;
   const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), group = threadIdx.x / G, per = kThreads / G;
   const float inv_n = 1.f / static_cast<float>(D * mul);
   const Span<I, kEven> span(lane, G, mul);
   float w[I][4], b[I][4];
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-    span.load_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, i, 1.f, w[i]);
-    span.load_or(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, i, 0.f, b[i]);
-  }
+  channel_values<D>(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, span, t.blk[k], 1.f, w);
+  channel_values<D>(a.b != nullptr && t.blk[k].bias >= 0 ? a.b + t.blk[k].bias : nullptr, span, t.blk[k], 0.f, b);
   const int64_t step = static_cast<int64_t>(parts) * per;
   for (int64_t first = static_cast<int64_t>(p) * per; first < a.rows; first += R * step) {
     float v[R][D][I][4];
@@ -169,7 +197,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
     for (int r = 0; r < R; ++r) {
       const Node q(first + r * step, group, a.rows);
       float s = 0.f, mean = 0.f;
-      if (D == 1) {
+      if (D == 1 && center) {
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
@@ -264,7 +292,7 @@ template <int I, bool kEven>
 __global__ __launch_bounds__(kThreads) void irreps_norm_fwd_kernel(const IrrepTable t, const FwdArgs a) {
   const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
   if (I == 2 && t.blk[k].mul > kRegMul) return fwd_long(t, k, p, parts, a);
-  if (l == 0) fwd_block<1, I, 4, kEven>(t, k, p, parts, a);
+  if (is_flat(t.blk[k], kFwdFlat)) fwd_block<1, I, 4, kEven>(t, k, p, parts, a);
   else if (l == 1) fwd_block<3, I, 2, kEven>(t, k, p, parts, a);
   else if (l == 2) fwd_block<5, I, 1, kEven>(t, k, p, parts, a);
   else fwd_block<7, I, 1, kEven>(t, k, p, parts, a);
@@ -286,13 +314,13 @@ __device__ inline void sum_outputs(const IrrepTable& t, int k, int p, const BwdA
 // nodes; lanes, then waves are added at the end in a fixed order.
 template <int D, int I, int R, bool kEven>
 __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, const BwdArgs& a, float* lds) {
-  const int mul = t.blk[k].mul;
+  const int mul = span_of(t.blk[k], kBwdFlat), channels = t.blk[k].mul;
+  const bool center = t.blk[k].l == 0;
   const int G = lanes_of(mul), lane = threadIdx.x & (G - 1), group = threadIdx.x / G, per = kThreads / G;
   const float inv_n = 1.f / static_cast<float>(D * mul);
   const Span<I, kEven> span(lane, G, mul);
   float w[I][4], dw[I][4] = {}, db[I][4] = {};
-#pragma unroll
-  for (int i = 0; i < I; ++i) span.load_or(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, i, 1.f, w[i]);
+  channel_values<D>(a.w != nullptr ? a.w + t.blk[k].ch : nullptr, span, t.blk[k], 1.f, w);
   const int64_t step = static_cast<int64_t>(parts) * per;
   for (int64_t first = static_cast<int64_t>(p) * per; first < a.rows; first += R * step) {
     float v[R][D][I][4], g[R][D][I][4], mean[R], rstd[R];
@@ -300,7 +328,7 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
     for (int r = 0; r < R; ++r) {
       const Node q(first + r * step, group, a.rows);
       const float* st = a.stats + 2 * (q.base * t.n + k);
-      mean[r] = D == 1 ? st[2 * q.offset * t.n] : 0.f;
+      mean[r] = D == 1 && center ? st[2 * q.offset * t.n] : 0.f;
       rstd[r] = st[2 * q.offset * t.n + 1];
 #pragma unroll
       for (int d = 0; d < D; ++d)
@@ -334,7 +362,7 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
             s1 = fmaf(c, x, s1);
           }
       if (a.x_bar == nullptr) continue;
-      const float m0 = D == 1 ? sum_lanes(s0, G) * inv_n : 0.f, m1 = sum_lanes(s1, G) * inv_n;
+      const float m0 = D == 1 && center ? sum_lanes(s0, G) * inv_n : 0.f, m1 = sum_lanes(s1, G) * inv_n;
       if (!q.live) continue;
 #pragma unroll
       for (int d = 0; d < D; ++d)
@@ -366,10 +394,11 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
   __syncthreads();
   float *wo, *bo;
   sum_outputs(t, k, p, a, &wo, &bo);
-  for (int c = threadIdx.x; c < mul; c += kThreads) {
-    float sw = lds[c], sb = 0.f;
+  for (int c = threadIdx.x; c < channels; c += kThreads) {
+    float sw = 0.f, sb = 0.f;
+    for (int e = c; e < mul; e += channels)   // the components of a flat segment
 #pragma unroll
-    for (int q = 1; q < kWaves; ++q) sw += lds[q * kRegMul + c];
+      for (int q = 0; q < kWaves; ++q) sw += lds[q * kRegMul + e];
     if (wo != nullptr) wo[c] = sw;
     if (D == 1 && bo != nullptr) {
 #pragma unroll
@@ -436,7 +465,7 @@ __global__ __launch_bounds__(kThreads) void irreps_norm_bwd_kernel(const IrrepTa
   __shared__ float lds[2 * kWaves * kRegMul];
   const int k = block_of(t, blockIdx.x), p = blockIdx.x - t.blk[k].wg, parts = groups_of(t, k), l = t.blk[k].l;
   if (I == 2 && t.blk[k].mul > kRegMul) return bwd_long(t, k, p, parts, a);
-  if (l == 0) bwd_block<1, I, 4, kEven>(t, k, p, parts, a, lds);
+  if (is_flat(t.blk[k], kBwdFlat)) bwd_block<1, I, 4, kEven>(t, k, p, parts, a, lds);
   else if (l == 1) bwd_block<3, I, 2, kEven>(t, k, p, parts, a, lds);
   else if (l == 2) bwd_block<5, I, 1, kEven>(t, k, p, parts, a, lds);
   else bwd_block<7, I, 1, kEven>(t, k, p, parts, a, lds);
@@ -471,8 +500,8 @@ __global__ __launch_bounds__(kCols* kSlices) void irreps_parts_kernel(const Irre
 bool is_wide(const IrrepTable& t) {
   return std::any_of(t.blk, t.blk + t.n, [](const IrrepBlock& b) { return b.mul > 256; });
 }
-bool is_even(const IrrepTable& t) {
-  return std::all_of(t.blk, t.blk + t.n, [](const IrrepBlock& b) { return b.mul % 4 == 0; });
+bool is_even(const IrrepTable& t, int below) {
+  return std::all_of(t.blk, t.blk + t.n, [below](const IrrepBlock& b) { return span_of(b, below) % 4 == 0; });
 }
 
 }  // namespace
@@ -483,22 +512,23 @@ bool is_even(const IrrepTable& t) {
 // by a few per cent between these.
 constexpr int kFwdGroups = 1024, kBwdGroups = 768, kBwdGroupsWide = 512;
 
-// Nodes a group has in flight, by degree.
-constexpr int kInFlight[kMaxL + 1] = {4, 2, 1, 1};
+// Nodes a group has in flight.
+int in_flight(const IrrepBlock& b, int below) { return is_flat(b, below) ? 4 : b.l == 1 ? 2 : 1; }
 
 // Deals about `total` workgroups to the blocks so that all blocks walk the nodes at one pace:
 // the rows in flight are one window of memory.  At least one workgroup each and no more than
 // the nodes fill.  Lays out the rows of partial sums too; returns the floats these need.
-int64_t irreps_deal(IrrepTable& t, int32_t rows, int total) {
+int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below) {
   double weight = 0.0;
-  for (int k = 0; k < t.n; ++k) weight += static_cast<double>(lanes_of(t.blk[k].mul)) / kInFlight[t.blk[k].l];
+  for (int k = 0; k < t.n; ++k)
+    weight += static_cast<double>(lanes_of(span_of(t.blk[k], below))) / in_flight(t.blk[k], below);
   int64_t floats = 0;
   t.groups = 0;
   for (int k = 0; k < t.n; ++k) {
     IrrepBlock& q = t.blk[k];
-    const int lanes = lanes_of(q.mul), per = kThreads / lanes;
+    const int lanes = lanes_of(span_of(q, below)), per = kThreads / lanes;
     const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per;
-    const int64_t share = static_cast<int64_t>(total * lanes / (kInFlight[q.l] * weight) + 0.5);
+    const int64_t share = static_cast<int64_t>(total * lanes / (in_flight(q, below) * weight) + 0.5);
     const int64_t parts = std::max<int64_t>(1, std::min(need, share));
     q.wg = t.groups;
     q.part = floats;
@@ -510,16 +540,16 @@ int64_t irreps_deal(IrrepTable& t, int32_t rows, int total) {
 
 hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w, const float* b, float eps, float* y,
                                   float* stats, int32_t rows, hipStream_t s) {
-  irreps_deal(t, rows, kFwdGroups);
+  irreps_deal(t, rows, kFwdGroups, kFwdFlat);
   const FwdArgs a{x, w, b, y, stats, eps, rows};
-  const auto kernel = is_wide(t) ? (is_even(t) ? irreps_norm_fwd_kernel<2, true> : irreps_norm_fwd_kernel<2, false>)
-                                 : (is_even(t) ? irreps_norm_fwd_kernel<1, true> : irreps_norm_fwd_kernel<1, false>);
+  const auto kernel = is_wide(t) ? (is_even(t, kFwdFlat) ? irreps_norm_fwd_kernel<2, true> : irreps_norm_fwd_kernel<2, false>)
+                                 : (is_even(t, kFwdFlat) ? irreps_norm_fwd_kernel<1, true> : irreps_norm_fwd_kernel<1, false>);
   kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   return hipGetLastError();
 }
 
 int64_t irreps_norm_part_floats(IrrepTable& t, int32_t rows) {
-  return irreps_deal(t, rows, is_wide(t) ? kBwdGroupsWide : kBwdGroups);
+  return irreps_deal(t, rows, is_wide(t) ? kBwdGroupsWide : kBwdGroups, kBwdFlat);
 }
 
 hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_bar, const float* stats,
@@ -527,8 +557,8 @@ hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_
                                   hipStream_t s) {
   const bool whole = irreps_norm_part_floats(t, rows) == 0;
   const BwdArgs a{x, y_bar, stats, w, x_bar, w_bar, b_bar, part, rows, whole};
-  const auto kernel = is_wide(t) ? (is_even(t) ? irreps_norm_bwd_kernel<2, true> : irreps_norm_bwd_kernel<2, false>)
-                                 : (is_even(t) ? irreps_norm_bwd_kernel<1, true> : irreps_norm_bwd_kernel<1, false>);
+  const auto kernel = is_wide(t) ? (is_even(t, kBwdFlat) ? irreps_norm_bwd_kernel<2, true> : irreps_norm_bwd_kernel<2, false>)
+                                 : (is_even(t, kBwdFlat) ? irreps_norm_bwd_kernel<1, true> : irreps_norm_bwd_kernel<1, false>);
   kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole || (w_bar == nullptr && b_bar == nullptr)) return e;
