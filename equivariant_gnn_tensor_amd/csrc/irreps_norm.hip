@@ -15,8 +15,8 @@
 // owns a segment: lane j holds channels 4 j .. 4 j + 3 with all their components, so a
 // gain, a bias and the gradients' sums are four registers a lane whatever the degree, and
 // 64 channels fill 16 lanes exactly at every degree (against lanes that span the segment:
-// backward of 65408 nodes of 64x0e+64x1o+64x2e 233 us -> 107).  That case reaches 90 us now,
-// 5.0 TB/s, sums included; forward 50 us, 6.0 TB/s.
+// backward of 65408 nodes of 64x0e+64x1o+64x2e 233 us -> 107).  That case reaches 91 us now,
+// 5.0 TB/s, sums included; forward 60 us, 5.0 TB/s.  A large copy runs at 5.1 to 5.4.
 #include <algorithm>
 
 #include "nodewise.hpp"
@@ -517,8 +517,10 @@ int in_flight(const IrrepBlock& b, int below) { return is_flat(b, below) ? 4 : b
 
 // Deals about `total` workgroups to the blocks so that all blocks walk the nodes at one pace:
 // the rows in flight are one window of memory.  At least one workgroup each and no more than
-// the nodes fill.  Lays out the rows of partial sums too; returns the floats these need.
-int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below) {
+// the nodes fill; one_round: one where a single round of loads takes every node (the backward
+// pass then often needs no second stage: 64 nodes of 8x0e+8x1o 7.8 us -> 5.3).  Lays out the
+// rows of partial sums too; returns the floats these need.
+int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below, bool one_round) {
   double weight = 0.0;
   for (int k = 0; k < t.n; ++k)
     weight += static_cast<double>(lanes_of(span_of(t.blk[k], below))) / in_flight(t.blk[k], below);
@@ -527,7 +529,8 @@ int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below) {
   for (int k = 0; k < t.n; ++k) {
     IrrepBlock& q = t.blk[k];
     const int lanes = lanes_of(span_of(q, below)), per = kThreads / lanes;
-    const int64_t need = (static_cast<int64_t>(rows) + per - 1) / per;
+    const bool one = one_round && static_cast<int64_t>(per) * in_flight(q, below) >= rows;
+    const int64_t need = one ? 1 : (static_cast<int64_t>(rows) + per - 1) / per;
     const int64_t share = static_cast<int64_t>(total * lanes / (in_flight(q, below) * weight) + 0.5);
     const int64_t parts = std::max<int64_t>(1, std::min(need, share));
     q.wg = t.groups;
@@ -540,7 +543,7 @@ int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below) {
 
 hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w, const float* b, float eps, float* y,
                                   float* stats, int32_t rows, hipStream_t s) {
-  irreps_deal(t, rows, kFwdGroups, kFwdFlat);
+  irreps_deal(t, rows, kFwdGroups, kFwdFlat, false);
   const FwdArgs a{x, w, b, y, stats, eps, rows};
   const auto kernel = is_wide(t) ? (is_even(t, kFwdFlat) ? irreps_norm_fwd_kernel<2, true> : irreps_norm_fwd_kernel<2, false>)
                                  : (is_even(t, kFwdFlat) ? irreps_norm_fwd_kernel<1, true> : irreps_norm_fwd_kernel<1, false>);
@@ -549,7 +552,7 @@ hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w,
 }
 
 int64_t irreps_norm_part_floats(IrrepTable& t, int32_t rows) {
-  return irreps_deal(t, rows, is_wide(t) ? kBwdGroupsWide : kBwdGroups, kBwdFlat);
+  return irreps_deal(t, rows, is_wide(t) ? kBwdGroupsWide : kBwdGroups, kBwdFlat, true);
 }
 
 hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_bar, const float* stats,

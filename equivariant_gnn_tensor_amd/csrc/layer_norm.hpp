@@ -130,8 +130,8 @@ __device__ inline int group_index() {
 
 // Read and write one row after another, no prefetch: waves enough are in flight, and fetching
 // a row ahead measured slower (65536 x 512 bf16 24.8 us without, 28 to 30 with).
-// What it reaches (reads and writes): 65536 x 512 bf16 21.9 us, 6.1 TB/s; 8192 x 2048 fp32
-// 22.9 us, 5.9 TB/s; join 65408 x 1024 bf16 98.6 us, 5.4 TB/s, the rate of a large copy.
+// What it reaches (reads and writes): 65536 x 512 bf16 23.0 us, 5.9 TB/s; 8192 x 2048 fp32
+// 26.1 us, 5.1 TB/s; join 65408 x 1024 bf16 98.8 us, 5.4 TB/s.  A large copy runs at 5.1 to 5.4.
 template <class T, int G, int V, bool kEven, bool kJoin>
 __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs a) {
   constexpr int kRows = fwd_threads<G>() / G;
@@ -225,9 +225,9 @@ struct Operands {
 // than more registers a thread (8192 x 4096 fp16: 512 threads of one vector 54.6 us, 256 of
 // two 81.4), the prefetch then gave 44.9.  Rows past 8192 columns need two vectors for 1024
 // threads, whose sums then live in LDS (each thread its own places).
-// What it reaches, sums included: 8192 x 4096 fp16 41.3 us, 4.9 TB/s; 65536 x 512 bf16
-// 37.6 us, 5.4 TB/s; join 65408 x 1024 bf16 133 us, 5.0 TB/s.  bf16 rows that start at an
-// odd element are read a third slower (32768 x 2047: 103 us against 80).
+// What it reaches, sums included: 8192 x 4096 fp16 43.4 us, 4.6 TB/s; 65536 x 512 bf16
+// 40.5 us, 5.0 TB/s; join 65408 x 1024 bf16 133 us, 5.0 TB/s.  bf16 rows that start at an
+// odd element are read a third slower (32768 x 2047: 103 us against 81 for 2048).
 template <class T, int G, int V, bool kEven, bool kJoin>
 __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs a) {
   constexpr int kRows = bwd_threads<G>() / G;
@@ -493,9 +493,10 @@ __global__ __launch_bounds__(kThreads) void bwd_long_cols_kernel(const NormBwdAr
 
 // ---------------------------------------------------------------- launch shapes
 // Threads per row and vectors of eight columns per thread, from the row length and the
-// element size: the smallest group that holds the row.  Forward, a thread wants 32 to 64
-// bytes in flight: two to four vectors of 16-bit rows (16384 x 2048 bf16: 22.3 us with four,
-// 28 to 30 with one), one or two of fp32 rows (8192 x 2048: 22.9 us with two, 27.3 with four).
+// element size: the smallest group that holds the row.  Forward, 16-bit rows past 64 columns
+// take two vectors a thread (32768 x 1024 bf16: 23 us with two, 28 to 32 with one; 8192 x
+// 4096 fp16: 27.5 us with two, 32.3 with four), fp32 rows past 512 (8192 x 2048: 22.9 us with
+// two, 27.3 with four; one and two are level, two halves the waves at a barrier).
 template <int kSize, class F>
 auto fwd_shape(int32_t cols, F&& f) {
   if (cols <= 8) return f.template operator()<1, 1>();
@@ -507,10 +508,10 @@ auto fwd_shape(int32_t cols, F&& f) {
     if (cols <= 256) return f.template operator()<16, 2>();
     if (cols <= 512) return f.template operator()<32, 2>();
     if (cols <= 1024) return f.template operator()<64, 2>();
-    if (cols <= 2048) return f.template operator()<64, 4>();
-    if (cols <= 4096) return f.template operator()<128, 4>();
-    if (cols <= 8192) return f.template operator()<256, 4>();
-    return f.template operator()<512, 4>();
+    if (cols <= 2048) return f.template operator()<128, 2>();
+    if (cols <= 4096) return f.template operator()<256, 2>();
+    if (cols <= 8192) return f.template operator()<512, 2>();
+    return f.template operator()<1024, 2>();
   }
   if (cols <= 128) return f.template operator()<16, 1>();
   if (cols <= 256) return f.template operator()<32, 1>();
@@ -538,13 +539,14 @@ auto bwd_shape(int32_t cols, F&& f) {
   return f.template operator()<1024, 2>();
 }
 
-// Workgroups of the forward pass by waves a CU: 64, twice what fits, so that a CU whose rows
-// are done takes more (16384 x 1024 fp32: 24.0 us with 32, 22.0 with 64); 32 where a wave
-// holds eight rows or more and loading gains and biases again costs more (100000 x 64 fp32:
-// 9.9 us with 32, 10.7 with 64).
-template <int G>
+// Workgroups of the forward pass by waves a CU.  Where a barrier ties waves together, as many
+// as are resident at once (8192 x 4096 fp16: 25.1 us with 24, 28.1 with 32, 27.4 with 64).
+// Otherwise 64, more than fit, so that a CU whose rows are done takes others (100000 x 256
+// bf16: 17.3 us with 64, 18.1 with 32, 18.4 with 24; the join of 8192 x 4096 bf16: 50.6 with
+// 64, 52.7 with 32, 53.4 with 24).
+template <int G, bool kJoin>
 constexpr int fwd_waves() {
-  return 256 * (G <= 8 ? 32 : 64);
+  return 256 * (G <= 64 || kJoin ? 64 : G < 1024 ? 24 : 32);
 }
 
 template <class T, bool kEven, bool kJoin>
@@ -554,7 +556,7 @@ struct LaunchFwd {
   template <int G, int V>
   hipError_t operator()() const {
     constexpr int threads = fwd_threads<G>(), rows = threads / G;
-    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, fwd_waves<G>() / (threads / 64));
+    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, fwd_waves<G, kJoin>() / (threads / 64));
     fwd_kernel<T, G, V, kEven, kJoin><<<dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
   }
