@@ -157,6 +157,26 @@ def test_layer_norm_strided_views(kind, cols, pitch, first):
     assert (out[:, :first] == 7).all() and (out[:, first + cols:] == 7).all()
 
 
+def test_outputs_between_the_columns_of_inputs():
+    """Columns of one tensor's rows as input and output: their rows interleave in memory without
+    meeting, which is no overlap; a dropout works in place on such a view."""
+    etpc = _etpc()
+    rng = np.random.default_rng(9)
+    big = tensor(rng.standard_normal((23, 150)))
+    before = big.clone()
+    x, y = big[:, :64], big[:, 64:128]
+    _, mean, rstd = etpc.etpc_layer_norm(x, y=y, eps=EPS)
+    check_forward(y, mean, rstd, f64(before[:, :64]), np.zeros(23), np.ones(64), np.zeros(64), "f32")
+    assert torch.equal(big[:, :64], before[:, :64]) and torch.equal(big[:, 128:], before[:, 128:])
+    with pytest.raises(etpc.EtpcError, match="overlap"):
+        etpc.etpc_layer_norm(big[:, :64], y=big[:, 63:127])
+    tail = big[:, 128:147]
+    etpc.etpc_dropout(tail, 0.4, 5, 6, y=tail)
+    ref = nw.dropout(f64(before[:, 128:147]), 0.4, 5, 6)
+    close(tail, ref, U * np.abs(ref), "y")
+    assert torch.equal(big[:, :64], before[:, :64]) and torch.equal(big[:, 147:], before[:, 147:])
+
+
 def test_layer_norm_broadcast_rows_and_shapes():
     """An expanded row (stride 0) is read for every row; leading axes are rows."""
     etpc = _etpc()
