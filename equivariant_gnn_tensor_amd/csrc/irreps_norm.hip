@@ -111,7 +111,7 @@ struct Span {
 // A group's nodes: first + r step + group for the unrolled r.  Past the last node it reads
 // the last one again (and writes nothing).
 struct Node {
-  int64_t base;      // uniform: the workgroup's first node of this round
+  int64_t base;      // uniform: the workgroup's first node of this step
   uint32_t offset;   // what the group adds to it
   bool live;
   __device__ inline Node(int64_t at, int group, int32_t rows) {
@@ -151,7 +151,9 @@ __device__ inline int block_of(const IrrepTable& t, int wg) {
   while (k + 1 < t.n && wg >= t.blk[k + 1].wg) ++k;
   return k;
 }
-__device__ inline int groups_of(const IrrepTable& t, int k) { return (k + 1 < t.n ? t.blk[k + 1].wg : t.groups) - t.blk[k].wg; }
+__device__ inline int groups_of(const IrrepTable& t, int k) {
+  return (k + 1 < t.n ? t.blk[k + 1].wg : t.groups) - t.blk[k].wg;
+}
 
 // The gains (or biases) of a lane's numbers: channel of number e of a flat segment = e mod C.
 template <int D, int I, bool kEven>
@@ -517,10 +519,10 @@ int in_flight(const IrrepBlock& b, int below) { return is_flat(b, below) ? 4 : b
 
 // Deals about `total` workgroups to the blocks so that all blocks walk the nodes at one pace:
 // the rows in flight are one window of memory.  At least one workgroup each and no more than
-// the nodes fill; one_round: one where a single round of loads takes every node (the backward
+// the nodes fill; single_step: one where a single step takes every node (the backward
 // pass then often needs no second stage: 64 nodes of 8x0e+8x1o 7.8 us -> 5.3).  Lays out the
 // rows of partial sums too; returns the floats these need.
-int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below, bool one_round) {
+int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below, bool single_step) {
   double weight = 0.0;
   for (int k = 0; k < t.n; ++k)
     weight += static_cast<double>(lanes_of(span_of(t.blk[k], below))) / in_flight(t.blk[k], below);
@@ -529,7 +531,7 @@ int64_t irreps_deal(IrrepTable& t, int32_t rows, int total, int below, bool one_
   for (int k = 0; k < t.n; ++k) {
     IrrepBlock& q = t.blk[k];
     const int lanes = lanes_of(span_of(q, below)), per = kThreads / lanes;
-    const bool one = one_round && static_cast<int64_t>(per) * in_flight(q, below) >= rows;
+    const bool one = single_step && static_cast<int64_t>(per) * in_flight(q, below) >= rows;
     const int64_t need = one ? 1 : (static_cast<int64_t>(rows) + per - 1) / per;
     const int64_t share = static_cast<int64_t>(total * lanes / (in_flight(q, below) * weight) + 0.5);
     const int64_t parts = std::max<int64_t>(1, std::min(need, share));
@@ -545,8 +547,9 @@ hipError_t launch_irreps_norm_fwd(IrrepTable& t, const float* x, const float* w,
                                   float* stats, int32_t rows, hipStream_t s) {
   irreps_deal(t, rows, kFwdGroups, kFwdFlat, false);
   const FwdArgs a{x, w, b, y, stats, eps, rows};
-  const auto kernel = is_wide(t) ? (is_even(t, kFwdFlat) ? irreps_norm_fwd_kernel<2, true> : irreps_norm_fwd_kernel<2, false>)
-                                 : (is_even(t, kFwdFlat) ? irreps_norm_fwd_kernel<1, true> : irreps_norm_fwd_kernel<1, false>);
+  const bool even = is_even(t, kFwdFlat);
+  const auto kernel = is_wide(t) ? (even ? irreps_norm_fwd_kernel<2, true> : irreps_norm_fwd_kernel<2, false>)
+                                 : (even ? irreps_norm_fwd_kernel<1, true> : irreps_norm_fwd_kernel<1, false>);
   kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   return hipGetLastError();
 }
@@ -560,8 +563,9 @@ hipError_t launch_irreps_norm_bwd(IrrepTable& t, const float* x, const float* y_
                                   hipStream_t s) {
   const bool whole = irreps_norm_part_floats(t, rows) == 0;
   const BwdArgs a{x, y_bar, stats, w, x_bar, w_bar, b_bar, part, rows, whole};
-  const auto kernel = is_wide(t) ? (is_even(t, kBwdFlat) ? irreps_norm_bwd_kernel<2, true> : irreps_norm_bwd_kernel<2, false>)
-                                 : (is_even(t, kBwdFlat) ? irreps_norm_bwd_kernel<1, true> : irreps_norm_bwd_kernel<1, false>);
+  const bool even = is_even(t, kBwdFlat);
+  const auto kernel = is_wide(t) ? (even ? irreps_norm_bwd_kernel<2, true> : irreps_norm_bwd_kernel<2, false>)
+                                 : (even ? irreps_norm_bwd_kernel<1, true> : irreps_norm_bwd_kernel<1, false>);
   kernel<<<dim3(static_cast<unsigned>(t.groups)), dim3(kThreads), 0, s>>>(t, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || whole || (w_bar == nullptr && b_bar == nullptr)) return e;

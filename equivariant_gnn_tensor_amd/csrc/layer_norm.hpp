@@ -199,21 +199,61 @@ __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs
   }
 }
 
+// Eight elements on their way into registers.  A 16-byte load of 16-bit elements whose
+// address is odd in elements takes about three cycles a lane, so two streams of them bound the
+// backward pass of long rows (32768 rows of 2047 bf16: 104 us).  With kOdd such a vector is
+// read one element lower, or one higher where it starts the row, and its eighth element on
+// its own: everything stays inside the row, which has nine elements at least (83 us; 8000 x
+// 4097 79 -> 69; rows up to 1024 columns gain nothing: 100000 x 65 13.8 -> 15.1).
+template <class T, bool kOdd>
+struct Raw8 {
+  Vec8<T> t;
+  T extra;
+  int shift;   // 0: t is the vector; -1, 1: t lies one element lower, higher
+  __device__ inline void read(const T* __restrict__ p, bool first) {
+    shift = (reinterpret_cast<uintptr_t>(p) & 2) == 0 ? 0 : first ? 1 : -1;
+    __builtin_memcpy(&t, __builtin_assume_aligned(p + shift, 4), sizeof(t));
+    extra = p[shift < 0 ? 7 : 0];
+  }
+  __device__ inline Vec8<T> get() const {
+    uint32_t d[4], o[4];
+    uint16_t e;
+    __builtin_memcpy(d, &t, sizeof(d));
+    __builtin_memcpy(&e, &extra, sizeof(e));
+    const uint32_t s[5] = {pick(shift > 0, static_cast<uint32_t>(e) << 16, d[0]), pick(shift > 0, d[0], d[1]),
+                           pick(shift > 0, d[1], d[2]), pick(shift > 0, d[2], d[3]), pick(shift > 0, d[3], e)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = pick(shift != 0, (s[k] >> 16) | (s[k + 1] << 16), d[k]);
+    Vec8<T> v;
+    __builtin_memcpy(&v, o, sizeof(v));
+    return v;
+  }
+};
+template <class T>
+struct Raw8<T, false> {
+  Vec8<T> t;
+  __device__ inline Vec8<T> get() const { return t; }
+};
+
 // What the backward pass reads of one row, a thread's share.
-template <class T, int G, int V, bool kEven, bool kJoin>
+template <class T, int G, int V, bool kEven, bool kJoin, bool kOdd>
 struct Operands {
-  Vec8<T> h[V], y_bar[V], h_bar[kJoin ? V : 1];
+  Raw8<T, kOdd> h[V], y_bar[V], h_bar[kJoin ? V : 1];
   float mean, rstd;
+  __device__ inline void one(Raw8<T, kOdd>& r, const Span<G, V, kEven>& span, const void* p, int64_t at, int i) {
+    if constexpr (kOdd) r.read(static_cast<const T*>(p) + at + span.at[i], span.at[i] == 0);
+    else r.t = span.fetch(static_cast<const T*>(p) + at, i);
+  }
   __device__ inline void read(const NormBwdArgs& a, const Span<G, V, kEven>& span, int64_t row) {
     if (kJoin && a.h_bar != nullptr)
 #pragma unroll
-      for (int i = 0; i < V; ++i) h_bar[i] = span.fetch(static_cast<const T*>(a.h_bar) + row * a.hbs, i);
+      for (int i = 0; i < V; ++i) one(h_bar[i], span, a.h_bar, row * a.hbs, i);
     mean = a.mean[row];
     rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      h[i] = span.fetch(static_cast<const T*>(a.h) + row * a.hs, i);
-      y_bar[i] = span.fetch(static_cast<const T*>(a.y_bar) + row * a.ybs, i);
+      one(h[i], span, a.h, row * a.hs, i);
+      one(y_bar[i], span, a.y_bar, row * a.ybs, i);
     }
   }
 };
@@ -226,9 +266,8 @@ struct Operands {
 // two 81.4), the prefetch then gave 44.9.  Rows past 8192 columns need two vectors for 1024
 // threads, whose sums then live in LDS (each thread its own places).
 // What it reaches, sums included: 8192 x 4096 fp16 43.4 us, 4.6 TB/s; 65536 x 512 bf16
-// 40.5 us, 5.0 TB/s; join 65408 x 1024 bf16 133 us, 5.0 TB/s.  bf16 rows that start at an
-// odd element are read a third slower (32768 x 2047: 103 us against 81 for 2048).
-template <class T, int G, int V, bool kEven, bool kJoin>
+// 40.5 us, 5.0 TB/s; join 65408 x 1024 bf16 133 us, 5.0 TB/s; 32768 x 2047 bf16 83 us, 4.9 TB/s.
+template <class T, int G, int V, bool kEven, bool kJoin, bool kOdd>
 __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs a) {
   constexpr int kRows = bwd_threads<G>() / G;
   constexpr bool kBarrier = G > 64 && kRows > 1;   // rows that share a barrier take it together
@@ -255,24 +294,25 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs
   }
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group_index<G>();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  Operands<T, G, V, kEven, kJoin> next;
+  Operands<T, G, V, kEven, kJoin, kOdd> next;
   if (kAhead && row < a.rows) next.read(a, span, row);
   for (; kBarrier ? row - group_index<G>() < a.rows : row < a.rows; row += step) {
-    if (kBarrier && row >= a.rows) {   // the last round may have a row for the first group only
+    if (kBarrier && row >= a.rows) {   // the last step may have a row for the first group only
       float none[2] = {0.f, 0.f};
       if (grads) group_sum<G, kRows>(none, lds, half);
       continue;
     }
     if (!kAhead) next.read(a, span, row);
-    const Operands<T, G, V, kEven, kJoin> now = next;
+    const Operands<T, G, V, kEven, kJoin, kOdd> now = next;
     if (kAhead) next.read(a, span, row + step < a.rows ? row + step : row);
     float v[V][8], g[V][8], s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      const Vec8<T> h = now.h[i].get(), y_bar = now.y_bar[i].get();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float y = static_cast<float>(now.y_bar[i][k]);
-        v[i][k] = (static_cast<float>(now.h[i][k]) - now.mean) * now.rstd;
+        const float y = static_cast<float>(y_bar[k]);
+        v[i][k] = (static_cast<float>(h[k]) - now.mean) * now.rstd;
         if (kLdsSums) {
           own[(16 * i + k) * G] = fmaf(y, v[i][k], own[(16 * i + k) * G]);
           own[(16 * i + 8 + k) * G] += y;
@@ -293,9 +333,11 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs
     for (int i = 0; i < V; ++i) {
       float t[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        t[k] = now.rstd * (g[i][k] - fmaf(v[i][k], m1, m0));
-        if (kJoin && a.h_bar != nullptr) t[k] += static_cast<float>(now.h_bar[i][k]);
+      for (int k = 0; k < 8; ++k) t[k] = now.rstd * (g[i][k] - fmaf(v[i][k], m1, m0));
+      if (kJoin && a.h_bar != nullptr) {
+        const Vec8<T> h_bar = now.h_bar[i].get();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] += static_cast<float>(h_bar[k]);
       }
       if (kJoin) {
         if (a.res_bar != nullptr) span.store(static_cast<T*>(a.res_bar) + row * a.rbs, i, t);
@@ -556,19 +598,21 @@ struct LaunchFwd {
   template <int G, int V>
   hipError_t operator()() const {
     constexpr int threads = fwd_threads<G>(), rows = threads / G;
-    const int64_t groups = std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, fwd_waves<G, kJoin>() / (threads / 64));
+    const int64_t groups =
+        std::min<int64_t>((static_cast<int64_t>(a.rows) + rows - 1) / rows, fwd_waves<G, kJoin>() / (threads / 64));
     fwd_kernel<T, G, V, kEven, kJoin><<<dim3(static_cast<unsigned>(groups)), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
   }
 };
 
-template <class T, bool kEven, bool kJoin>
+template <class T, bool kEven, bool kJoin, bool kOdd>
 struct LaunchBwd {
   const NormBwdArgs& a;
   hipStream_t s;
   template <int G, int V>
   hipError_t operator()() const {
-    bwd_kernel<T, G, V, kEven, kJoin>
+    // the kernel with sums in LDS has no registers to spare for it
+    bwd_kernel<T, G, V, kEven, kJoin, kOdd && V == 1 && (G > 128)>
         <<<dim3(static_cast<unsigned>(a.parts)), dim3(bwd_threads<G>()), 0, s>>>(a);
     return hipGetLastError();
   }
@@ -583,10 +627,21 @@ inline bool bwd_join(const NormBwdArgs& a) {
   return a.x_bar == nullptr || a.res_bar != nullptr || a.h_bar != nullptr || a.drop.threshold != 0;
 }
 
+// Whether any row of an operand starts at an odd element (of 16 bits).
+inline bool odd_rows(const void* p, int64_t stride, int32_t rows) {
+  return p != nullptr && ((reinterpret_cast<uintptr_t>(p) & 2) != 0 || (rows > 1 && (stride & 1) != 0));
+}
+
 template <class T, bool kJoin>
 hipError_t reg_bwd(const NormBwdArgs& a, hipStream_t s) {
-  return a.cols % 8 == 0 ? bwd_shape(a.cols, LaunchBwd<T, true, kJoin>{a, s})
-                         : bwd_shape(a.cols, LaunchBwd<T, false, kJoin>{a, s});
+  if constexpr (sizeof(T) == 2) {
+    if (a.cols > 1024 &&
+        (odd_rows(a.h, a.hs, a.rows) || odd_rows(a.y_bar, a.ybs, a.rows) || odd_rows(a.h_bar, a.hbs, a.rows)))
+      return a.cols % 8 == 0 ? bwd_shape(a.cols, LaunchBwd<T, true, kJoin, true>{a, s})
+                             : bwd_shape(a.cols, LaunchBwd<T, false, kJoin, true>{a, s});
+  }
+  return a.cols % 8 == 0 ? bwd_shape(a.cols, LaunchBwd<T, true, kJoin, false>{a, s})
+                         : bwd_shape(a.cols, LaunchBwd<T, false, kJoin, false>{a, s});
 }
 
 // The plain layer norm has kernels of its own: nothing in their loops depends on what the
