@@ -40,8 +40,8 @@ struct CountParts {
   int operator()() const {
     constexpr int threads = norm::bwd_threads<G>(), per = threads / G;
     const bool idle = G > 64 && 4 * ((static_cast<int64_t>(cols) + 7) / 8) <= 3 * G * V;
-    const int waves = (idle && !wide) || G == 1024 ? 16 : join && !wide ? 12 : 8;
-    const int64_t most = 256 * waves / (threads / 64);
+    const int waves = idle && !wide ? 16 : join && !wide ? 12 : 8;
+    const int64_t most = G > 512 ? 256 : 256 * waves / (threads / 64);   // from 640 threads on, one a CU
     const int64_t units = (static_cast<int64_t>(rows) + per - 1) / per;
     return static_cast<int>(std::min(units, std::max<int64_t>(128, std::min((units + 2) / 3, most))));
   }
