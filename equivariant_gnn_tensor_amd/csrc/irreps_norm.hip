@@ -49,15 +49,25 @@ __host__ __device__ inline int span_of(const IrrepBlock& b, int below) {
   return is_flat(b, below) ? (2 * b.l + 1) * b.mul : b.mul;
 }
 
-// The sum over aligned groups of g lanes, g uniform in the workgroup.
+// The sums over aligned groups of g lanes, g uniform in the workgroup; two at once hide each
+// other's latency.
+template <int N>
+__device__ inline void sum_lanes(float (&v)[N], int g) {
+  const auto add = [&](auto step) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = step(v[i]);
+  };
+  if (g >= 2) add([](float x) { return x + dpp_f<0xB1>(x); });
+  if (g >= 4) add([](float x) { return x + dpp_f<0x4E>(x); });
+  if (g >= 8) add([](float x) { return x + dpp_f<0x141>(x); });
+  if (g >= 16) add([](float x) { return x + dpp_f<0x140>(x); });
+  if (g >= 32) add([](float x) { return add_lane16(x); });
+  if (g >= 64) add([](float x) { return add_lane32(x); });
+}
 __device__ inline float sum_lanes(float v, int g) {
-  if (g >= 2) v += dpp_f<0xB1>(v);
-  if (g >= 4) v += dpp_f<0x4E>(v);
-  if (g >= 8) v += dpp_f<0x141>(v);
-  if (g >= 16) v += dpp_f<0x140>(v);
-  if (g >= 32) v = add_lane16(v);
-  if (g >= 64) v = add_lane32(v);
-  return v;
+  float a[1] = {v};
+  sum_lanes(a, g);
+  return a[0];
 }
 
 // Where a lane's vector i lies among the channels of a component.  A vector that would start
@@ -198,7 +208,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const Node q(first + r * step, group, a.rows);
-      float s = 0.f, mean = 0.f;
+      float s = 0.f, mean = 0.f, off = 0.f;
       if (D == 1 && center) {
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -216,12 +226,22 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
             if (D == 1) v[r][d][i][j] -= mean;
             const float c = span.counts(i, j) ? v[r][d][i][j] : 0.f;
             s = fmaf(c, c, s);
+            if (D == 1) off += c;
           }
-      const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, G), inv_n, a.eps));
+      if (D == 1 && center) {
+        float both[2] = {s, off};
+        sum_lanes(both, G);
+        s = both[0];
+        off = both[1] * inv_n;   // what the rounded mean is off by
+      } else {
+        s = sum_lanes(s, G);
+        off = 0.f;
+      }
+      const float rstd = norm_rstd(s, off, inv_n, a.eps);
       if (!q.live) continue;
       if (a.stats != nullptr) {   // every lane of the group, the same bits
         float* st = a.stats + 2 * (q.base * t.n + k);
-        st[2 * q.offset * t.n] = mean;
+        st[2 * q.offset * t.n] = mean + off;
         st[2 * q.offset * t.n + 1] = rstd;
       }
 #pragma unroll
@@ -230,7 +250,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
         for (int i = 0; i < I; ++i) {
           float o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = fmaf(v[r][d][i][j] * rstd, w[i][j], b[i][j]);
+          for (int j = 0; j < 4; ++j) o[j] = fmaf((v[r][d][i][j] - off) * rstd, w[i][j], b[i][j]);
           span.store(a.y + (q.base * t.dim + t.blk[k].off + d * mul), q.offset * t.dim, i, o);
         }
     }
@@ -255,7 +275,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
   for (int64_t row = static_cast<int64_t>(p) * kWaves + threadIdx.x / 64; row < a.rows;
        row += static_cast<int64_t>(parts) * kWaves) {
     const float* x = a.x + row * t.dim + t.blk[k].off;
-    float s = 0.f, mean = 0.f;
+    float s = 0.f, mean = 0.f, off = 0.f;
     if (n == mul) {
       for (int e = 4 * lane; e < n; e += 256) {
         float v[4];
@@ -270,11 +290,15 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
       load<4, false>(x, e, n, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (e + j < n) s = fmaf(v[j] - mean, v[j] - mean, s);
+        if (e + j < n) {
+          s = fmaf(v[j] - mean, v[j] - mean, s);
+          off += v[j] - mean;
+        }
     }
-    const float rstd = 1.f / sqrtf(fmaf(sum_lanes(s, 64), inv_n, a.eps));
+    off = n == mul ? sum_lanes(off, 64) * inv_n : 0.f;
+    const float rstd = norm_rstd(sum_lanes(s, 64), off, inv_n, a.eps);
     if (lane == 0 && a.stats != nullptr) {
-      a.stats[2 * (row * t.n + k)] = mean;
+      a.stats[2 * (row * t.n + k)] = mean + off;
       a.stats[2 * (row * t.n + k) + 1] = rstd;
     }
     for (int d = 0; d * mul < n; ++d)
@@ -284,7 +308,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
         load4_or(w, c, mul, 1.f, g);
         load4_or(b, c, mul, 0.f, h);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], h[j]);
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(((v[j] - mean) - off) * rstd, g[j], h[j]);
         store<4, false>(a.y + row * t.dim + t.blk[k].off + d * mul, c, mul, v);
       }
   }
@@ -364,7 +388,15 @@ __device__ inline void bwd_block(const IrrepTable& t, int k, int p, int parts, c
             s1 = fmaf(c, x, s1);
           }
       if (a.x_bar == nullptr) continue;
-      const float m0 = D == 1 && center ? sum_lanes(s0, G) * inv_n : 0.f, m1 = sum_lanes(s1, G) * inv_n;
+      float m0 = 0.f, m1;
+      if (D == 1 && center) {
+        float both[2] = {s0, s1};
+        sum_lanes(both, G);
+        m0 = both[0] * inv_n;
+        m1 = both[1] * inv_n;
+      } else {
+        m1 = sum_lanes(s1, G) * inv_n;
+      }
       if (!q.live) continue;
 #pragma unroll
       for (int d = 0; d < D; ++d)

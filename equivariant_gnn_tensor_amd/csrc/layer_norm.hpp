@@ -8,10 +8,11 @@
 //   w_bar = sum_rows y_bar xh,  b_bar = sum_rows y_bar.
 //
 // Memory bound: one pass reads every operand once and writes every result once.  A group of
-// G threads owns a row and keeps it in registers (8 V columns a thread), so the two sums of
-// the forward pass (mean, then the sum of squares of what is left after it, which does not
-// cancel) and the backward's two cost no second read.  Statistics, sums and the normalised
-// row are fp32 whatever the element type; y comes from the unrounded h.
+// G threads owns a row and keeps it in registers (8 V columns a thread), so the sums of the
+// forward pass (mean, then sum and sum of squares of what is left after it, which do not
+// cancel; the sum is what the rounded mean is off by, and corrects it) and the backward's two
+// cost no second read.  Statistics, sums and the normalised row are fp32 whatever the element
+// type; y comes from the unrounded h.
 #pragma once
 
 #include <algorithm>
@@ -135,7 +136,7 @@ __device__ inline int group_index() {
 template <class T, int G, int V, bool kEven, bool kJoin>
 __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs a) {
   constexpr int kRows = fwd_threads<G>() / G;
-  __shared__ float lds[G > 64 ? 2 * G / 64 : 1];
+  __shared__ float lds[G > 64 ? 4 * G / 64 : 1];
   const Span<G, V, kEven> span(threadIdx.x % G, a.cols);
   const float inv_n = 1.f / static_cast<float>(a.cols);
   const bool drop = kJoin && a.drop.threshold != 0;
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs
   // shares of adjacent rows measured 5 to 15 % slower).
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group_index<G>(); row < a.rows; row += step) {
-    float v[V][8], s[1] = {0.f};
+    float v[V][8], s[1] = {0.f}, q[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) span.load(static_cast<const T*>(a.x) + row * a.xs, i, v[i]);
     if (kJoin) {
@@ -177,23 +178,23 @@ __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs
       for (int k = 0; k < 8; ++k) s[0] += span.counts(i, k) ? v[i][k] : 0.f;
     group_sum<G, kRows>(s, lds, half);
     const float mean = s[0] / static_cast<float>(a.cols);   // exact for a constant row, unlike s * (1 / n)
-    s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         v[i][k] -= mean;
         const float c = span.counts(i, k) ? v[i][k] : 0.f;
-        s[0] = fmaf(c, c, s[0]);
+        q[0] = fmaf(c, c, q[0]);
+        q[1] += c;
       }
-    group_sum<G, kRows>(s, lds, half);
-    const float rstd = 1.f / sqrtf(fmaf(s[0], inv_n, a.eps));
-    if (a.mean != nullptr) a.mean[row] = mean;   // every thread of the group, the same bits
+    group_sum<G, kRows>(q, lds, half);
+    const float off = q[1] * inv_n, rstd = norm_rstd(q[0], off, inv_n, a.eps);
+    if (a.mean != nullptr) a.mean[row] = mean + off;   // every thread of the group, the same bits
     if (a.rstd != nullptr) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][k] = fmaf(v[i][k] * rstd, w[i][k], b[i][k]);
+      for (int k = 0; k < 8; ++k) v[i][k] = fmaf((v[i][k] - off) * rstd, w[i][k], b[i][k]);
       span.store(static_cast<T*>(a.y) + row * a.ys, i, v[i]);
     }
   }
@@ -401,7 +402,7 @@ __device__ inline void long_h(const NormFwdArgs& a, int64_t row, int c, bool dro
 
 template <class T>
 __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
-  __shared__ float lds[2 * kLong / 64];
+  __shared__ float lds[4 * kLong / 64];
   const int n = a.cols;
   const float inv_n = 1.f / static_cast<float>(n);
   const bool drop = a.drop.threshold != 0;
@@ -419,19 +420,23 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
     }
     group_sum<kLong, 1>(s, lds, half);
     const float mean = s[0] / static_cast<float>(n);   // exact for a constant row, unlike s * (1 / n)
-    s[0] = 0.f;
+    float q[2] = {0.f, 0.f};
     for (int64_t c = 8 * threadIdx.x; c < n; c += 8 * kLong) {
-      float v[8], t = 0.f;
+      float v[8], t0 = 0.f, t1 = 0.f;
       long_h<T>(a, row, static_cast<int>(c), drop, offset, v);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k < n) t = fmaf(v[k] - mean, v[k] - mean, t);
-      s[0] += t;
+        if (c + k < n) {
+          t0 = fmaf(v[k] - mean, v[k] - mean, t0);
+          t1 += v[k] - mean;
+        }
+      q[0] += t0;
+      q[1] += t1;
     }
-    group_sum<kLong, 1>(s, lds, half);
-    const float rstd = 1.f / sqrtf(fmaf(s[0], inv_n, a.eps));
+    group_sum<kLong, 1>(q, lds, half);
+    const float off = q[1] * inv_n, rstd = norm_rstd(q[0], off, inv_n, a.eps);
     if (threadIdx.x == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.mean != nullptr) a.mean[row] = mean + off;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     for (int64_t cc = 8 * threadIdx.x; cc < n; cc += 8 * kLong) {
@@ -442,7 +447,7 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
       if (a.b != nullptr) load<8, false>(a.b, c, n, b);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        v[k] = fmaf((v[k] - mean) * rstd, a.w != nullptr ? w[k] : 1.f, a.b != nullptr ? b[k] : 0.f);
+        v[k] = fmaf(((v[k] - mean) - off) * rstd, a.w != nullptr ? w[k] : 1.f, a.b != nullptr ? b[k] : 0.f);
       store<8, false>(static_cast<T*>(a.y) + row * a.ys, c, n, v);
     }
   }

@@ -133,6 +133,11 @@ __device__ inline void group_sum(float (&v)[N], float* lds, int& half) {
   }
 }
 
+// 1 / sqrt(var + eps) from the sum of squares about a mean that is `off` too low.
+__device__ inline float norm_rstd(float squares, float off, float inv_n, float eps) {
+  return 1.f / sqrtf(fmaxf(fmaf(squares, inv_n, -off * off), 0.f) + eps);
+}
+
 // p[slice width] + p[(slice + kSlices) width] + ... over the first `parts` rows, in order, with
 // eight loads in flight.
 template <int kSlices>

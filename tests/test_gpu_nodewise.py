@@ -223,6 +223,27 @@ def test_layer_norm_hard_rows():
     assert torch.isnan(etpc.etpc_layer_norm(x, eps=0.0)[0][0]).all()
 
 
+@pytest.mark.parametrize("level", [0.0, 300.0, 1e5])
+def test_rows_far_from_zero(level):
+    """The mean is corrected by what is left after it, so the centred numbers d are off by 64 u
+    of their own size (the sum of what is left) whatever the level: exact differences of
+    numbers near each other.  Held to that, with 64 u of the result and its level's rounding
+    for the stored mean."""
+    etpc = _etpc()
+    rng = np.random.default_rng(10)
+    for n, cols in ((40, 700), (3, 64), (2, 3000), (2, 18000)):
+        x = tensor(level + rng.standard_normal((n, cols)))
+        for y, mean, rstd in (etpc.etpc_layer_norm(x, eps=EPS),
+                              (lambda y, st: (y, st[:, 0, 0], st[:, 0, 1]))(*etpc.etpc_irreps_norm(f"{cols}x0e", x, eps=EPS))):
+            ry, rm, rs = nw.layer_norm(f64(x), np.ones(cols), np.zeros(cols), EPS)
+            top = np.abs(ry).max(axis=1)
+            # the irreps norm's segments past 512 numbers add up to 256 numbers in a lane
+            terms = 64 * U if cols <= 512 else 320 * U
+            assert (np.abs(f64(y) - ry) <= 2 * terms * top[:, None] + terms * np.abs(ry)).all()
+            assert (np.abs(f64(mean) - rm) <= terms * top / rs + 2 * U * np.abs(rm)).all()
+            assert (np.abs(f64(rstd) - rs) <= 2 * terms * rs).all()
+
+
 def test_layer_norm_wanted_outputs():
     etpc = _etpc()
     rng = np.random.default_rng(7)
