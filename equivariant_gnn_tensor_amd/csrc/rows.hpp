@@ -133,9 +133,12 @@ __device__ inline void group_sum(float (&v)[N], float* lds, int& half) {
   }
 }
 
-// 1 / sqrt(var + eps) from the sum of squares about a mean that is `off` too low.
+// 1 / sqrt(var + eps) from the sum of squares about a mean that is `off` too low.  A variance
+// that rounding took below zero is zero; one that is NaN stays so (a maximum with zero would
+// hide it), and with it every number of the row.
 __device__ inline float norm_rstd(float squares, float off, float inv_n, float eps) {
-  return 1.f / sqrtf(fmaxf(fmaf(squares, inv_n, -off * off), 0.f) + eps);
+  const float var = fmaf(squares, inv_n, -off * off);
+  return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
 }
 
 // p[slice width] + p[(slice + kSlices) width] + ... over the first `parts` rows, in order, with
