@@ -241,7 +241,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
       if (!q.live) continue;
       if (a.stats != nullptr) {   // every lane of the group, the same bits
         float* st = a.stats + 2 * (q.base * t.n + k);
-        st[2 * q.offset * t.n] = mean + off;
+        st[2 * q.offset * t.n] = norm_mean(mean, off, rstd);
         st[2 * q.offset * t.n + 1] = rstd;
       }
 #pragma unroll
@@ -298,7 +298,7 @@ __device__ inline void fwd_long(const IrrepTable& t, int k, int p, int parts, co
     off = n == mul ? sum_lanes(off, 64) * inv_n : 0.f;
     const float rstd = norm_rstd(sum_lanes(s, 64), off, inv_n, a.eps);
     if (lane == 0 && a.stats != nullptr) {
-      a.stats[2 * (row * t.n + k)] = mean + off;
+      a.stats[2 * (row * t.n + k)] = norm_mean(mean, off, rstd);
       a.stats[2 * (row * t.n + k) + 1] = rstd;
     }
     for (int d = 0; d * mul < n; ++d)

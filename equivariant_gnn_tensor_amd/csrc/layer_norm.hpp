@@ -189,7 +189,7 @@ __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs
       }
     group_sum<G, kRows>(q, lds, half);
     const float off = q[1] * inv_n, rstd = norm_rstd(q[0], off, inv_n, a.eps);
-    if (a.mean != nullptr) a.mean[row] = mean + off;   // every thread of the group, the same bits
+    if (a.mean != nullptr) a.mean[row] = norm_mean(mean, off, rstd);   // every thread of the group, the same bits
     if (a.rstd != nullptr) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -436,7 +436,7 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
     group_sum<kLong, 1>(q, lds, half);
     const float off = q[1] * inv_n, rstd = norm_rstd(q[0], off, inv_n, a.eps);
     if (threadIdx.x == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean + off;
+      if (a.mean != nullptr) a.mean[row] = norm_mean(mean, off, rstd);
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     for (int64_t cc = 8 * threadIdx.x; cc < n; cc += 8 * kLong) {

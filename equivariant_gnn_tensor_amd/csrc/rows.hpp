@@ -141,6 +141,16 @@ __device__ inline float norm_rstd(float squares, float off, float inv_n, float e
   return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
 }
 
+// The mean to keep for the backward pass.  `off` corrects the rounding of a mean of the size
+// of the spread and above.  Near zero it does not: all numbers of one binade round x - mean
+// by the same amount, their average is that amount, and the sum it would correct is the
+// better one (4096 normal numbers about 0: median relative error 1e-7 without, 6e-7 with;
+// about 1/4 of their spread 3.1e-8 and 2.5e-8; about 300 spreads 3.0e-8 and 2.4e-8).  An
+// infinite mean stays as it is: `off` is NaN then, and so is rstd.
+__device__ inline float norm_mean(float mean, float off, float rstd) {
+  return fabsf(mean) * rstd > 0.25f ? mean + off : mean;
+}
+
 // p[slice width] + p[(slice + kSlices) width] + ... over the first `parts` rows, in order, with
 // eight loads in flight.
 template <int kSlices>

@@ -1,5 +1,5 @@
 """GPU checks of the node-wise operators where they can go wrong: rows that hold a NaN or an
-infinity, against oracle/nodewise.py (float64).
+infinity, the stored mean of rows near zero, against oracle/nodewise.py (float64).
 
 `same` compares values that are not finite by kind: NaN with NaN, an infinity with the
 infinity of its sign.  u = 2^-24.
@@ -53,7 +53,8 @@ def same(got, ref, bound, what):
 @pytest.mark.parametrize("cols", [5, 64, 600, 3000, 18000])
 @pytest.mark.parametrize("join", [False, True])
 def test_a_nan_in_a_row_reaches_its_statistics(cols, join):
-    """A row with a NaN or an infinity has no rstd and no finite y; no other row is touched."""
+    """A row with a NaN has neither mean nor rstd, one with an infinity has an infinite mean and
+    no rstd; neither has a finite y, and no other row is touched."""
     etpc = _etpc()
     rng = np.random.default_rng(cols)
     clean = rng.standard_normal((9, cols)).astype(np.float32)
@@ -75,6 +76,7 @@ def test_a_nan_in_a_row_reaches_its_statistics(cols, join):
         assert torch.equal(p[keep], q[keep])
     y, mean, rstd = got
     assert torch.isnan(mean[2]) and torch.isnan(rstd[[2, 5, 7]]).all() and torch.isnan(y[[2, 5, 7]]).all()
+    assert mean[5] == float("inf") and mean[7] == -float("inf")
 
 
 # flat segments (narrow or l = 0), channel by channel, more channels than a wave keeps
@@ -100,9 +102,7 @@ def test_a_nan_in_an_irreps_block_spoils_the_block(text, value):
             ry, rs = nw.irreps_norm(bad, ir, f64(w), f64(b), EPS)
         part = slice(off, off + width)
         same(y[4, part], ry[4, part], 256 * U * np.abs(ry[4, part]), (text, k, "y"))
-        if l > 0:   # an infinite l = 0 block: the mean is infinite, what is left after it is not
-            same(stats[4, k], rs[4, k], 0.0, (text, k, "stats"))
-        assert torch.isnan(stats[4, k, 1]) or (l > 0 and np.isinf(value) and stats[4, k, 1] == 0)
+        same(stats[4, k], rs[4, k], 0.0, (text, k, "stats"))   # none of them finite but 0
         other = torch.ones_like(y, dtype=torch.bool)
         other[4, part] = False
         assert torch.equal(y[other], y0[other])
@@ -112,3 +112,30 @@ def test_a_nan_in_an_irreps_block_spoils_the_block(text, value):
         if np.isnan(value):   # the gradients' sums show it too
             _, wb, _ = etpc.etpc_irreps_norm_backward(text, tensor(bad), y0, stats, w)
             assert torch.isnan(wb[ch:ch + mul]).all() and torch.isfinite(wb[:ch]).all() and torch.isfinite(wb[ch + mul:]).all()
+
+
+# ---------------------------------------------------------------- the stored mean
+
+@pytest.mark.parametrize("cols", [20, 100, 600, 1000, 3000, 12000, 18000])
+@pytest.mark.parametrize("level", [0, 1, 37, 1000])
+def test_stored_mean_of_rows_near_zero(cols, level):
+    """Pairs a, -a of numbers in [1, 2) on a grid of 2^-18, `level` steps of which are added to
+    the first 2/3 of the row: every partial sum is a multiple of 2^-18 below 2^6, hence exact
+    in 24 bits, and the stored mean is off by the roundings of its division and of what may
+    still be added to it, 2 u of itself.  (The differences x - mean are not exact: their
+    average is off by up to half a step of [1, 2), 2^-24, which is 1e-2 of these means.)"""
+    etpc = _etpc()
+    rng = np.random.default_rng(cols + level)
+    step = 2.0 ** -18
+    a = 1.0 + rng.integers(2000, (1 << 18) - 2000, (6, cols // 2)) * step
+    a *= rng.choice([-1.0, 1.0], a.shape)
+    x = np.stack([a, -a], axis=-1).reshape(6, cols)
+    x[:, :2 * cols // 3] += level * step
+    assert 2 + cols * level * step < 128 and x.sum(axis=1).max() < 64 and np.array_equal(x, x.astype(np.float32))
+    note(f"stored mean near zero, cols={cols} level={level}")
+    ref, t = x.mean(axis=1), tensor(x)
+    yb = tensor(np.zeros((6, cols)))
+    means = [etpc.etpc_layer_norm(t, eps=EPS)[1], etpc.etpc_dropout_add_layer_norm(t, yb, eps=EPS)[2],
+             etpc.etpc_irreps_norm(f"{cols}x0e", t, eps=EPS)[1][:, 0, 0]]
+    for m in means:
+        same(m, ref, 2 * U * np.abs(ref), "mean")
