@@ -5,25 +5,32 @@ namespace etpc {
 namespace {
 
 // A workgroup sums 16 adjacent columns of `part`: 64 slices of the rows, each in order, then
-// the slices in order.  16 columns are one 64-byte segment of a row of `part`.
+// the slices in order.  16 columns are one 64-byte segment of a row of `part`.  More workgroups
+// than kMaxGroups walk on (a launch holds less than 2^32 threads).
 constexpr int kCols = 16, kSlices = 64;
+constexpr int64_t kMaxGroups = int64_t{1} << 20;
 
 __global__ __launch_bounds__(kCols* kSlices) void parts_reduce_kernel(const float* __restrict__ part, int parts,
                                                                       int cols, int64_t total,
                                                                       float* w_bar, float* b_bar) {
   __shared__ float lds[kSlices][kCols];
   const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kCols + lane;
-  lds[slice][lane] = c < total ? sum_slice<kSlices>(part + c, total, slice, parts) : 0.f;
-  __syncthreads();
-  if (slice != 0 || c >= total) return;
-  float s = 0.f;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kCols; first < total;
+       first += static_cast<int64_t>(gridDim.x) * kCols) {
+    const int64_t c = first + lane;
+    lds[slice][lane] = c < total ? sum_slice<kSlices>(part + c, total, slice, parts) : 0.f;
+    __syncthreads();
+    if (slice == 0 && c < total) {
+      float s = 0.f;
 #pragma unroll 8
-  for (int q = 0; q < kSlices; ++q) s += lds[q][lane];
-  if (c < cols) {
-    if (w_bar != nullptr) w_bar[c] = s;
-  } else if (b_bar != nullptr) {
-    b_bar[c - cols] = s;
+      for (int q = 0; q < kSlices; ++q) s += lds[q][lane];
+      if (c < cols) {
+        if (w_bar != nullptr) w_bar[c] = s;
+      } else if (b_bar != nullptr) {
+        b_bar[c - cols] = s;
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -56,8 +63,8 @@ int norm_parts_most(int32_t rows, int32_t cols) {
 
 hipError_t launch_parts_reduce(const float* part, int parts, int cols, float* w_bar, float* b_bar, hipStream_t s) {
   const int64_t total = 2 * static_cast<int64_t>(cols);
-  parts_reduce_kernel<<<dim3(static_cast<unsigned>((total + kCols - 1) / kCols)), dim3(kCols * kSlices), 0, s>>>(
-      part, parts, cols, total, w_bar, b_bar);
+  const unsigned groups = static_cast<unsigned>(std::min((total + kCols - 1) / kCols, kMaxGroups));
+  parts_reduce_kernel<<<dim3(groups), dim3(kCols * kSlices), 0, s>>>(part, parts, cols, total, w_bar, b_bar);
   return hipGetLastError();
 }
 

@@ -1,5 +1,6 @@
 """GPU checks of the node-wise operators where they can go wrong: rows that hold a NaN or an
-infinity, the stored mean of rows near zero, against oracle/nodewise.py (float64).
+infinity, the stored mean of rows near zero, rows of 2^25 and
+more columns, against oracle/nodewise.py (float64).
 
 `same` compares values that are not finite by kind: NaN with NaN, an infinity with the
 infinity of its sign.  u = 2^-24.
@@ -139,3 +140,23 @@ def test_stored_mean_of_rows_near_zero(cols, level):
              etpc.etpc_irreps_norm(f"{cols}x0e", t, eps=EPS)[1][:, 0, 0]]
     for m in means:
         same(m, ref, 2 * U * np.abs(ref), "mean")
+
+
+# ---------------------------------------------------------------- very long rows
+
+@pytest.mark.parametrize("kind,cols", [(torch.bfloat16, (1 << 25) + 3), (torch.float32, 1 << 26)])
+def test_gradients_of_rows_past_2_to_the_25(kind, cols):
+    """Both stages of the parameter gradients' sums at row lengths where the second stage's
+    columns, sixteen a workgroup of 1024 threads, are more than one launch holds.  Two rows:
+    one difference, two products and one sum, 5 u of their magnitudes."""
+    etpc = _etpc()
+    torch.manual_seed(3)
+    x, yb = torch.randn(2, cols, device="cuda").to(kind), torch.randn(2, cols, device="cuda").to(kind)
+    mean, rstd = torch.tensor([0.25, -0.5], device="cuda"), torch.tensor([1.5, 0.75], device="cuda")
+    note(f"parameter gradients of rows of {cols} columns")
+    x_bar, wb, bb = etpc.etpc_layer_norm_backward(x, yb, mean, rstd, want=("w", "b"))
+    assert x_bar is None and wb.shape == bb.shape == (cols,)
+    t = yb.double() * (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    assert ((wb.double() - t.sum(0)).abs() <= 5 * U * t.abs().sum(0)).all()
+    t = yb.double()
+    assert ((bb.double() - t.sum(0)).abs() <= U * t.abs().sum(0)).all()
