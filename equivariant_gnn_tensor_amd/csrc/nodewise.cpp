@@ -40,30 +40,49 @@ etpc_status check_mat(const Mat& m, int64_t rows, int64_t cols, int32_t dtype, b
   return ETPC_OK;
 }
 
-// Whether two matrices of the same shape share memory.  Rows of one stride may interleave:
-// columns of wider rows that do not meet are apart although their extents cross.
-bool overlap(const Mat& a, const Mat& b, int64_t rows, int64_t cols, int64_t size) {
-  if (a.p == nullptr || b.p == nullptr) return false;
-  const int64_t pa = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p));
-  const int64_t pb = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p));
-  const int64_t ea = rows > 1 ? (rows - 1) * a.stride : 0, eb = rows > 1 ? (rows - 1) * b.stride : 0;
-  if (pa + (ea + cols) * size <= pb || pb + (eb + cols) * size <= pa) return false;
-  if (rows > 1 && a.stride == b.stride && a.stride > 0 && (pb - pa) % size == 0) {
-    const int64_t s = a.stride, m = (((pb - pa) / size) % s + s) % s;
-    return m < cols || s - m < cols;
+// `rows` runs of `run` bytes, `pitch` bytes apart.
+struct Runs {
+  int64_t at, rows, run, pitch;
+};
+
+Runs runs_of(const Mat& m, int64_t rows, int64_t cols, int64_t size) {
+  const bool one = rows == 1 || m.stride == 0;
+  return Runs{static_cast<int64_t>(reinterpret_cast<uintptr_t>(m.p)), one ? 1 : rows, cols * size,
+              one ? 0 : m.stride * size};
+}
+
+// Whether the single run `one` meets a run of `many`: the first that ends past its start.
+bool meets(const Runs& one, const Runs& many) {
+  const int64_t left = one.at - many.at - many.run;
+  const int64_t r = left < 0 ? 0 : left / many.pitch + 1;
+  return r < many.rows && many.at + r * many.pitch < one.at + one.run;
+}
+
+// Whether two matrices share memory.  Extents may cross where runs do not meet: columns of
+// wider rows of one pitch, or a single row between the columns of others.
+bool overlap(const Runs& a, const Runs& b) {
+  if (a.at == 0 || b.at == 0) return false;
+  if (a.at + (a.rows - 1) * a.pitch + a.run <= b.at || b.at + (b.rows - 1) * b.pitch + b.run <= a.at) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (a.rows == 1) return meets(a, b);
+  if (b.rows == 1) return meets(b, a);
+  if (a.pitch == b.pitch) {
+    const int64_t s = a.pitch, m = ((b.at - a.at) % s + s) % s;
+    return m < a.run || s - m < b.run;
   }
   return true;
 }
 
 etpc_status check_apart(std::initializer_list<Mat> outs, std::initializer_list<Mat> ins, int64_t rows, int64_t cols,
                         int32_t dtype) {
+  const auto meet = [&](const Mat& p, const Mat& q) {
+    return overlap(runs_of(p, rows, cols, size_of(dtype)), runs_of(q, rows, cols, size_of(dtype)));
+  };
   for (const Mat* o = outs.begin(); o != outs.end(); ++o) {
     for (const Mat& i : ins)
-      if (overlap(*o, i, rows, cols, size_of(dtype)))
-        ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + i.name + " overlap");
+      if (meet(*o, i)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + i.name + " overlap");
     for (const Mat* q = outs.begin(); q != o; ++q)
-      if (overlap(*o, *q, rows, cols, size_of(dtype)))
-        ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + q->name + " overlap");
+      if (meet(*o, *q)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + q->name + " overlap");
   }
   return ETPC_OK;
 }

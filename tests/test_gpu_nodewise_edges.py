@@ -1,6 +1,6 @@
 """GPU checks of the node-wise operators where they can go wrong: rows that hold a NaN or an
 infinity, the stored mean of rows near zero, rows of 2^25 and
-more columns, against oracle/nodewise.py (float64).
+more columns, single rows between the columns of others, against oracle/nodewise.py (float64).
 
 `same` compares values that are not finite by kind: NaN with NaN, an infinity with the
 infinity of its sign.  u = 2^-24.
@@ -160,3 +160,30 @@ def test_gradients_of_rows_past_2_to_the_25(kind, cols):
     assert ((wb.double() - t.sum(0)).abs() <= 5 * U * t.abs().sum(0)).all()
     t = yb.double()
     assert ((bb.double() - t.sum(0)).abs() <= U * t.abs().sum(0)).all()
+
+
+# ---------------------------------------------------------------- where operands may lie
+
+def test_a_broadcast_row_between_the_columns_of_the_output():
+    """One row read for all rows may lie in the gap between two rows of the output: their
+    extents cross, their numbers do not.  One that meets a row is refused."""
+    etpc = _etpc()
+    rng = np.random.default_rng(2)
+    big = tensor(rng.standard_normal((23, 150)))
+    before = big.clone()
+    for r in (0, 7, 22):
+        big.copy_(before)
+        res, y = big[r:r + 1, 64:128].expand(23, 64), big[:, :64]
+        x = tensor(rng.standard_normal((23, 64)))
+        note(f"broadcast row {r} between the rows of y")
+        got = etpc.etpc_dropout_add_layer_norm(x, res, y=y, eps=EPS)
+        ref = etpc.etpc_dropout_add_layer_norm(x, res.contiguous(), eps=EPS)
+        assert got[0] is y and torch.equal(y, ref[0]) and torch.equal(got[1], ref[1])
+        assert torch.equal(big[:, 64:], before[:, 64:])
+        for meets in (big[r:r + 1, 63:127], big[r:r + 1, 0:64]):
+            with pytest.raises(etpc.EtpcError, match="overlap"):
+                etpc.etpc_dropout_add_layer_norm(x, meets.expand(23, 64), y=y, eps=EPS)
+    last = big.view(-1)[86:150]   # the gap before row 1: ends where the row starts
+    etpc.etpc_layer_norm(last.expand(23, 64), y=big[:, :64])
+    with pytest.raises(etpc.EtpcError, match="overlap"):
+        etpc.etpc_layer_norm(big.view(-1)[87:151].expand(23, 64), y=big[:, :64])
