@@ -45,11 +45,17 @@ struct Runs {
   int64_t at, rows, run, pitch;
 };
 
-Runs runs_of(const Mat& m, int64_t rows, int64_t cols, int64_t size) {
-  const bool one = rows == 1 || m.stride == 0;
-  return Runs{static_cast<int64_t>(reinterpret_cast<uintptr_t>(m.p)), one ? 1 : rows, cols * size,
-              one ? 0 : m.stride * size};
-}
+// An operand for the overlap check: a matrix, or n bytes (parameters, statistics, workspace).
+struct Operand {
+  const char* name;
+  Runs r;
+  Operand(const Mat& m, int64_t rows, int64_t cols, int64_t size)
+      : name(m.name), r{address(m.p), rows, cols * size, m.stride * size} {
+    if (rows == 1 || m.stride == 0) r.rows = 1, r.pitch = 0;
+  }
+  Operand(const char* what, const void* p, int64_t n) : name(what), r{address(p), 1, n, 0} {}
+  static int64_t address(const void* p) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)); }
+};
 
 // Whether the single run `one` meets a run of `many`: the first that ends past its start.
 bool meets(const Runs& one, const Runs& many) {
@@ -58,10 +64,10 @@ bool meets(const Runs& one, const Runs& many) {
   return r < many.rows && many.at + r * many.pitch < one.at + one.run;
 }
 
-// Whether two matrices share memory.  Extents may cross where runs do not meet: columns of
+// Whether two operands share memory (null ones do not).  Extents may cross where runs do not meet: columns of
 // wider rows of one pitch, or a single row between the columns of others.
 bool overlap(const Runs& a, const Runs& b) {
-  if (a.at == 0 || b.at == 0) return false;
+  if (a.at == 0 || b.at == 0 || a.run == 0 || b.run == 0) return false;
   if (a.at + (a.rows - 1) * a.pitch + a.run <= b.at || b.at + (b.rows - 1) * b.pitch + b.run <= a.at) return false;
   if (a.rows == 1 && b.rows == 1) return true;
   if (a.rows == 1) return meets(a, b);
@@ -73,17 +79,21 @@ bool overlap(const Runs& a, const Runs& b) {
   return true;
 }
 
-etpc_status check_apart(std::initializer_list<Mat> outs, std::initializer_list<Mat> ins, int64_t rows, int64_t cols,
-                        int32_t dtype) {
-  const auto meet = [&](const Mat& p, const Mat& q) {
-    return overlap(runs_of(p, rows, cols, size_of(dtype)), runs_of(q, rows, cols, size_of(dtype)));
-  };
-  for (const Mat* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Mat& i : ins)
-      if (meet(*o, i)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + i.name + " overlap");
-    for (const Mat* q = outs.begin(); q != o; ++q)
-      if (meet(*o, *q)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + q->name + " overlap");
+etpc_status check_apart(std::initializer_list<Operand> outs, std::initializer_list<Operand> ins) {
+  for (const Operand* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Operand& i : ins)
+      if (overlap(o->r, i.r)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + i.name + " overlap");
+    for (const Operand* q = outs.begin(); q != o; ++q)
+      if (overlap(o->r, q->r)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(o->name) + " and " + q->name + " overlap");
   }
+  return ETPC_OK;
+}
+
+// fp32 vectors; null ones pass.
+etpc_status check_floats(std::initializer_list<Operand> vectors) {
+  for (const Operand& v : vectors)
+    if (v.r.at % static_cast<int64_t>(sizeof(float)) != 0)
+      ETPC_FAIL(ETPC_ERR_INVALID_ARG, std::string(v.name) + " is not aligned to its elements");
   return ETPC_OK;
 }
 
@@ -91,6 +101,8 @@ etpc_status make_drop(const etpc_dropout_spec* d, DropArgs* out) {
   *out = DropArgs{};
   if (d == nullptr) return ETPC_OK;
   if (!(d->p >= 0.0 && d->p <= 1.0)) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "dropout probability must be in [0, 1]");
+  if (reinterpret_cast<uintptr_t>(d->offset_add) % sizeof(uint64_t) != 0)
+    ETPC_FAIL(ETPC_ERR_INVALID_ARG, "offset_add is not aligned to its element");
   const uint32_t t = static_cast<uint32_t>(std::nearbyint(65536.0 * d->p));
   out->threshold = t;
   out->scale = t < 65536u ? static_cast<float>(65536.0 / (65536.0 - t)) : 0.f;
@@ -136,7 +148,11 @@ etpc_status norm_forward(int64_t rows, int64_t cols, int32_t dtype, const Mat& x
   if (res.p != nullptr) ETPC_TRY(check_mat(res, rows, cols, dtype, false));
   ETPC_TRY(check_mat(y, rows, cols, dtype, true));
   if (h.p != nullptr) ETPC_TRY(check_mat(h, rows, cols, dtype, true));
-  ETPC_TRY(check_apart({y, h}, {x, res}, rows, cols, dtype));
+  const int64_t size = size_of(dtype);
+  const Operand ow{"w", w, 4 * cols}, ob{"b", b, 4 * cols}, om{"mean", mean, 4 * rows}, os{"rstd", rstd, 4 * rows};
+  ETPC_TRY(check_floats({ow, ob, om, os}));
+  ETPC_TRY(check_apart({{y, rows, cols, size}, {h, rows, cols, size}, om, os},
+                       {{x, rows, cols, size}, {res, rows, cols, size}, ow, ob, {"offset_add", a.drop.offset_add, 8}}));
   a.x = x.p, a.res = res.p, a.w = w, a.b = b;
   a.y = const_cast<void*>(y.p), a.h = const_cast<void*>(h.p), a.mean = mean, a.rstd = rstd;
   a.xs = x.stride, a.ress = res.stride, a.ys = y.stride, a.hs = h.stride;
@@ -164,10 +180,18 @@ etpc_status norm_backward(int64_t rows, int64_t cols, int32_t dtype, const Mat& 
   if (x_bar.p != nullptr) ETPC_TRY(check_mat(x_bar, rows, cols, dtype, true));
   if (res_bar.p != nullptr) ETPC_TRY(check_mat(res_bar, rows, cols, dtype, true));
   if (mean == nullptr || rstd == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null mean or rstd");
-  ETPC_TRY(check_apart({x_bar, res_bar}, {h, y_bar, h_bar}, rows, cols, dtype));
   a.rows = static_cast<int32_t>(rows), a.cols = static_cast<int32_t>(cols);
   const bool sums = w_bar != nullptr || b_bar != nullptr;
-  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, parts_bytes(norm_parts_most(a.rows, a.cols), 2 * cols)));
+  const size_t need = sums ? parts_bytes(norm_parts_most(a.rows, a.cols), 2 * cols) : 0;
+  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, need));
+  const int64_t size = size_of(dtype);
+  const Operand ow{"w", w, 4 * cols}, om{"mean", mean, 4 * rows}, os{"rstd", rstd, 4 * rows},
+      owb{"w_bar", w_bar, 4 * cols}, obb{"b_bar", b_bar, 4 * cols};
+  ETPC_TRY(check_floats({ow, om, os, owb, obb}));
+  ETPC_TRY(check_apart({{x_bar, rows, cols, size}, {res_bar, rows, cols, size}, owb, obb,
+                        {"the workspace", ws, static_cast<int64_t>(need)}},
+                       {{h, rows, cols, size}, {y_bar, rows, cols, size}, {h_bar, rows, cols, size}, ow, om, os,
+                        {"offset_add", a.drop.offset_add, 8}}));
   if (!sums && x_bar.p == nullptr && res_bar.p == nullptr) return ETPC_OK;
   a.h = h.p, a.y_bar = y_bar.p, a.h_bar = h_bar.p, a.mean = mean, a.rstd = rstd, a.w = w;
   a.x_bar = const_cast<void*>(x_bar.p), a.res_bar = const_cast<void*>(res_bar.p), a.w_bar = w_bar, a.b_bar = b_bar;
@@ -208,6 +232,10 @@ etpc_status make_table(int32_t n, const etpc_irrep* irreps, IrrepTable* t) {
 }
 
 Mat features(const char* name, const float* p, const IrrepTable& t) { return Mat{name, p, t.dim}; }
+Operand features(const Mat& m, int64_t n_nodes, const IrrepTable& t) {
+  return Operand{m.name, m.p, n_nodes * t.dim * int64_t{4}};
+}
+Operand floats(const char* name, const float* p, int64_t n) { return Operand{name, p, 4 * n}; }
 
 }  // namespace
 }  // namespace etpc
@@ -227,7 +255,9 @@ etpc_status etpc_dropout(int64_t n_rows, int64_t n_cols, int32_t dtype, const vo
   ETPC_TRY(check_mat(in, n_rows, n_cols, dtype, false));
   ETPC_TRY(check_mat(out, n_rows, n_cols, dtype, true));
   const bool in_place = x == y && (n_rows == 1 || x_stride == y_stride);
-  if (!in_place) ETPC_TRY(check_apart({out}, {in}, n_rows, n_cols, dtype));
+  const Operand src{in, n_rows, n_cols, size_of(dtype)}, dst{out, n_rows, n_cols, size_of(dtype)};
+  if (!in_place) ETPC_TRY(check_apart({dst}, {src}));
+  ETPC_TRY(check_apart({dst}, {{"offset_add", d.offset_add, 8}}));
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_dropout(x, x_stride, y, y_stride, static_cast<int32_t>(n_rows),
                                                  static_cast<int32_t>(n_cols), dtype, d, s));
   return ETPC_OK;
@@ -297,9 +327,11 @@ etpc_status etpc_irreps_dropout(int32_t n_blocks, const etpc_irrep* irreps, int3
   DropArgs d;
   ETPC_TRY(make_drop(drop, &d));
   if (n_nodes == 0 || t.n == 0) return ETPC_OK;
-  ETPC_TRY(check_mat(features("x", x, t), n_nodes, t.dim, ETPC_F32, false));
-  ETPC_TRY(check_mat(features("y", y, t), n_nodes, t.dim, ETPC_F32, true));
-  if (x != y) ETPC_TRY(check_apart({features("y", y, t)}, {features("x", x, t)}, n_nodes, t.dim, ETPC_F32));
+  const Mat mx = features("x", x, t), my = features("y", y, t);
+  ETPC_TRY(check_mat(mx, n_nodes, t.dim, ETPC_F32, false));
+  ETPC_TRY(check_mat(my, n_nodes, t.dim, ETPC_F32, true));
+  if (x != y) ETPC_TRY(check_apart({features(my, n_nodes, t)}, {features(mx, n_nodes, t)}));
+  ETPC_TRY(check_apart({features(my, n_nodes, t)}, {{"offset_add", d.offset_add, 8}}));
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_irreps_dropout(t, x, y, n_nodes, d, s));
   return ETPC_OK;
 }
@@ -311,9 +343,13 @@ etpc_status etpc_irreps_norm(int32_t n_blocks, const etpc_irrep* irreps, int32_t
   ETPC_TRY(check_eps(eps));
   if (n_nodes < 0) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "negative n_nodes");
   if (n_nodes == 0 || t.n == 0) return ETPC_OK;
-  ETPC_TRY(check_mat(features("x", x, t), n_nodes, t.dim, ETPC_F32, false));
-  ETPC_TRY(check_mat(features("y", y, t), n_nodes, t.dim, ETPC_F32, true));
-  ETPC_TRY(check_apart({features("y", y, t)}, {features("x", x, t)}, n_nodes, t.dim, ETPC_F32));
+  const Mat mx = features("x", x, t), my = features("y", y, t);
+  ETPC_TRY(check_mat(mx, n_nodes, t.dim, ETPC_F32, false));
+  ETPC_TRY(check_mat(my, n_nodes, t.dim, ETPC_F32, true));
+  const Operand ow = floats("w", w, t.channels), ob = floats("b", b, t.biases),
+                os = floats("stats", stats, int64_t{2} * n_nodes * t.n);
+  ETPC_TRY(check_floats({ow, ob, os}));
+  ETPC_TRY(check_apart({features(my, n_nodes, t), os}, {features(mx, n_nodes, t), ow, ob}));
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_irreps_norm_fwd(t, x, w, b, eps, y, stats, n_nodes, s));
   return ETPC_OK;
 }
@@ -346,9 +382,14 @@ etpc_status etpc_irreps_norm_backward(int32_t n_blocks, const etpc_irrep* irreps
   ETPC_TRY(check_mat(my, n_nodes, t.dim, ETPC_F32, false));
   if (x_bar != nullptr) ETPC_TRY(check_mat(mo, n_nodes, t.dim, ETPC_F32, true));
   if (stats == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null stats");
-  ETPC_TRY(check_apart({mo}, {mx, my}, n_nodes, t.dim, ETPC_F32));
   const bool sums = w_bar != nullptr || b_bar != nullptr;
-  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, static_cast<size_t>(irreps_norm_part_floats(t, n_nodes)) * sizeof(float)));
+  const int64_t part_floats = sums ? irreps_norm_part_floats(t, n_nodes) : 0;
+  if (sums) ETPC_TRY(check_parts(ws, ws_bytes, static_cast<size_t>(part_floats) * sizeof(float)));
+  const Operand ow = floats("w", w, t.channels), os = floats("stats", stats, int64_t{2} * n_nodes * t.n),
+                owb = floats("w_bar", w_bar, t.channels), obb = floats("b_bar", b_bar, t.biases);
+  ETPC_TRY(check_floats({ow, os, owb, obb}));
+  ETPC_TRY(check_apart({features(mo, n_nodes, t), owb, obb, floats("the workspace", static_cast<const float*>(ws), part_floats)},
+                       {features(mx, n_nodes, t), features(my, n_nodes, t), ow, os}));
   if (!sums && x_bar == nullptr) return ETPC_OK;
   float* part = static_cast<float*>(ws);
   ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_irreps_norm_bwd(t, x, y_bar, stats, w, x_bar, w_bar, b_bar, part, n_nodes, s));

@@ -331,9 +331,10 @@ etpc_status etpc_double_backward(etpc_plan plan, const etpc_graph* graph, const 
  * at pointer + r * stride elements, so a block of wider rows (the scalars inside ir_mul
  * feature rows) is passed in place.  An input's stride is 0 (one row for all) or at least
  * n_cols, an output's at least n_cols; pointers are aligned to the element, no more.
- * Outputs do not overlap inputs or one another (etpc_dropout may work in place).  Gains,
- * biases, statistics and the gradients of parameters are fp32 and contiguous whatever the
- * dtype; sums are taken in fp32 and each result is rounded to the dtype once.
+ * Outputs (statistics, gradients of parameters and the workspace among them) do not overlap
+ * inputs or one another; etpc_dropout may work in place.  Gains, biases, statistics and the
+ * gradients of parameters are fp32 and contiguous whatever the dtype; sums are taken in fp32
+ * and each result is rounded to the dtype once.
  * n_rows < 2^31 and n_cols <= 2^30, else ETPC_ERR_OVERFLOW.  No rows is no work (parameter
  * gradients are then zero). */
 typedef enum { ETPC_F32 = 0, ETPC_BF16 = 1, ETPC_F16 = 2 } etpc_dtype;

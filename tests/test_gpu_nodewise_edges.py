@@ -187,3 +187,25 @@ def test_a_broadcast_row_between_the_columns_of_the_output():
     etpc.etpc_layer_norm(last.expand(23, 64), y=big[:, :64])
     with pytest.raises(etpc.EtpcError, match="overlap"):
         etpc.etpc_layer_norm(big.view(-1)[87:151].expand(23, 64), y=big[:, :64])
+
+
+def test_statistics_in_the_gaps_of_feature_rows():
+    """Statistics and parameter gradients as parts of one buffer, and in the columns that a
+    strided matrix leaves free, are apart from it and from one another."""
+    etpc = _etpc()
+    rng = np.random.default_rng(4)
+    n, cols = 12, 40
+    x, yb = tensor(rng.standard_normal((n, cols))), tensor(rng.standard_normal((n, cols)))
+    w = tensor(rng.standard_normal(cols))
+    ref = etpc.etpc_layer_norm(x, w, eps=EPS)
+    big = torch.zeros(n, 80, device="cuda")
+    note("statistics beside y")
+    got = etpc.etpc_layer_norm(x, w, y=big[:, :cols], mean=big[3, 40:52], rstd=big[11, 68:80], eps=EPS)
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    _, wb, bb = etpc.etpc_layer_norm_backward(x, yb, ref[1], ref[2], w)
+    flat = torch.zeros(2 * cols, device="cuda")
+    outs = (big[:, 40:], flat[:cols], flat[cols:])
+    etpc.etpc_layer_norm_backward(x, yb, ref[1], ref[2], w, outs=outs)
+    assert torch.equal(outs[1], wb) and torch.equal(outs[2], bb)
+    with pytest.raises(etpc.EtpcError, match="overlap"):
+        etpc.etpc_layer_norm_backward(x, yb, ref[1], ref[2], w, outs=(None, flat[:cols], flat[cols - 1:-1]))
