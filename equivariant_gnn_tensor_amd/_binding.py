@@ -699,7 +699,7 @@ def etpc_dropout(x, p: float, seed: int, offset=0, y=None, stream=None) -> torch
     return y
 
 
-def _norm_forward(x, residual, drop, w, b, eps, y, h, join, stats, mean, rstd, stream):
+def _norm_forward(x, residual, drop, w, b, eps, y, h, join, keep_h, stats, mean, rstd, stream):
     dtype, dev = _row_type(x), x.device
     handle = _check_device("x", x, stream)
     xp, xs, rows, cols = _rows("x", x)
@@ -721,7 +721,7 @@ def _norm_forward(x, residual, drop, w, b, eps, y, h, join, stats, mean, rstd, s
     wp, bp = _vector("w", w, cols, dev), _vector("b", b, cols, dev)
     if join:
         rp, rs = _rows_like("residual", residual, x)
-        if h is None:
+        if h is None and keep_h:
             h = _new_like(x, stream)
             hp, hs = h.data_ptr(), cols
         else:
@@ -739,7 +739,7 @@ def etpc_layer_norm(x, w=None, b=None, eps: float = 1e-5, y=None, mean=None, rst
                     stream=None):
     """(y, mean, rstd): y = (x - mean) rstd w + b over the rows x [..., C].  stats=False skips
     the statistics (inference) and returns (y, None, None)."""
-    y, _, mean, rstd = _norm_forward(x, None, None, w, b, eps, y, None, False, stats, mean, rstd, stream)
+    y, _, mean, rstd = _norm_forward(x, None, None, w, b, eps, y, None, False, False, stats, mean, rstd, stream)
     return y, mean, rstd
 
 
@@ -808,10 +808,11 @@ def etpc_layer_norm_backward(x, y_bar, mean, rstd, w=None, want=("x", "w", "b"),
 
 def etpc_dropout_add_layer_norm(x, residual, w=None, b=None, p: float = 0.0, seed: int = 0, offset=0,
                                 eps: float = 1e-5, y=None, h=None, mean=None, rstd=None, stats: bool = True,
-                                stream=None):
-    """(y, h, mean, rstd): h = residual + dropout(x) (residual may be None), y = layer_norm(h)."""
+                                stream=None, keep_h: bool = True):
+    """(y, h, mean, rstd): h = residual + dropout(x) (residual may be None), y = layer_norm(h).
+    stats=False skips the statistics and keep_h=False writing h (inference): None instead."""
     drop = _drop_spec(p, seed, offset, x.device)
-    return _norm_forward(x, residual, drop, w, b, eps, y, h, True, stats, mean, rstd, stream)
+    return _norm_forward(x, residual, drop, w, b, eps, y, h, True, keep_h, stats, mean, rstd, stream)
 
 
 def etpc_dropout_add_layer_norm_backward(h, y_bar, mean, rstd, w=None, h_bar=None, p: float = 0.0, seed: int = 0,

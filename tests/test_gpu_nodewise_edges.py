@@ -209,3 +209,25 @@ def test_statistics_in_the_gaps_of_feature_rows():
     assert torch.equal(outs[1], wb) and torch.equal(outs[2], bb)
     with pytest.raises(etpc.EtpcError, match="overlap"):
         etpc.etpc_layer_norm_backward(x, yb, ref[1], ref[2], w, outs=(None, flat[:cols], flat[cols - 1:-1]))
+
+
+# ---------------------------------------------------------------- outputs left out
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cols", [7, 64, 577, 2048, 18000])
+def test_join_without_its_sum(kind, cols):
+    """keep_h=False (a forward pass with no backward) leaves h out and changes nothing else."""
+    etpc = _etpc()
+    torch.manual_seed(cols)
+    x, res = torch.randn(37, cols, device="cuda").to(kind), torch.randn(37, cols, device="cuda").to(kind)
+    w = torch.randn(cols, device="cuda")
+    note(f"join without h, {kind} cols={cols}")
+    for p in (0.0, 0.3):
+        y, h, mean, rstd = etpc.etpc_dropout_add_layer_norm(x, res, w, p=p, seed=3, offset=4)
+        got = etpc.etpc_dropout_add_layer_norm(x, res, w, p=p, seed=3, offset=4, keep_h=False)
+        assert got[1] is None and torch.equal(got[0], y) and torch.equal(got[2], mean) and torch.equal(got[3], rstd)
+        got = etpc.etpc_dropout_add_layer_norm(x, res, w, p=p, seed=3, offset=4, keep_h=False, stats=False)
+        assert got[1:] == (None, None, None) and torch.equal(got[0], y)
+        given = torch.empty_like(x)   # a given h is written all the same
+        got = etpc.etpc_dropout_add_layer_norm(x, res, w, p=p, seed=3, offset=4, h=given, keep_h=False)
+        assert got[1] is given and torch.equal(given, h)
