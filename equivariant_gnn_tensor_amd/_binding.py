@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 import os
 import re
 from typing import Dict, List, Optional, Sequence, Tuple
@@ -675,11 +676,12 @@ def _drop_spec(p: float, seed: int, offset, device) -> etpc_dropout_spec:
     """offset: a whole number, or a one-element int64 tensor on the GPU that is read when the
     kernel runs (what a captured graph needs for a fresh mask in every replay)."""
     m64 = (1 << 64) - 1
+    seed = operator.index(seed)   # numpy's whole numbers do not go with a mask of 64 bits
     if isinstance(offset, torch.Tensor):
         if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != device:
             raise ValueError(f"an offset tensor is one int64 number on {device}")
         return etpc_dropout_spec(p, seed & m64, 0, offset.data_ptr())
-    return etpc_dropout_spec(p, seed & m64, offset & m64, None)
+    return etpc_dropout_spec(p, seed & m64, operator.index(offset) & m64, None)
 
 
 def etpc_dropout(x, p: float, seed: int, offset=0, y=None, stream=None) -> torch.Tensor:

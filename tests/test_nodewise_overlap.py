@@ -1,8 +1,9 @@
-"""Refusals of operands of the node-wise operators that share memory or are not aligned (no
-GPU): every call fails its checks on the host before anything is enqueued, so its
-placeholder pointers are never read."""
+"""Refusals of operands of the node-wise operators that share memory or are not aligned, and
+whole numbers as seeds (no GPU).  Every call fails its checks on the host before anything is
+enqueued, so its placeholder pointers are never read."""
 import ctypes as C
 
+import numpy as np
 import pytest
 
 import equivariant_gnn_tensor_amd as etpc
@@ -98,3 +99,16 @@ def test_irreps_norm_backward(kwargs, words):
     st = lib.etpc_irreps_norm_backward(2, IR, ROWS, X, H, a["stats"], a["w"], a["x_bar"], a["w_bar"], a["b_bar"], a["ws"],
                                        IR_NEED, None)
     refused(st, "overlap" if "aligned" not in words else "aligned", *words)
+
+
+@pytest.mark.parametrize("kind", [int, np.int64, np.uint64, np.int32, np.uint8])
+def test_whole_numbers_as_seed_and_offset(kind):
+    """Any whole number is a seed or an offset, taken modulo 2^64."""
+    s = _binding._drop_spec(0.5, kind(7), kind(9), None)
+    assert (s.p, s.seed, s.offset, s.offset_add) == (0.5, 7, 9, None)
+    if kind not in (np.uint64, np.uint8):
+        s = _binding._drop_spec(0.5, kind(-1), kind(-2), None)
+        assert (s.seed, s.offset) == ((1 << 64) - 1, (1 << 64) - 2)
+    for seed, offset in ((1.0, 2), (1, 2.0), ("1", 2)):
+        with pytest.raises(TypeError):
+            _binding._drop_spec(0.5, seed, offset, None)
