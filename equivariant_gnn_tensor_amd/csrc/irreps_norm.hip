@@ -41,7 +41,7 @@ __host__ __device__ inline int lanes_of(int mul) {
 // channel, lanes would read runs shorter than a cache line.  Below 24 channels backward
 // (27542 nodes of 192x0e+8x2e+53x0e+32x1e+8x3o+6x1e 64 us -> 42; 36350 of 10x2o+48x3o+16x1e
 // 62 -> 49, with 16 the bound 57), below 16 forward (25985 nodes of 88x0o+8x3o+8x1o+24x3o+
-// 24x2o+88x0e 37.7 -> 32.8, 60000 of 16x0e+16x1o+16x2e 14.7, with 24 the bound 16.8).
+// 24x2o+88x0e 38 -> 34, 60000 of 16x0e+16x1o+16x2e 14.7, with 24 the bound 16.8).
 constexpr int kFwdFlat = 16, kBwdFlat = 24;
 __host__ __device__ inline bool is_flat(const IrrepBlock& b, int below) { return b.l == 0 || b.mul < below; }
 // What the lanes of a group span: numbers of the segment, or channels.
@@ -214,7 +214,7 @@ __device__ inline void fwd_block(const IrrepTable& t, int k, int p, int parts, c
         for (int i = 0; i < I; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s += span.counts(i, j) ? v[r][0][i][j] : 0.f;
-        mean = sum_lanes(s, G) / static_cast<float>(mul);   // exact for a constant row
+        mean = sum_lanes(s, G) / static_cast<float>(mul);   // one rounding, s * (1 / n) has two
         s = 0.f;
       }
 #pragma unroll

@@ -131,8 +131,9 @@ __device__ inline int group_index() {
 
 // Read and write one row after another, no prefetch: waves enough are in flight, and fetching
 // a row ahead measured slower (65536 x 512 bf16 24.8 us without, 28 to 30 with).
-// What it reaches (reads and writes): 65536 x 512 bf16 23.0 us, 5.9 TB/s; 8192 x 2048 fp32
-// 26.1 us, 5.1 TB/s; join 65408 x 1024 bf16 98.8 us, 5.4 TB/s.  A large copy runs at 5.1 to 5.4.
+// What it reaches (reads and writes): 65536 x 512 bf16 23.2 us, 5.8 TB/s; 8192 x 2048 fp32
+// 26.4 us, 5.1 TB/s; join 65408 x 1024 bf16 98.6 us, 5.4 TB/s.  A copy of the same bytes runs
+// at 5.5, 5.5 and 5.4.
 template <class T, int G, int V, bool kEven, bool kJoin>
 __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs a) {
   constexpr int kRows = fwd_threads<G>() / G;
@@ -177,7 +178,7 @@ __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[0] += span.counts(i, k) ? v[i][k] : 0.f;
     group_sum<G, kRows>(s, lds, half);
-    const float mean = s[0] / static_cast<float>(a.cols);   // exact for a constant row, unlike s * (1 / n)
+    const float mean = s[0] / static_cast<float>(a.cols);   // one rounding, s * (1 / n) has two
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -204,8 +205,8 @@ __global__ __launch_bounds__(fwd_threads<G>()) void fwd_kernel(const NormFwdArgs
 // address is odd in elements takes about three cycles a lane, so two streams of them bound the
 // backward pass of long rows (32768 rows of 2047 bf16: 104 us).  With kOdd such a vector is
 // read one element lower, or one higher where it starts the row, and its eighth element on
-// its own: everything stays inside the row, which has nine elements at least (83 us; 8000 x
-// 4097 79 -> 69; rows up to 1024 columns gain nothing: 100000 x 65 13.8 -> 15.1).
+// its own: everything stays inside the row, which has nine elements at least (83 us; rows up
+// to 1024 columns gain nothing: 100000 x 65 13.8 -> 15.1).
 template <class T, bool kOdd>
 struct Raw8 {
   Vec8<T> t;
@@ -266,8 +267,8 @@ struct Operands {
 // than more registers a thread (8192 x 4096 fp16: 512 threads of one vector 54.6 us, 256 of
 // two 81.4), the prefetch then gave 44.9.  Rows past 8192 columns need two vectors for 1024
 // threads, whose sums then live in LDS (each thread its own places).
-// What it reaches, sums included: 8192 x 4096 fp16 43.4 us, 4.6 TB/s; 65536 x 512 bf16
-// 40.5 us, 5.0 TB/s; join 65408 x 1024 bf16 133 us, 5.0 TB/s; 32768 x 2047 bf16 83 us, 4.9 TB/s.
+// What it reaches, sums included: 8192 x 4096 fp16 43.2 us, 4.7 TB/s; 65536 x 512 bf16
+// 41.0 us, 4.9 TB/s; join 65408 x 1024 bf16 131 us, 5.1 TB/s; 32768 x 2047 bf16 83 us, 4.9 TB/s.
 template <class T, int G, int V, bool kEven, bool kJoin, bool kOdd>
 __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const NormBwdArgs a) {
   constexpr int kRows = bwd_threads<G>() / G;
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(kLong) void fwd_long_kernel(const NormFwdArgs a) {
       s[0] += t;
     }
     group_sum<kLong, 1>(s, lds, half);
-    const float mean = s[0] / static_cast<float>(n);   // exact for a constant row, unlike s * (1 / n)
+    const float mean = s[0] / static_cast<float>(n);   // one rounding, s * (1 / n) has two
     float q[2] = {0.f, 0.f};
     for (int64_t c = 8 * threadIdx.x; c < n; c += 8 * kLong) {
       float v[8], t0 = 0.f, t1 = 0.f;
@@ -541,9 +542,10 @@ __global__ __launch_bounds__(kThreads) void bwd_long_cols_kernel(const NormBwdAr
 // ---------------------------------------------------------------- launch shapes
 // Threads per row and vectors of eight columns per thread, from the row length and the
 // element size: the smallest group that holds the row.  Forward, 16-bit rows past 64 columns
-// take two vectors a thread (32768 x 1024 bf16: 23 us with two, 28 to 32 with one; 8192 x
-// 4096 fp16: 27.5 us with two, 32.3 with four), fp32 rows past 512 (8192 x 2048: 22.9 us with
-// two, 27.3 with four; one and two are level, two halves the waves at a barrier).
+// take two vectors a thread (32768 x 1024 bf16: 24.3 us with two, 28.9 with one, 25.7 with
+// four; 8192 x 4096 fp16: 26.0 with two, 30.5 with one, 28.6 with four), fp32 rows past 512
+// (one and two are level, two halves the waves at a barrier: 8192 x 2048 26.4 us with two,
+// 26.5 with one, 27.6 with four; 4096 x 4096 25.7, 26.6, 27.6; 16384 x 1024 27.0, 25.6, 27.1).
 template <int kSize, class F>
 auto fwd_shape(int32_t cols, F&& f) {
   if (cols <= 8) return f.template operator()<1, 1>();
@@ -595,7 +597,10 @@ auto bwd_shape(int32_t cols, F&& f) {
 // as are resident at once (8192 x 4096 fp16: 25.1 us with 24, 28.1 with 32, 27.4 with 64).
 // Otherwise 64, more than fit, so that a CU whose rows are done takes others (100000 x 256
 // bf16: 17.3 us with 64, 18.1 with 32, 18.4 with 24; the join of 8192 x 4096 bf16: 50.6 with
-// 64, 52.7 with 32, 53.4 with 24).
+// 64, 52.7 with 32, 53.4 with 24).  Groups of up to 8 lanes, 64 against 32: 400000 x 128 bf16
+// 38.4 and 41.0 us, 400000 x 32 fp32 18.0 and 19.1, 214980 x 64 bf16 11.0 and 11.1, 65408 x 64
+// fp32 of rows of 576 8.1 and 8.1, the join of 214980 x 128 bf16 41.4 and 44.4; 32 is the
+// faster for 100000 x 64 fp32 (10.8 and 10.1) and rows of 8 (1000000 fp32 13.6 and 12.5).
 template <int G, bool kJoin>
 constexpr int fwd_waves() {
   return 256 * (G <= 64 || kJoin ? 64 : G < 1024 ? 24 : 32);

@@ -371,7 +371,10 @@ etpc_status etpc_layer_norm(int64_t n_rows, int64_t n_cols, int32_t dtype, const
 /* Workspace of both backward calls below: partial sums of the parameter gradients. */
 etpc_status etpc_layer_norm_workspace_size(int64_t n_rows, int64_t n_cols, size_t* bytes);
 /* Gradients of <y_bar, y>, from the forward pass's x, mean and rstd.  x_bar, w_bar, b_bar:
- * NULL skips.  Sums over rows have a fixed order. */
+ * NULL skips.  Sums over rows have a fixed order.  Rows are centred again with the fp32 mean,
+ * which is off by up to 2^-24 of itself: (x - mean) rstd is here off by that times
+ * |mean| rstd (6e-3 for a mean 1e5 spreads from zero), while the forward pass also takes out
+ * what its rounded mean leaves. */
 etpc_status etpc_layer_norm_backward(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride,
                                      const void* y_bar, int64_t y_bar_stride, const float* mean, const float* rstd,
                                      const float* w, void* x_bar, int64_t x_bar_stride, float* w_bar, float* b_bar,
