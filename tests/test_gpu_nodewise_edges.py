@@ -1,6 +1,6 @@
-"""GPU checks of the node-wise operators where they can go wrong: rows that hold a NaN or an
-infinity, the stored mean of rows near zero, rows of 2^25 and
-more columns, single rows between the columns of others, against oracle/nodewise.py (float64).
+"""GPU checks of the node-wise operators where they can go wrong, against oracle/nodewise.py
+(float64): rows that hold a NaN or an infinity, the stored mean of rows near zero, rows of
+2^25 and more columns, single rows between the columns of others, outputs left out.
 
 `same` compares values that are not finite by kind: NaN with NaN, an infinity with the
 infinity of its sign.  u = 2^-24.
