@@ -82,6 +82,7 @@ SYMBOLS = (
     "etpc_dropout", "etpc_layer_norm", "etpc_layer_norm_workspace_size", "etpc_layer_norm_backward",
     "etpc_dropout_add_layer_norm", "etpc_dropout_add_layer_norm_backward", "etpc_irreps_dims", "etpc_irreps_dropout",
     "etpc_irreps_norm", "etpc_irreps_norm_workspace_size", "etpc_irreps_norm_backward",
+    "etpc_linear", "etpc_linear_workspace_size", "etpc_linear_backward",
 )
 KINDS = ("csr", "fwd_traverse", "channel_gemm", "bwd_traverse", "node_gemm", "aux", "prep", "nodewise")
 
@@ -132,6 +133,10 @@ def _load():
         "etpc_irreps_norm": [i32, ir, i32, vp, vp, vp, f32, vp, vp, vp],
         "etpc_irreps_norm_workspace_size": [i32, ir, i32, P(sz)],
         "etpc_irreps_norm_backward": [i32, ir, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "etpc_linear": [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, i64, vp],
+        "etpc_linear_workspace_size": [i64, i64, i64, i32, i32, P(sz)],
+        "etpc_linear_backward": [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i64,
+                                 vp, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -950,6 +955,133 @@ def etpc_irreps_norm_backward(irreps, x, y_bar, stats, w=None, want=("x", "w", "
     wsp, wsn, _keep = _scratch(ws, need, dev, stream)
     st = lib.etpc_irreps_norm_backward(ir.n, ir.c, n, xp, yp, _vector("stats", stats, 2 * n * ir.n, dev),
                                        _vector("w", w, ir.channels, dev), xbp, wbp, bbp, wsp, wsn, handle)
+    if st:
+        _check(st)
+    return x_bar, w_bar, b_bar
+
+
+# ---------------------------------------------------------------- feed-forward operators
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "tanh": 4}   # etpc_act
+
+
+def _act_code(act: str) -> int:
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
+    return code
+
+
+def _rows_of(name: str, t: torch.Tensor, lead, cols: int, like: torch.Tensor) -> Tuple[int, int]:
+    """(pointer, row stride) of a tensor of shape [*lead, cols] and like's type and device."""
+    if t.shape[:-1] != lead or t.shape[-1] != cols:
+        raise ValueError(f"{name} must have shape {(*lead, cols)}, got {tuple(t.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    return _rows(name, t)[:2]
+
+
+def _weights(name: str, w: torch.Tensor, like: torch.Tensor) -> Tuple[int, int, int, int, int]:
+    """(pointer, strides, inputs, outputs) of a weight matrix; one of its axes is contiguous."""
+    if w.dim() != 2:
+        raise ValueError(f"{name} must have shape (n_in, n_out), got {tuple(w.shape)}")
+    if w.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {w.dtype}")
+    if w.device != like.device:
+        raise ValueError(f"{name} is on {w.device}, expected {like.device}")
+    (n_in, n_out), (si, so) = w.shape, w.stride()
+    if so != 1 and si != 1 and n_in > 1 and n_out > 1:
+        raise ValueError(f"{name}: one of the axes must be contiguous")
+    return w.data_ptr(), si, so, n_in, n_out
+
+
+def _new_rows(lead, cols, like, stream) -> torch.Tensor:
+    """A contiguous output [*lead, cols] of like's type, allocated on the call's stream."""
+    if stream is None:
+        return torch.empty((*lead, cols), dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(_torch_stream(stream, like.device)):
+        return torch.empty((*lead, cols), dtype=like.dtype, device=like.device)
+
+
+def etpc_linear(x, w, b=None, residual=None, act: str = "none", y=None, z=None, keep_z: bool = True, stream=None):
+    """(y, z): z = x w + b, y = act(z) + residual over the rows x [..., n_in]; w [n_in, n_out] with
+    either axis contiguous (a transposed view of [n_out, n_in] weights goes in place), b f32.  act:
+    "none", "relu", "silu", "gelu" or "tanh".  z is what the backward pass reads; it is None for
+    "none" and with keep_z=False (inference), unless the caller gives one."""
+    dtype, code, dev = _row_type(x), _act_code(act), x.device
+    handle = _check_device("x", x, stream)
+    xp, xs, rows, cols = _rows("x", x)
+    wp, wi, wo, n_in, n_out = _weights("w", w, x)
+    if cols != n_in:
+        raise ValueError(f"x has {cols} columns, w {n_in} inputs")
+    lead = x.shape[:-1]
+    if y is None:
+        y = _new_rows(lead, n_out, x, stream)
+        yp, ys = y.data_ptr(), n_out
+    else:
+        yp, ys = _rows_of("y", y, lead, n_out, x)
+    if z is not None:
+        zp, zs = _rows_of("z", z, lead, n_out, x)
+    elif code and keep_z:
+        z = _new_rows(lead, n_out, x, stream)
+        zp, zs = z.data_ptr(), n_out
+    else:
+        zp, zs = None, 0
+    rp, rs = (None, 0) if residual is None else _rows_of("residual", residual, lead, n_out, x)
+    st = lib.etpc_linear(rows, n_in, n_out, dtype, xp, xs, wp, wi, wo, _vector("b", b, n_out, dev), rp, rs, code, yp, ys,
+                         zp, zs, handle)
+    if st:
+        _check(st)
+    return y, z
+
+
+@functools.lru_cache(maxsize=512)
+def _linear_ws(n_rows: int, n_in: int, n_out: int, dtype: int, act: int) -> int:
+    b = C.c_size_t()
+    _check(lib.etpc_linear_workspace_size(n_rows, n_in, n_out, dtype, act, b))
+    return b.value
+
+
+def etpc_linear_workspace_size(n_rows: int, n_in: int, n_out: int, dtype=torch.float32, act: str = "none") -> int:
+    if dtype not in _ROW_TYPES:
+        raise TypeError(f"rows must be float32, bfloat16 or float16, got {dtype}")
+    return _linear_ws(n_rows, n_in, n_out, _ROW_TYPES[dtype], _act_code(act))
+
+
+def etpc_linear_backward(x, w, y_bar, z=None, act: str = "none", want=("x", "w", "b"), outs=None, ws=None, stream=None):
+    """(x_bar, w_bar, b_bar) of <y_bar, y>; None for what `want` leaves out (the residual's
+    gradient is y_bar).  z as the forward call gave it, act the same.  x_bar and w_bar have x's
+    type, b_bar is f32; a new w_bar is laid out like w.  outs: three caller-given tensors (or None
+    to skip one)."""
+    dtype, code, dev = _row_type(x), _act_code(act), x.device
+    handle = _check_device("x", x, stream)
+    xp, xs, rows, cols = _rows("x", x)
+    wp, wi, wo, n_in, n_out = _weights("w", w, x)
+    if cols != n_in:
+        raise ValueError(f"x has {cols} columns, w {n_in} inputs")
+    lead = x.shape[:-1]
+    yp, ys = _rows_of("y_bar", y_bar, lead, n_out, x)
+    if code and z is None:
+        raise ValueError(f"the gradient through {act} needs z")
+    zp, zs = _rows_of("z", z, lead, n_out, x) if code else (None, 0)
+    x_bar, xbp, xbs = _bar_like("x_bar", want, "x", outs, 0, x, cols, stream)
+    wbp, wbi, wbo = None, 0, 0
+    if outs is not None:
+        w_bar = outs[1]
+        if w_bar is not None:
+            if w_bar.shape != w.shape:
+                raise ValueError(f"w_bar must have shape {tuple(w.shape)}, got {tuple(w_bar.shape)}")
+            wbp, wbi, wbo = _weights("w_bar", w_bar, x)[:3]
+    elif "w" in want:
+        w_bar = _new_rows((n_in,), n_out, x, stream) if wo == 1 or n_out == 1 else _new_rows((n_out,), n_in, x, stream).t()
+        wbp, (wbi, wbo) = w_bar.data_ptr(), w_bar.stride()
+    else:
+        w_bar = None
+    b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 2, n_out, dev, stream)
+    wsp, wsn, _keep = _scratch(ws, _linear_ws(rows, n_in, n_out, dtype, code), dev, stream)
+    st = lib.etpc_linear_backward(rows, n_in, n_out, dtype, xp, xs, wp, wi, wo, yp, ys, zp, zs, code, xbp, xbs, wbp, wbi,
+                                  wbo, bbp, wsp, wsn, handle)
     if st:
         _check(st)
     return x_bar, w_bar, b_bar

@@ -1,0 +1,173 @@
+// The dense layer beside its products: shapes of the products, the gradient through the
+// activation with the bias's gradient, and sums of partial results.
+#include <algorithm>
+
+#include "activation.hpp"
+#include "linear.hpp"
+#include "rows.hpp"
+
+namespace etpc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxGroups = int64_t{1} << 20;
+
+// ---- z_bar = y_bar act'(z) and its column sums
+// Memory bound: one pass, eight columns a thread, G threads along a row and 256 / G rows at a
+// time.  A workgroup keeps its columns' sums in registers over all its rows and leaves one row
+// of them; they are added up in a fixed order afterwards.
+struct SlopeShape {
+  int g;        // threads along a row
+  int groups;   // workgroups along a row
+  int parts;
+};
+SlopeShape slope_shape(int32_t rows, int32_t cols) {
+  const int vecs = (cols + 7) / 8;
+  SlopeShape s{8, 1, 1};
+  while (s.g < kThreads && s.g < vecs) s.g *= 2;
+  s.groups = (vecs + s.g - 1) / s.g;
+  const int per = kThreads / s.g;
+  const int units = (rows + per - 1) / per;
+  s.parts = std::max(1, std::min((units + 3) / 4, 1024 / s.groups));
+  return s;
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void slope_kernel(const SlopeArgs a, const SlopeShape sh) {
+  __shared__ float lds[kThreads][8];
+  const int part = blockIdx.x / sh.groups, group = blockIdx.x - part * sh.groups;
+  const int lane = threadIdx.x & (sh.g - 1), row = threadIdx.x / sh.g, per = kThreads / sh.g;
+  const int c = (group * sh.g + lane) * 8;
+  float sum[8] = {};
+  if (c < a.cols) {
+    const int64_t step = static_cast<int64_t>(per) * sh.parts;
+    for (int64_t r = static_cast<int64_t>(part) * per + row; r < a.rows; r += step) {
+      float v[8], z[8];
+      load<8, false>(static_cast<const T*>(a.y_bar) + r * a.ybs, c, a.cols, v);
+      if (a.z != nullptr) {
+        load<8, false>(static_cast<const T*>(a.z) + r * a.zs, c, a.cols, z);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= slope<sizeof(T) == 4>(z[k], a.act);
+      }
+      if (a.z_bar != nullptr) store<8, false>(static_cast<T*>(a.z_bar) + r * a.zbs, c, a.cols, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += c + k < a.cols ? v[k] : 0.f;
+    }
+  }
+  if (a.part == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) lds[threadIdx.x][k] = sum[k];
+  __syncthreads();
+  if (row == 0 && c < a.cols) {
+    for (int i = 1; i < per; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += lds[i * sh.g + lane][k];
+    store<8, false>(a.part + static_cast<int64_t>(part) * a.cols, c, a.cols, sum);
+  }
+}
+
+// ---- sums of partial results
+// kSlices threads share a number's parts: each takes every kSlices-th in order, then the slices
+// in order.
+template <class T, int kSlices>
+__global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float* __restrict__ part, int parts, int64_t rows,
+                                                             int64_t cols, T* __restrict__ out, int64_t ld) {
+  constexpr int kNumbers = kThreads / kSlices;
+  __shared__ float lds[kSlices][kNumbers];
+  const int64_t total = rows * cols;
+  const int lane = threadIdx.x % kNumbers, slice = threadIdx.x / kNumbers;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kNumbers; first < total;
+       first += static_cast<int64_t>(gridDim.x) * kNumbers) {
+    const int64_t i = first + lane;
+    float s = i < total ? sum_slice<kSlices>(part + i, total, slice, parts) : 0.f;
+    if (kSlices > 1) {
+      lds[slice][lane] = s;
+      __syncthreads();
+      if (slice == 0) {
+        s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kSlices; ++q) s += lds[q][lane];
+      }
+    }
+    if (slice == 0 && i < total) {
+      const int64_t r = i / cols;
+      out[r * ld + (i - r * cols)] = static_cast<T>(s);
+    }
+    if (kSlices > 1) __syncthreads();
+  }
+}
+
+template <class T>
+hipError_t sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, hipStream_t s) {
+  const int64_t total = rows * cols;
+  if (total == 0) return hipSuccess;
+  const int slices = parts >= 16 ? 16 : 1, numbers = kThreads / slices;
+  const dim3 grid(static_cast<unsigned>(std::min((total + numbers - 1) / numbers, kMaxGroups)));
+  if (slices == 16)
+    sum_parts_kernel<T, 16><<<grid, kThreads, 0, s>>>(part, parts, rows, cols, static_cast<T*>(out), ld);
+  else
+    sum_parts_kernel<T, 1><<<grid, kThreads, 0, s>>>(part, parts, rows, cols, static_cast<T*>(out), ld);
+  return hipGetLastError();
+}
+
+// Whether an operand can go straight into LDS: whole aligned chunks, offsets inside a tile in 31 bits.
+// n: its other index; cols: contiguous along that one.
+bool direct(const void* p, int64_t ld, int64_t n, int64_t k, bool cols, int64_t size) {
+  const int64_t e = 16 / size, row = cols ? n : k;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % e == 0 && row % e == 0 && ld >= row &&
+         256 * ld * size < 0x70000000;
+}
+
+}  // namespace
+
+int slope_parts(int32_t rows, int32_t cols) { return slope_shape(rows, cols).parts; }
+
+hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t s) {
+  const SlopeShape sh = slope_shape(a.rows, a.cols);
+  const dim3 grid(static_cast<unsigned>(sh.parts) * static_cast<unsigned>(sh.groups));
+  if (dtype == ETPC_F32)
+    slope_kernel<float><<<grid, kThreads, 0, s>>>(a, sh);
+  else if (dtype == ETPC_BF16)
+    slope_kernel<Bf16><<<grid, kThreads, 0, s>>>(a, sh);
+  else
+    slope_kernel<F16><<<grid, kThreads, 0, s>>>(a, sh);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, int dtype,
+                            hipStream_t s) {
+  return dtype == ETPC_F32    ? sum_parts<float>(part, parts, rows, cols, out, ld, s)
+         : dtype == ETPC_BF16 ? sum_parts<Bf16>(part, parts, rows, cols, out, ld, s)
+                              : sum_parts<F16>(part, parts, rows, cols, out, ld, s);
+}
+
+MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split) {
+  const int64_t size = dtype == ETPC_F32 ? 4 : 2;
+  MatmulShape s{64, false, 1, a.K};
+  s.direct = direct(a.a, a.lda, a.M, a.K, form == MatmulForm::kColsCols, size) &&
+             direct(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size);
+  const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
+  const int64_t bk = 128 / size;
+  if (split) {
+    s.tile = std::min(a.M, a.N) > 64 ? 128 : 64;
+    const int64_t want = std::max<int64_t>(1, 512 / tiles(s.tile)), most = std::max<int64_t>(1, a.K / 512);
+    int64_t each = (a.K + std::min(want, most) - 1) / std::min(want, most);
+    each = (each + bk - 1) / bk * bk;
+    s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));
+    s.splits = static_cast<int>((a.K + each - 1) / each);
+  } else {
+    s.tile = size == 2 && tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+  }
+  return s;
+}
+
+hipError_t launch_matmul(const MatmulArgs& args, MatmulForm form, int dtype, const MatmulShape& shape, hipStream_t s) {
+  MatmulArgs a = args;
+  a.splits = shape.splits;
+  a.k_split = shape.k_split;
+  return dtype == ETPC_F32    ? mm::launch_f32(a, form, shape, s)
+         : dtype == ETPC_BF16 ? mm::launch_bf16(a, form, shape, s)
+                              : mm::launch_f16(a, form, shape, s);
+}
+
+}  // namespace etpc

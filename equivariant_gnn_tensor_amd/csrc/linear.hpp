@@ -1,0 +1,58 @@
+// Launchers of the dense layer (internal).
+#pragma once
+
+#include "common.hpp"
+
+namespace etpc {
+
+// C(m, n) = epilogue(sum_k A(m, k) B(k, n)); see matmul.hpp.  Strides in elements.
+struct MatmulArgs {
+  const void* a;
+  const void* b;
+  void* c;
+  void* z;              // or null: the sum with its bias, before the activation
+  const void* res;      // or null
+  const float* bias;    // or null
+  float* part;          // or null: fp32 sums of `splits` ranges of k go to part[split][M][N] instead
+  int64_t lda, ldb, ldc, ldz, ldres;
+  int32_t M, N, K;
+  int32_t k_split, splits;
+  int32_t act;
+  int32_t tiles_m, tiles_n;   // filled in by the launch
+};
+// Which index of A and of B is contiguous.
+enum class MatmulForm { kRowsCols, kRowsRows, kColsCols };   // A by rows (k), B by columns (n), ...
+
+struct MatmulShape {
+  int tile;        // side of a workgroup's tile
+  bool direct;     // slices go straight into LDS
+  int splits, k_split;
+};
+// The shape for a product; `split` allows ranges of k.  Operands' addresses do not matter to the splits.
+MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split);
+hipError_t launch_matmul(const MatmulArgs& a, MatmulForm form, int dtype, const MatmulShape& shape, hipStream_t s);
+namespace mm {
+hipError_t launch_f32(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s);
+hipError_t launch_bf16(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s);
+hipError_t launch_f16(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s);
+}  // namespace mm
+
+// z_bar = y_bar act'(z) (null: not written), and per part the column sums of it (null: none):
+// part[p][cols], p < slope_parts(rows, cols).
+struct SlopeArgs {
+  const void* y_bar;
+  const void* z;        // or null: act is none
+  void* z_bar;          // or null
+  float* part;          // or null
+  int64_t ybs, zs, zbs;
+  int32_t rows, cols, parts, act;
+};
+int slope_parts(int32_t rows, int32_t cols);
+hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t s);
+
+// out[r ld + c] = sum_{p < parts} part[p][rows][cols], in a fixed order, rounded to the dtype once.
+// No parts: zeros.
+hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, int dtype,
+                            hipStream_t s);
+
+}  // namespace etpc

@@ -1,0 +1,351 @@
+// Matrix products on the gfx950 matrix cores with the dense layer's epilogue (templates;
+// matmul_*.hip hold the instantiations of one element type each).
+//
+//   C(m, n) = epilogue(sum_k A(m, k) B(k, n)),  sums in fp32
+//
+// An operand is either contiguous along k ("rows": A[m lda + k], B[n ldb + k]) or along its
+// other index ("columns": A[k lda + m], B[k ldb + n]).  The layer's three products need three
+// of the four pairs (MatmulForm).
+//
+// A workgroup owns a BM x BN tile of C and walks k in slices of 128 bytes (64 elements of 16
+// bits, 32 of 32), two slices in LDS in turn.
+//   LDS, rows: [row][8 chunks of 16 bytes], chunk c of row r at c ^ (r & 7): a fragment read
+//   takes one chunk of each of 32 rows, and the exclusive or spreads eight neighbours over all banks.
+//   LDS, columns: [k][columns].  16-bit fragments hold eight k of one column, so they are read
+//   with the transposing LDS load (four k of 16 columns at a time); its 32-byte blocks are
+//   spread over the banks by an exclusive or with k.  fp32 fragments are one number a lane.
+// Slices come in by loads that write LDS directly where both operands are aligned to 16 bytes
+// and hold whole chunks (kDirect): no registers, and what lies past the end is cleared by the
+// loads' range check.  Anything else goes through registers, chunk by chunk, ends masked.
+//
+// v_mfma_f32_32x32x16 (16 bits) and v_mfma_f32_32x32x2 (fp32) take B's fragment first, so a
+// lane ends up with four adjacent columns of one row at a time; the epilogue turns them over
+// to whole row segments through LDS and is then plain row code: bias, pre-activation,
+// activation, residual, one rounding, 16-byte accesses of any alignment.
+#pragma once
+
+#include "activation.hpp"
+#include "linear.hpp"
+#include "rows.hpp"
+
+namespace etpc {
+namespace mm {
+
+typedef float Acc __attribute__((ext_vector_type(16)));
+typedef uint32_t Chunk __attribute__((ext_vector_type(4)));   // 16 bytes
+typedef short Tr4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void LdsVoid;
+typedef __attribute__((address_space(3))) Tr4 LdsTr4;
+
+constexpr int kSliceBytes = 128;
+template <class T>
+constexpr int slice() {
+  return kSliceBytes / static_cast<int>(sizeof(T));
+}
+
+// Elements c .. of a row of n as 16 bytes; zero past the end.
+template <class T>
+__device__ inline Chunk fetch_chunk(const T* __restrict__ row, int c, int n) {
+  constexpr int E = 16 / sizeof(T);
+  Chunk t = {};
+  if (c >= n) return t;
+  if (n >= E) {
+    const int at = min(c, n - E);
+    __builtin_memcpy(&t, row + at, 16);
+    if (at != c) {
+      unsigned __int128 v;
+      __builtin_memcpy(&v, &t, 16);
+      v >>= (c - at) * 8 * static_cast<int>(sizeof(T));
+      __builtin_memcpy(&t, &v, 16);
+    }
+  } else {
+    T e[E] = {};
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (c + k < n) e[k] = row[c + k];
+    __builtin_memcpy(&t, e, 16);
+  }
+  return t;
+}
+
+// One operand's slice: SIDE rows (columns) of the tile by one slice of k.
+template <class T, int SIDE, bool kCols, int kThreads>
+struct Side {
+  static constexpr int E = 16 / sizeof(T), BK = slice<T>();
+  static constexpr int kBytes = SIDE * kSliceBytes;
+  static constexpr int kPer = kBytes / 16 / kThreads;      // chunks a thread
+  static constexpr int kRow = kCols ? SIDE / E : 8;        // chunks of a row in LDS
+  static_assert(kPer >= 1 && kBytes % (16 * kThreads) == 0, "whole chunks for every thread");
+  static_assert((kThreads / kRow) % 8 == 0, "a thread's chunks share their swizzle");
+
+  // Logical chunk at place p of LDS row r.
+  static __device__ inline int unswizzle(int p, int r) {
+    if (!kCols) return p ^ (r & 7);
+    return sizeof(T) == 2 ? p ^ spread(r) : p;
+  }
+  // Chunks of columns move in pairs (32 bytes, what the transposing load takes of one k).
+  static __device__ inline int spread(int k) { return ((k & 3) << 1) & (kRow - 1); }
+
+  // Reads the slice from k0 on (first: the tile's first row or column) into LDS.
+  struct Direct {
+    int off[kPer];
+    int k[kPer];
+    const char* p;
+    int64_t left, step;   // bytes from p to the operand's end; per slice
+    __device__ inline void start(const T* base, int64_t ld, int64_t first, int n, int K, int k0) {
+      const int64_t at = kCols ? k0 * ld + first : first * ld + k0;
+      const int64_t all = kCols ? (K - 1) * ld + n : (n - 1) * ld + K;
+      p = reinterpret_cast<const char*>(base + at);
+      left = (all - at) * static_cast<int64_t>(sizeof(T));
+      step = (kCols ? BK * ld : BK) * static_cast<int64_t>(sizeof(T));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r);
+        off[i] = static_cast<int>(r * ld) * static_cast<int>(sizeof(T)) + 16 * c;
+        k[i] = kCols ? r : c * E;
+      }
+    }
+    // `have`: k values from here to the end; chunks past it are read as zero.
+    __device__ inline void issue(char* lds, int have) {
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0,
+                                                          static_cast<uint32_t>(min(left, int64_t{0x7fffff00})), 0x00020000);
+      char* dst = lds + (threadIdx.x / 64) * 1024;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int o = have >= BK || k[i] < have ? off[i] : 0x7ffffff0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (LdsVoid*)(dst + i * kThreads * 16), 16, o, 0, 0, 0);
+      }
+      p += step;
+      left -= step;
+    }
+    __device__ inline void commit(char*) {}
+  };
+
+  struct Staged {
+    Chunk t[kPer];
+    const T* p;
+    int64_t ld, first;
+    int n, K, k0;
+    __device__ inline void start(const T* base, int64_t ld_, int64_t first_, int n_, int K_, int k0_) {
+      p = base, ld = ld_, first = first_, n = n_, K = K_, k0 = k0_;
+    }
+    __device__ inline void issue(char*, int) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r) * E;
+        t[i] = Chunk{};
+        if (kCols) {
+          if (k0 + r < K) t[i] = fetch_chunk(p + (k0 + r) * ld, static_cast<int>(first) + c, n);
+        } else {
+          if (first + r < n) t[i] = fetch_chunk(p + (first + r) * ld, k0 + c, K);
+        }
+      }
+      k0 += BK;
+    }
+    __device__ inline void commit(char* lds) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        *reinterpret_cast<Chunk*>(lds + (threadIdx.x + i * kThreads) * 16) = t[i];
+    }
+  };
+
+  // Fragment: 16 bytes a lane, k = 2E s + E (lane / 32) .., index at + lane % 32.
+  static __device__ inline Chunk fragment(const char* lds, int at, int s, int lane) {
+    const int h = lane >> 5;
+    if (!kCols) {
+      const int r = at + (lane & 31);
+      return *reinterpret_cast<const Chunk*>(lds + r * 128 + (((2 * s + h) ^ (r & 7)) << 4));
+    }
+    Chunk t;
+    if (sizeof(T) == 2) {
+      const int k = 16 * s + 8 * h + ((lane & 15) >> 2);
+      const int col = at + (lane & 16) + (lane & 3) * 4;
+      const int place = (((col >> 3) ^ spread(k)) << 4) + ((col & 7) << 1);
+      const char* p = lds + k * (SIDE * 2) + place;
+      const Tr4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr4*)p);
+      const Tr4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr4*)(p + 4 * (SIDE * 2)));
+      __builtin_memcpy(&t, &lo, 8);
+      __builtin_memcpy(reinterpret_cast<char*>(&t) + 8, &hi, 8);
+    } else {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(lds) + (8 * s + 4 * h) * SIDE + at + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] = p[j * SIDE];
+    }
+    return t;
+  }
+};
+
+template <class T>
+__device__ inline Acc multiply(const Chunk& b, const Chunk& a, Acc acc) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(b[j]), __uint_as_float(a[j]), acc, 0, 0, 0);
+    return acc;
+  } else {
+    Vec8<T> x, y;
+    __builtin_memcpy(&x, &b, 16);
+    __builtin_memcpy(&y, &a, 16);
+    if constexpr (__is_same(T, F16))
+      return __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, acc, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, acc, 0, 0, 0);
+  }
+}
+
+// Tile of id (bands of eight tile rows, so that the tiles that run together share rows and columns).
+__device__ inline void place_tile(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, tiles_m - 8 * band);
+  tn = in / high;
+  tm = 8 * band + in - tn * high;
+}
+
+template <class T, int BM, int BN, int WM, int WN, bool kACols, bool kBCols, bool kDirect>
+__global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a) {
+  constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, BK = slice<T>();
+  constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
+  using A = Side<T, BM, kACols, kThreads>;
+  using B = Side<T, BN, kBCols, kThreads>;
+  constexpr int kStage = A::kBytes + B::kBytes;
+  constexpr int kPitch = TN + 4, kTurn = 32 * kPitch * 4;   // a wave's 32 rows on their way out
+  static_assert(kTurn * kWaves <= 2 * kStage && kWaves % 2 == 0, "the epilogue turns its rows over in the slices' space");
+  __shared__ __attribute__((aligned(16))) char even[kStage];
+  __shared__ __attribute__((aligned(16))) char odd[kStage];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int per = a.tiles_m * a.tiles_n, total = per * a.splits;
+  const int h = lane >> 5;
+  for (int id = gridDim.x == static_cast<unsigned>(total) ? node_block(blockIdx.x, gridDim.x) : blockIdx.x; id < total;
+       id += gridDim.x) {
+    const int split = id / per;
+    int tm, tn;
+    place_tile(id - split * per, a.tiles_m, a.tiles_n, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+    const int k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
+    const int slices = (k1 - k0 + BK - 1) / BK;
+
+    Acc acc[MI][NI] = {};
+    typename std::conditional<kDirect, typename A::Direct, typename A::Staged>::type la;
+    typename std::conditional<kDirect, typename B::Direct, typename B::Staged>::type lb;
+    la.start(static_cast<const T*>(a.a), a.lda, m0, a.M, a.K, k0);
+    lb.start(static_cast<const T*>(a.b), a.ldb, n0, a.N, a.K, k0);
+    const auto issue = [&](char* lds, int t) {
+      la.issue(lds, k1 - k0 - t * BK);
+      lb.issue(lds + A::kBytes, k1 - k0 - t * BK);
+    };
+    const auto commit = [&](char* lds) {
+      la.commit(lds);
+      lb.commit(lds + A::kBytes);
+    };
+    const auto compute = [&](const char* lds) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        Chunk fa[MI], fb[NI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i] = A::fragment(lds, wm * TM + 32 * i, s, lane);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[j] = B::fragment(lds + A::kBytes, wn * TN + 32 * j, s, lane);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NI; ++j) acc[i][j] = multiply<T>(fb[j], fa[i], acc[i][j]);
+      }
+    };
+    issue(even, 0);
+    commit(even);
+    __syncthreads();
+    for (int t = 0; t < slices; t += 2) {
+      if (t + 1 < slices) issue(odd, t + 1);
+      compute(even);
+      if (t + 1 < slices) commit(odd);
+      __syncthreads();
+      if (t + 1 == slices) break;
+      if (t + 2 < slices) issue(even, t + 2);
+      compute(odd);
+      if (t + 2 < slices) commit(even);
+      __syncthreads();
+    }
+
+    // ---- epilogue
+    char* const space = wave < kWaves / 2 ? even + wave * kTurn : odd + (wave - kWaves / 2) * kTurn;
+    float* const turn = reinterpret_cast<float*>(space);
+    constexpr int kVecs = TN / 8, kRows = 64 / kVecs;   // vectors a row, rows a pass
+    const int n = static_cast<int>(n0) + wn * TN + (lane % kVecs) * 8;
+    float bias[8] = {};
+    if (a.bias != nullptr && n < a.N) load<8, false>(a.bias, n, a.N, bias);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const VecN<float, 4> v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          *reinterpret_cast<VecN<float, 4>*>(turn + (lane & 31) * kPitch + 32 * j + 8 * q + 4 * h) = v;
+        }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int p = 0; p < 32 / kRows; ++p) {
+        const int r = p * kRows + lane / kVecs;
+        const int64_t m = m0 + wm * TM + 32 * i + r;
+        if (m < a.M && n < a.N) {
+          float v[8];
+          const float* src = turn + r * kPitch + (lane % kVecs) * 8;
+          __builtin_memcpy(v, src, 16);
+          __builtin_memcpy(v + 4, src + 4, 16);
+          if (a.part != nullptr) {
+            store<8, false>(a.part + (static_cast<int64_t>(split) * a.M + m) * a.N, n, a.N, v);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] += bias[k];
+            if (a.z != nullptr) store<8, false>(static_cast<T*>(a.z) + m * a.ldz, n, a.N, v);
+            if (a.act != ETPC_ACT_NONE)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = activate<sizeof(T) == 4>(v[k], a.act);
+            if (a.res != nullptr) {
+              float w[8];
+              load<8, false>(static_cast<const T*>(a.res) + m * a.ldres, n, a.N, w);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] += w[k];
+            }
+            store<8, false>(static_cast<T*>(a.c) + m * a.ldc, n, a.N, v);
+          }
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+  }
+}
+
+constexpr int kMaxGroups = 1 << 20;
+
+template <class T, int BM, int BN, int WM, int WN, bool kDirect>
+hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
+  a.tiles_m = (a.M + BM - 1) / BM;
+  a.tiles_n = (a.N + BN - 1) / BN;
+  const int64_t total = static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.splits;
+  if (total >= int64_t{1} << 31) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(total, kMaxGroups))), block(64 * WM * WN);
+  if (form == MatmulForm::kRowsCols)
+    matmul_kernel<T, BM, BN, WM, WN, false, true, kDirect><<<grid, block, 0, s>>>(a);
+  else if (form == MatmulForm::kRowsRows)
+    matmul_kernel<T, BM, BN, WM, WN, false, false, kDirect><<<grid, block, 0, s>>>(a);
+  else
+    matmul_kernel<T, BM, BN, WM, WN, true, true, kDirect><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s) {
+  if (shape.direct) {
+    if (sizeof(T) == 2 && shape.tile == 256) return launch_tiles<T, sizeof(T) == 2 ? 256 : 128, sizeof(T) == 2 ? 256 : 128, sizeof(T) == 2 ? 2 : 2, sizeof(T) == 2 ? 4 : 2, true>(a, form, s);
+    if (shape.tile >= 128) return launch_tiles<T, 128, 128, 2, 2, true>(a, form, s);
+    return launch_tiles<T, 64, 64, 2, 2, true>(a, form, s);
+  }
+  if (shape.tile >= 128) return launch_tiles<T, 128, 128, 2, 2, false>(a, form, s);
+  return launch_tiles<T, 64, 64, 2, 2, false>(a, form, s);
+}
+
+}  // namespace mm
+}  // namespace etpc

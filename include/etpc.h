@@ -422,6 +422,42 @@ etpc_status etpc_irreps_norm_backward(int32_t n_blocks, const etpc_irrep* irreps
                                       const float* y_bar, const float* stats, const float* w, float* x_bar,
                                       float* w_bar, float* b_bar, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------ feed-forward operators
+ * A dense layer over node or edge rows, with its gradient.  Rows, types, strides, alignment and
+ * overlap are those of the node-wise operators. */
+typedef enum {
+  ETPC_ACT_NONE = 0,
+  ETPC_ACT_RELU = 1, /* max(z, 0); its slope at 0 is 0 */
+  ETPC_ACT_SILU = 2, /* z / (1 + exp(-z)) */
+  ETPC_ACT_GELU = 3, /* z Phi(z), Phi the normal distribution function */
+  ETPC_ACT_TANH = 4
+} etpc_act;
+
+/* z = x w + b, y = act(z) + residual: x [n_rows][n_in], w [n_in][n_out], b [n_out] fp32 (NULL =
+ * zeros), residual (NULL = none), y and z [n_rows][n_out] (z, the numbers before the activation,
+ * is what the backward pass reads; NULL = not kept).  Element (i, o) of w is at
+ * w + i * w_in_stride + o * w_out_stride, and one of the two strides is 1: weights stored either
+ * way are read in place.  Sums are taken in fp32, y comes from the unrounded z, and each result is
+ * rounded once.  n_in, n_out >= 1; n_rows n_in, n_rows n_out and n_in n_out < 2^56.  NaN stays NaN;
+ * silu and gelu of -inf are -0. */
+etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, const void* x, int64_t x_stride,
+                        const void* w, int64_t w_in_stride, int64_t w_out_stride, const float* b, const void* residual,
+                        int64_t residual_stride, int32_t act, void* y, int64_t y_stride, void* z, int64_t z_stride,
+                        hipStream_t stream);
+/* Workspace of the backward call: the gradient before the activation, and partial sums. */
+etpc_status etpc_linear_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act,
+                                       size_t* bytes);
+/* Gradients of <y_bar, y>: with z_bar = y_bar act'(z), x_bar = z_bar w^T, w_bar = x^T z_bar and
+ * b_bar = the column sums of z_bar; the residual's is y_bar itself.  x_bar and w_bar have the
+ * rows' type (z_bar is rounded to it where it enters their products), b_bar is fp32, summed from
+ * z_bar before that.  w_bar's strides are its own.  z may be NULL when act is ETPC_ACT_NONE, x
+ * when w_bar is, w when x_bar is; a NULL output is skipped.  Sums over rows have a fixed order. */
+etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, const void* x,
+                                 int64_t x_stride, const void* w, int64_t w_in_stride, int64_t w_out_stride,
+                                 const void* y_bar, int64_t y_bar_stride, const void* z, int64_t z_stride, int32_t act,
+                                 void* x_bar, int64_t x_bar_stride, void* w_bar, int64_t w_bar_in_stride,
+                                 int64_t w_bar_out_stride, float* b_bar, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Kernel timing (off by default), a measurement aid outside the compute path.  While
  * enabled, every kernel the library enqueues is bracketed by a pair of HIP events recorded
  * on its launch stream, grouped by kind.  etpc_profile_read synchronizes on the recorded
@@ -437,7 +473,7 @@ typedef enum {
   ETPC_KIND_NODE_GEMM = 4,    /* Xt = x W, x_bar = P W^T, W_bar = x^T P */
   ETPC_KIND_AUX = 5,          /* weight re-layout, fixed-order reductions, fills, pos_bar */
   ETPC_KIND_PREP = 6,         /* radius graph and layout conversion */
-  ETPC_KIND_NODEWISE = 7,     /* layer norm, dropout, irreps norm */
+  ETPC_KIND_NODEWISE = 7,     /* layer norm, dropout, irreps norm, feed-forward operators */
   ETPC_KIND_COUNT = 8
 } etpc_kind;
 etpc_status etpc_profile_enable(int32_t enable);
