@@ -23,19 +23,20 @@ __device__ inline float logistic(float x) {
 
 // Both limits are taken where the formulas would multiply zero by infinity: silu and gelu of
 // -inf are -0 and their slopes at +-inf 1 and 0.  NaN passes through every comparison.
-template <bool kWide>
-__device__ inline float activate(float z, int act) {
-  switch (act) {
-    case ETPC_ACT_RELU:
-      return z < 0.f ? 0.f : z;
-    case ETPC_ACT_SILU:
-      return z < -200.f ? -0.f : z * logistic<kWide>(z);
-    case ETPC_ACT_GELU:   // z Phi(z), by erfc: 1 + erf would cancel below zero
-      return z < -200.f ? -0.f : 0.5f * z * erfcf(-0.70710678f * z);
-    case ETPC_ACT_TANH:
-      return tanhf(z);
-    default:
-      return z;
+template <bool kWide, int N>
+__device__ inline void activate(float (&v)[N], int act) {
+  if (act == ETPC_ACT_RELU) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = v[k] < 0.f ? 0.f : v[k];
+  } else if (act == ETPC_ACT_SILU) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = v[k] < -200.f ? -0.f : v[k] * logistic<kWide>(v[k]);
+  } else if (act == ETPC_ACT_GELU) {   // z Phi(z), by erfc: 1 + erf would cancel below zero
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = v[k] < -200.f ? -0.f : 0.5f * v[k] * erfcf(-0.70710678f * v[k]);
+  } else if (act == ETPC_ACT_TANH) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = tanhf(v[k]);
   }
 }
 

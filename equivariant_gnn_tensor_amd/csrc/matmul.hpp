@@ -255,15 +255,19 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     issue(even, 0);
     commit(even);
     __syncthreads();
-    for (int t = 0; t < slices; t += 2) {
-      if (t + 1 < slices) issue(odd, t + 1);
+    int t = 0;
+    for (; t + 2 <= slices; t += 2) {
+      issue(odd, t + 1);
       compute(even);
-      if (t + 1 < slices) commit(odd);
+      commit(odd);
       __syncthreads();
-      if (t + 1 == slices) break;
       if (t + 2 < slices) issue(even, t + 2);
       compute(odd);
       if (t + 2 < slices) commit(even);
+      __syncthreads();
+    }
+    if (t < slices) {
+      compute(even);
       __syncthreads();
     }
 
@@ -284,7 +288,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
           *reinterpret_cast<VecN<float, 4>*>(turn + (lane & 31) * kPitch + 32 * j + 8 * q + 4 * h) = v;
         }
       __builtin_amdgcn_wave_barrier();
-#pragma unroll
+#pragma unroll 1
       for (int p = 0; p < 32 / kRows; ++p) {
         const int r = p * kRows + lane / kVecs;
         const int64_t m = m0 + wm * TM + 32 * i + r;
@@ -299,9 +303,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += bias[k];
             if (a.z != nullptr) store<8, false>(static_cast<T*>(a.z) + m * a.ldz, n, a.N, v);
-            if (a.act != ETPC_ACT_NONE)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = activate<sizeof(T) == 4>(v[k], a.act);
+            if (a.act != ETPC_ACT_NONE) activate<sizeof(T) == 4>(v, a.act);
             if (a.res != nullptr) {
               float w[8];
               load<8, false>(static_cast<const T*>(a.res) + m * a.ldres, n, a.N, w);
