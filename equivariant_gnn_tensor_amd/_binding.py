@@ -83,6 +83,8 @@ SYMBOLS = (
     "etpc_dropout_add_layer_norm", "etpc_dropout_add_layer_norm_backward", "etpc_irreps_dims", "etpc_irreps_dropout",
     "etpc_irreps_norm", "etpc_irreps_norm_workspace_size", "etpc_irreps_norm_backward",
     "etpc_linear", "etpc_linear_workspace_size", "etpc_linear_backward",
+    "etpc_norm_gate_add_norm", "etpc_norm_gate_add_norm_workspace_size", "etpc_norm_gate_add_norm_backward",
+    "etpc_grad_norm_workspace_size", "etpc_grad_norm", "etpc_clip_grad_norm",
 )
 KINDS = ("csr", "fwd_traverse", "channel_gemm", "bwd_traverse", "node_gemm", "aux", "prep", "nodewise")
 
@@ -137,6 +139,14 @@ def _load():
         "etpc_linear_workspace_size": [i64, i64, i64, i32, i32, P(sz)],
         "etpc_linear_backward": [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i64,
                                  vp, vp, sz, vp],
+        "etpc_norm_gate_add_norm": [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, f32, vp, i64, vp, i64, vp,
+                                    vp],
+        "etpc_norm_gate_add_norm_workspace_size": [i64, i64, P(sz)],
+        "etpc_norm_gate_add_norm_backward": [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp,
+                                             vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp],
+        "etpc_grad_norm_workspace_size": [i32, vp, P(sz)],
+        "etpc_grad_norm": [i32, vp, vp, vp, i32, vp, vp, sz, vp],
+        "etpc_clip_grad_norm": [i32, vp, vp, vp, vp, i32, f32, vp, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -1085,3 +1095,178 @@ def etpc_linear_backward(x, w, y_bar, z=None, act: str = "none", want=("x", "w",
     if st:
         _check(st)
     return x_bar, w_bar, b_bar
+
+
+def etpc_norm_gate_add_norm(x, gate=None, residual=None, w1=None, b1=None, scale=None, w2=None, b2=None, eps: float = 1e-5,
+                            y=None, h=None, stats=None, keep_h: bool = True, keep_stats: bool = True, stream=None):
+    """(y, h, stats): n = norm(x) w1 + b1, h = residual + scale sigmoid(gate) n, y = norm(h) w2 + b2
+    over the rows x [..., C]; gate (None: 1) and residual (None: 0) like x.  stats [..., 4]: mean and
+    rstd of x and of h.  keep_h=False and keep_stats=False skip what only the backward pass (and,
+    for h, the next block's residual) reads: None instead."""
+    dtype, dev = _row_type(x), x.device
+    handle = _check_device("x", x, stream)
+    xp, xs, rows, cols = _rows("x", x)
+    gp, gs = _rows_like("gate", gate, x)
+    rp, rs = _rows_like("residual", residual, x)
+    if y is None:
+        y = _new_like(x, stream)
+        yp, ys = y.data_ptr(), cols
+    else:
+        yp, ys = _rows_like("y", y, x)
+    if h is None and keep_h:
+        h = _new_like(x, stream)
+        hp, hs = h.data_ptr(), cols
+    else:
+        hp, hs = _rows_like("h", h, x)
+    if stats is None and keep_stats:
+        stats = _new((*x.shape[:-1], 4), dev, stream)
+        sp = stats.data_ptr()
+    else:
+        sp = _vector("stats", stats, 4 * rows, dev)
+    st = lib.etpc_norm_gate_add_norm(rows, cols, dtype, xp, xs, gp, gs, rp, rs, _vector("w1", w1, cols, dev),
+                                     _vector("b1", b1, cols, dev), _vector("scale", scale, cols, dev),
+                                     _vector("w2", w2, cols, dev), _vector("b2", b2, cols, dev), eps, yp, ys, hp, hs, sp,
+                                     handle)
+    if st:
+        _check(st)
+    return y, h, stats
+
+
+def etpc_norm_gate_add_norm_workspace_size(n_rows: int, n_cols: int) -> int:
+    return _join_ws(n_rows, n_cols)
+
+
+@functools.lru_cache(maxsize=512)
+def _join_ws(n_rows: int, n_cols: int) -> int:
+    b = C.c_size_t()
+    _check(lib.etpc_norm_gate_add_norm_workspace_size(n_rows, n_cols, b))
+    return b.value
+
+
+_JOIN_BARS = ("x", "gate", "residual", "w1", "b1", "scale", "w2", "b2")
+
+
+def etpc_norm_gate_add_norm_backward(x, h, y_bar, stats, gate=None, w1=None, b1=None, scale=None, w2=None, h_bar=None,
+                                     want=_JOIN_BARS, outs=None, ws=None, stream=None):
+    """(x_bar, gate_bar, residual_bar, w1_bar, b1_bar, scale_bar, w2_bar, b2_bar) of <y_bar, y> +
+    <h_bar, h>; None for what `want` leaves out, and for gate_bar without a gate.  h and stats as
+    the forward call gave them.  outs: eight caller-given tensors (or None to skip one)."""
+    dtype, dev = _row_type(x), x.device
+    handle = _check_device("x", x, stream)
+    xp, xs, rows, cols = _rows("x", x)
+    gp, gs = _rows_like("gate", gate, x)
+    hp, hs = _rows_like("h", h, x)
+    yp, ys = _rows_like("y_bar", y_bar, x)
+    hbp, hbs = _rows_like("h_bar", h_bar, x)
+    if gate is None and outs is None:
+        want = tuple(k for k in want if k != "gate")
+    bars, args = [], []
+    for i, key in enumerate(_JOIN_BARS[:3]):
+        t, p, stride = _bar_like(key + "_bar", want, key, outs, i, x, cols, stream)
+        bars.append(t)
+        args += [p, stride]
+    sums = False
+    for i, key in enumerate(_JOIN_BARS[3:], 3):
+        t, p = _bar_vector(key + "_bar", want, key, outs, i, cols, dev, stream)
+        bars.append(t)
+        args.append(p)
+        sums = sums or p is not None
+    wsp, wsn, _keep = _scratch(ws, _join_ws(rows, cols) if sums else 0, dev, stream)
+    st = lib.etpc_norm_gate_add_norm_backward(rows, cols, dtype, xp, xs, gp, gs, hp, hs, yp, ys, hbp, hbs,
+                                              _vector("stats", stats, 4 * rows, dev), _vector("w1", w1, cols, dev),
+                                              _vector("b1", b1, cols, dev), _vector("scale", scale, cols, dev),
+                                              _vector("w2", w2, cols, dev), *args, wsp, wsn, handle)
+    if st:
+        _check(st)
+    return tuple(bars)
+
+
+_NORM_ORDS = {2: 0, 2.0: 0, float("inf"): 1}   # etpc_norm_ord
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether a tensor's elements are one block of memory, in any order of its axes."""
+    if t.is_contiguous():
+        return True
+    expect = 1
+    for st, n in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if st != expect:
+            return False
+        expect *= n
+    return True
+
+
+def _grad_list(grads):
+    """(pointers, sizes, dtypes) as C arrays of a list of dense tensors on one device."""
+    n = len(grads)
+    ptrs, sizes, dtypes = (C.c_void_p * n)(), (C.c_int64 * n)(), (C.c_int32 * n)()
+    dev = grads[0].device if n else None
+    for k, t in enumerate(grads):
+        code = _ROW_TYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"tensor {k} must be float32, bfloat16 or float16, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"tensor {k} is on {t.device}, expected {dev}")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"tensor {k} must be one block of memory")
+        ptrs[k], sizes[k], dtypes[k] = t.data_ptr() or None, t.numel(), code
+    return ptrs, sizes, dtypes
+
+
+def _norm_call(grads, ord, norm, ws, stream):
+    grads = list(grads)
+    if ord not in _NORM_ORDS:
+        raise ValueError(f"ord must be 2 or inf, got {ord!r}")
+    if grads:
+        handle, dev = _check_device("tensor 0", grads[0], stream), grads[0].device
+    else:
+        dev = torch.device("cuda", torch.cuda.current_device()) if norm is None else norm.device
+        handle = _stream(stream)
+    ptrs, sizes, dtypes = _grad_list(grads)
+    if norm is None:
+        norm = _new((), dev, stream)
+    need = C.c_size_t()
+    _check(lib.etpc_grad_norm_workspace_size(len(grads), sizes, need))
+    wsp, wsn, keep = _scratch(ws, need.value, dev, stream)
+    return grads, ptrs, sizes, dtypes, _NORM_ORDS[ord], norm, _vector("norm", norm, 1, dev), wsp, wsn, keep, handle
+
+
+def etpc_grad_norm_workspace_size(sizes) -> int:
+    """Workspace of the two calls below for tensors of these numbers of elements."""
+    sizes = list(sizes)
+    b = C.c_size_t()
+    _check(lib.etpc_grad_norm_workspace_size(len(sizes), (C.c_int64 * len(sizes))(*sizes), b))
+    return b.value
+
+
+def etpc_grad_norm(grads, ord=2, norm=None, ws=None, stream=None) -> torch.Tensor:
+    """The global norm of a list of tensors (f32, bf16 and f16 may be mixed; any dense layout) as
+    one f32 number on the GPU: ord 2, or inf for the largest magnitude."""
+    grads, ptrs, sizes, dtypes, code, norm, np_, wsp, wsn, _keep, handle = _norm_call(grads, ord, norm, ws, stream)
+    st = lib.etpc_grad_norm(len(grads), ptrs, sizes, dtypes, code, np_, wsp, wsn, handle)
+    if st:
+        _check(st)
+    return norm
+
+
+def etpc_clip_grad_norm(grads, max_norm: float, ord=2, outs=None, norm=None, ws=None, stream=None) -> torch.Tensor:
+    """The global norm, and every tensor times min(1, max_norm / (norm + 1e-6)), in place or into
+    `outs` (tensors of the same shapes, strides and types).  A norm that is not finite leaves the
+    gradients as they are."""
+    grads, ptrs, sizes, dtypes, code, norm, np_, wsp, wsn, _keep, handle = _norm_call(grads, ord, norm, ws, stream)
+    if outs is None:
+        op = None
+    else:
+        outs = list(outs)
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(grads)} tensors and {len(outs)} outs")
+        for k, (o, g) in enumerate(zip(outs, grads)):
+            if o.shape != g.shape or o.dtype != g.dtype or o.device != g.device:
+                raise ValueError(f"outs {k} must be like its tensor")
+            if o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()):
+                raise ValueError(f"outs {k} must have its tensor's strides")
+        op = (C.c_void_p * len(outs))(*[o.data_ptr() or None for o in outs])
+    st = lib.etpc_clip_grad_norm(len(grads), ptrs, op, sizes, dtypes, code, max_norm, np_, wsp, wsn, handle)
+    if st:
+        _check(st)
+    return norm

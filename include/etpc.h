@@ -423,7 +423,8 @@ etpc_status etpc_irreps_norm_backward(int32_t n_blocks, const etpc_irrep* irreps
                                       float* w_bar, float* b_bar, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------ feed-forward operators
- * A dense layer over node or edge rows, with its gradient.  Rows, types, strides, alignment and
+ * A feed-forward block over node or edge rows and its training step: dense layers, the gated join
+ * between two norms, their gradients, and the clipping of all gradients by their norm.  Rows, types, strides, alignment and
  * overlap are those of the node-wise operators. */
 typedef enum {
   ETPC_ACT_NONE = 0,
@@ -457,6 +458,53 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
                                  const void* y_bar, int64_t y_bar_stride, const void* z, int64_t z_stride, int32_t act,
                                  void* x_bar, int64_t x_bar_stride, void* w_bar, int64_t w_bar_in_stride,
                                  int64_t w_bar_out_stride, float* b_bar, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Two norms and the gated join between them, as they follow one another where a block ends and
+ * the next begins:
+ *   n = norm(x) w1 + b1                       (x: what the block computed)
+ *   h = residual + scale sigmoid(gate) n
+ *   y = norm(h) w2 + b2                       (y: what the next block reads, h: what it adds to)
+ * norm as in etpc_layer_norm, eps the same for both.  gate (NULL: sigmoid = 1) and residual (NULL:
+ * zeros) are matrices like x, of the rows' type; w1, b1, scale, w2, b2 [n_cols] fp32, NULL = ones,
+ * zeros, ones, ones, zeros.  h: NULL = not kept (the backward pass reads it).  stats [n_rows][4] =
+ * mean and rstd of x, mean and rstd of h, for the backward pass, or NULL.  y and the statistics
+ * are those of h before it is rounded. */
+etpc_status etpc_norm_gate_add_norm(int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride,
+                                    const void* gate, int64_t gate_stride, const void* residual, int64_t residual_stride,
+                                    const float* w1, const float* b1, const float* scale, const float* w2,
+                                    const float* b2, float eps, void* y, int64_t y_stride, void* h, int64_t h_stride,
+                                    float* stats, hipStream_t stream);
+/* Workspace of the backward call: partial sums of the parameter gradients. */
+etpc_status etpc_norm_gate_add_norm_workspace_size(int64_t n_rows, int64_t n_cols, size_t* bytes);
+/* Gradients of <y_bar, y> + <h_bar, h> (h_bar NULL = zero).  Any output may be NULL; those of rows
+ * (x_bar, gate_bar, residual_bar) have the rows' type and one row for each row of the call also
+ * where an input repeats one (stride 0); those of parameters are fp32 and summed over rows in a
+ * fixed order.  Rows are centred again with the stored means, like etpc_layer_norm_backward. */
+etpc_status etpc_norm_gate_add_norm_backward(
+    int64_t n_rows, int64_t n_cols, int32_t dtype, const void* x, int64_t x_stride, const void* gate,
+    int64_t gate_stride, const void* h, int64_t h_stride, const void* y_bar, int64_t y_bar_stride, const void* h_bar,
+    int64_t h_bar_stride, const float* stats, const float* w1, const float* b1, const float* scale, const float* w2,
+    void* x_bar, int64_t x_bar_stride, void* gate_bar, int64_t gate_bar_stride, void* residual_bar,
+    int64_t residual_bar_stride, float* w1_bar, float* b1_bar, float* scale_bar, float* w2_bar, float* b2_bar, void* ws,
+    size_t ws_bytes, hipStream_t stream);
+
+/* The global norm of n gradient tensors: sqrt of the sum of all squares (ord = ETPC_NORM_2), or the
+ * largest magnitude (ETPC_NORM_MAX).  grads[k] (device, in a host array) holds sizes[k] contiguous
+ * numbers of dtypes[k], aligned to the element; a tensor without elements may be NULL.  *norm
+ * [device]: one fp32 number; NaN when any number is, and infinite past fp32's range.  Squares and
+ * their sums are taken in 64 bits, in an order that depends on the sizes only. */
+typedef enum { ETPC_NORM_2 = 0, ETPC_NORM_MAX = 1 } etpc_norm_ord;
+etpc_status etpc_grad_norm_workspace_size(int32_t n, const int64_t* sizes, size_t* bytes);
+etpc_status etpc_grad_norm(int32_t n, const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t ord,
+                           float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
+/* The same, then every gradient times min(1, max_norm / (norm + 1e-6)), rounded once, to outs[k]
+ * (an array of the same sizes and types, or NULL: in place).  A norm that is not finite leaves the
+ * gradients as they are (outs gets copies): the caller reads *norm and skips the step.  In place,
+ * gradients within the norm are not touched.  max_norm >= 0, infinite allowed.  Written tensors
+ * share memory with nothing else, except that outs[k] may be grads[k]. */
+etpc_status etpc_clip_grad_norm(int32_t n, const void* const* grads, void* const* outs, const int64_t* sizes,
+                                const int32_t* dtypes, int32_t ord, float max_norm, float* norm, void* ws,
+                                size_t ws_bytes, hipStream_t stream);
 
 /* Kernel timing (off by default), a measurement aid outside the compute path.  While
  * enabled, every kernel the library enqueues is bracketed by a pair of HIP events recorded

@@ -85,3 +85,88 @@ def test_binding_refusals():
         etpc.etpc_linear(x, w, act="swish")
     with pytest.raises(TypeError, match="float32"):
         etpc.etpc_linear(x.double(), w)
+
+
+def join(rows=4, cols=8, dtype=F32, x=A, xs=8, gate=A + 4096, gs=8, res=A + 8192, rs=8, w1=None, b2=None, eps=1e-5, y=B, ys=8,
+         h=B + 4096, hs=8, stats=B + 8192):
+    return lib.etpc_norm_gate_add_norm(rows, cols, dtype, x, xs, gate, gs, res, rs, w1, None, None, None, b2, eps, y, ys, h, hs,
+                                       stats, None)
+
+
+@pytest.mark.parametrize("kwargs,status,word", [
+    (dict(rows=-1), INVALID, "negative"), (dict(cols=0), INVALID, "column"), (dict(dtype=7), INVALID, "dtype"),
+    (dict(rows=1 << 31), OVERFLOW, "n_rows"), (dict(eps=-1.0), INVALID, "eps"), (dict(eps=float("nan")), INVALID, "eps"),
+    (dict(x=None), INVALID, "null x"), (dict(y=None), INVALID, "null y"), (dict(gate=A + 4097), INVALID, "aligned"),
+    (dict(gs=7), INVALID, "stride"), (dict(rs=7), INVALID, "stride"), (dict(hs=7), INVALID, "stride"), (dict(ys=0), INVALID, "stride"),
+    (dict(w1=D + 1), INVALID, "aligned"), (dict(stats=D + 2), INVALID, "aligned"), (dict(y=A), INVALID, "overlap"),
+    (dict(h=A + 8192), INVALID, "overlap"), (dict(y=B + 4096), INVALID, "overlap"), (dict(stats=B), INVALID, "overlap"),
+    (dict(w1=B), INVALID, "overlap"), (dict(b2=B + 8192), INVALID, "overlap"),
+])
+def test_join_refusals(kwargs, status, word):
+    assert join(**kwargs) == status and word in message()
+
+
+def join_backward(rows=1000, cols=8, dtype=F32, x=A, xs=8, gate=A + (1 << 16), h=A + (2 << 16), y_bar=A + (3 << 16), ys=8, h_bar=None, stats=A + (4 << 16),
+                  w1=None, x_bar=B, xbs=8, gate_bar=B + (1 << 16), res_bar=B + (2 << 16), bars=(D, D + 64, D + 128, D + 192, D + 256), ws=E,
+                  n=1 << 16):
+    return lib.etpc_norm_gate_add_norm_backward(rows, cols, dtype, x, xs, gate, 8, h, 8, y_bar, ys, h_bar, 8, stats, w1, None, None,
+                                                None, x_bar, xbs, gate_bar, 8, res_bar, 8, *bars, ws, n, None)
+
+
+@pytest.mark.parametrize("kwargs,status,word", [
+    (dict(rows=-1), INVALID, "negative"), (dict(cols=0), INVALID, "column"), (dict(gate=None), INVALID, "gate_bar"),
+    (dict(x=None), INVALID, "null x"), (dict(h=None), INVALID, "null h"), (dict(y_bar=None), INVALID, "null y_bar"),
+    (dict(stats=None), INVALID, "null stats"), (dict(xbs=7), INVALID, "stride"), (dict(ys=7), INVALID, "stride"),
+    (dict(h_bar=F + 1), INVALID, "aligned"), (dict(bars=(D + 2, None, None, None, None)), INVALID, "aligned"),
+    (dict(ws=None), WORKSPACE, "null"), (dict(n=8), WORKSPACE, "too small"), (dict(x_bar=A), INVALID, "overlap"),
+    (dict(res_bar=B), INVALID, "overlap"), (dict(bars=(D, D, None, None, None)), INVALID, "overlap"),
+    (dict(bars=(A, None, None, None, None)), INVALID, "overlap"), (dict(ws=B), INVALID, "overlap"), (dict(w1=D), INVALID, "overlap"),
+])
+def test_join_backward_refusals(kwargs, status, word):
+    assert join_backward(**kwargs) == status and word in message()
+
+
+def test_join_no_work():
+    assert join(rows=0, x=None, y=None) == OK
+    none = (None,) * 5
+    assert join_backward(rows=0, x=None, h=None, y_bar=None, stats=None, bars=none, ws=None, n=0) == OK
+    assert join_backward(x_bar=None, gate_bar=None, res_bar=None, bars=none, ws=None, n=0) == OK
+    assert etpc.etpc_norm_gate_add_norm_workspace_size(0, 8) == 0
+    assert etpc.etpc_norm_gate_add_norm_workspace_size(1000, 64) > 0
+
+
+def clip(sizes=(8, 16), dtypes=(F32, BF16), grads=(A, B), outs=None, ord=0, max_norm=1.0, norm=D, ws=E, n=1 << 16, count=None):
+    k = len(sizes)
+    p = (C.c_void_p * k)(*grads)
+    o = None if outs is None else (C.c_void_p * k)(*outs)
+    return lib.etpc_clip_grad_norm(k if count is None else count, p, o, (C.c_int64 * k)(*sizes), (C.c_int32 * k)(*dtypes), ord,
+                                   max_norm, norm, ws, n, None)
+
+
+@pytest.mark.parametrize("kwargs,status,word", [
+    (dict(count=-1), INVALID, "negative number"), (dict(sizes=(8, -1)), INVALID, "negative size"),
+    (dict(sizes=(1 << 47, (1 << 47) + 1)), OVERFLOW, "2^48"), (dict(dtypes=(F32, 5)), INVALID, "dtype"), (dict(ord=2), INVALID, "norm"),
+    (dict(norm=None), INVALID, "null norm"), (dict(norm=D + 2), INVALID, "aligned"), (dict(max_norm=-1.0), INVALID, "max_norm"),
+    (dict(max_norm=float("nan")), INVALID, "max_norm"), (dict(grads=(A, None)), INVALID, "null tensor"),
+    (dict(grads=(A + 2, B)), INVALID, "aligned"), (dict(outs=(A, B + 1)), INVALID, "aligned"), (dict(ws=None), WORKSPACE, "null"),
+    (dict(n=8), WORKSPACE, "too small"), (dict(ws=E + 4), WORKSPACE, "doubles"), (dict(grads=(A, A)), INVALID, "overlap"),
+    (dict(grads=(A, A + 16)), INVALID, "overlap"), (dict(outs=(A + 4, D + 64)), INVALID, "overlap"),
+    (dict(outs=(D + 64, D + 64)), INVALID, "overlap"), (dict(outs=(B, D + 64)), INVALID, "overlap"), (dict(norm=A + 4), INVALID, "overlap"),
+    (dict(ws=B), INVALID, "overlap"),
+])
+def test_clip_refusals(kwargs, status, word):
+    assert clip(**kwargs) == status and word in message()
+
+
+def test_norm_workspace():
+    assert etpc.etpc_grad_norm_workspace_size([]) == 0 and etpc.etpc_grad_norm_workspace_size([0, 0]) == 0
+    assert etpc.etpc_grad_norm_workspace_size([5]) == 8
+    assert etpc.etpc_grad_norm_workspace_size([1] * 1000) == 8000
+    assert etpc.etpc_grad_norm_workspace_size([1 << 40] * 3) == 8 * 2048
+
+
+def test_binding_lists():
+    with pytest.raises(ValueError, match="ord"):
+        etpc.etpc_grad_norm([torch.zeros(3)], ord=1)
+    with pytest.raises(ValueError, match="GPU"):
+        etpc.etpc_grad_norm([torch.zeros(3)])
