@@ -108,7 +108,7 @@ struct Side {
     // `have`: k values from here to the end; chunks past it are read as zero.
     __device__ inline void issue(char* lds, int have) {
       const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0,
-                                                          static_cast<uint32_t>(min(left, int64_t{0x7fffff00})), 0x00020000);
+                                                          static_cast<uint32_t>(max(min(left, int64_t{0x7fffff00}), int64_t{0})), 0x00020000);
       char* dst = lds + (threadIdx.x / 64) * 1024;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -193,6 +193,13 @@ __device__ inline Acc multiply(const Chunk& b, const Chunk& a, Acc acc) {
   }
 }
 
+// Barrier after which every wave's loads into LDS are there: a barrier alone waits for a wave's
+// own LDS reads and writes, not for its loads on their way to LDS.
+__device__ inline void barrier_after_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+  __syncthreads();
+}
+
 // Tile of id (bands of eight tile rows, so that the tiles that run together share rows and columns).
 __device__ inline void place_tile(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, tiles_m - 8 * band);
@@ -238,38 +245,50 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
       la.commit(lds);
       lb.commit(lds + A::kBytes);
     };
-    const auto compute = [&](const char* lds) {
+    // Fragments are read one step of k ahead of their products.
+    Chunk fa[2][MI], fb[2][NI];
+    const auto read = [&](const char* lds, int s) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        Chunk fa[MI], fb[NI];
+      for (int j = 0; j < NI; ++j) fb[s & 1][j] = B::fragment(lds + A::kBytes, wn * TN + 32 * j, s, lane);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i] = A::fragment(lds, wm * TM + 32 * i, s, lane);
+      for (int i = 0; i < MI; ++i) fa[s & 1][i] = A::fragment(lds, wm * TM + 32 * i, s, lane);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto products = [&](int s) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[j] = B::fragment(lds + A::kBytes, wn * TN + 32 * j, s, lane);
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int j = 0; j < NI; ++j) acc[i][j] = multiply<T>(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // Slice t, whose first fragments are read already, from `cur`.  After its last ones are, one
+    // barrier frees `cur` for slice t + 2 and opens slice t + 1, whose loads are a slice old by then.
+    // What is read past the last slice is not used.
+    const auto walk = [&](char* cur, char* nxt, int t) {
+      if (!kDirect) issue(nxt, t + 1);
 #pragma unroll
-          for (int j = 0; j < NI; ++j) acc[i][j] = multiply<T>(fb[j], fa[i], acc[i][j]);
+      for (int s = 0; s < 3; ++s) {
+        read(cur, s + 1);
+        products(s);
       }
+      if (!kDirect) commit(nxt);
+      barrier_after_loads();
+      if (kDirect) issue(cur, t + 2);
+      read(nxt, 0);
+      products(3);
     };
     issue(even, 0);
     commit(even);
-    __syncthreads();
+    if (kDirect) issue(odd, 1);
+    barrier_after_loads();
+    read(even, 0);
     int t = 0;
     for (; t + 2 <= slices; t += 2) {
-      issue(odd, t + 1);
-      compute(even);
-      commit(odd);
-      __syncthreads();
-      if (t + 2 < slices) issue(even, t + 2);
-      compute(odd);
-      if (t + 2 < slices) commit(even);
-      __syncthreads();
+      walk(even, odd, t);
+      walk(odd, even, t + 1);
     }
-    if (t < slices) {
-      compute(even);
-      __syncthreads();
-    }
+    if (t < slices) walk(even, odd, t);
+    barrier_after_loads();
 
     // ---- epilogue
     char* const space = wave < kWaves / 2 ? even + wave * kTurn : odd + (wave - kWaves / 2) * kTurn;
