@@ -9,11 +9,14 @@
 //
 // A workgroup owns a BM x BN tile of C and walks k in slices of 128 bytes (64 elements of 16
 // bits, 32 of 32), two slices in LDS in turn.
-//   LDS, rows: [row][8 chunks of 16 bytes], chunk c of row r at c ^ (r & 7): a fragment read
-//   takes one chunk of each of 32 rows, and the exclusive or spreads eight neighbours over all banks.
+//   LDS, rows: [row][8 chunks of 16 bytes], chunk c of row r at c ^ (r / 2 mod 8).  The 64 banks
+//   hold two rows, and a fragment read takes one chunk of each of 16 rows at a time: the exclusive
+//   or puts those of the eight even (odd) rows on different banks (with r mod 8 half of all LDS
+//   cycles were conflicts).
 //   LDS, columns: [k][columns].  16-bit fragments hold eight k of one column, so they are read
-//   with the transposing LDS load (four k of 16 columns at a time); its 32-byte blocks are
-//   spread over the banks by an exclusive or with k.  fp32 fragments are one number a lane.
+//   with the transposing LDS load, 32 bytes of each of four k and two neighbouring blocks at a
+//   time, which an exclusive or of the block with k spreads over all banks.  fp32 fragments are
+//   one number a lane.
 // Slices come in by loads that write LDS directly where both operands are aligned to 16 bytes
 // and hold whole chunks (kDirect): no registers, and what lies past the end is cleared by the
 // loads' range check.  Anything else goes through registers, chunk by chunk, ends masked.
@@ -76,15 +79,15 @@ struct Side {
   static constexpr int kPer = kBytes / 16 / kThreads;      // chunks a thread
   static constexpr int kRow = kCols ? SIDE / E : 8;        // chunks of a row in LDS
   static_assert(kPer >= 1 && kBytes % (16 * kThreads) == 0, "whole chunks for every thread");
-  static_assert((kThreads / kRow) % 8 == 0, "a thread's chunks share their swizzle");
+  static_assert((kThreads / kRow) % (kCols ? 4 : 16) == 0, "a thread's chunks share their swizzle");
 
   // Logical chunk at place p of LDS row r.
   static __device__ inline int unswizzle(int p, int r) {
-    if (!kCols) return p ^ (r & 7);
+    if (!kCols) return p ^ ((r >> 1) & 7);
     return sizeof(T) == 2 ? p ^ spread(r) : p;
   }
   // Chunks of columns move in pairs (32 bytes, what the transposing load takes of one k).
-  static __device__ inline int spread(int k) { return ((k & 3) << 1) & (kRow - 1); }
+  static __device__ inline int spread(int k) { return SIDE >= 128 ? (k & 3) << 2 : (k & 2) << 1; }
 
   // Reads the slice from k0 on (first: the tile's first row or column) into LDS.
   struct Direct {
@@ -154,7 +157,7 @@ struct Side {
     const int h = lane >> 5;
     if (!kCols) {
       const int r = at + (lane & 31);
-      return *reinterpret_cast<const Chunk*>(lds + r * 128 + (((2 * s + h) ^ (r & 7)) << 4));
+      return *reinterpret_cast<const Chunk*>(lds + r * 128 + (((2 * s + h) ^ ((r >> 1) & 7)) << 4));
     }
     Chunk t;
     if (sizeof(T) == 2) {
