@@ -89,37 +89,49 @@ struct Side {
   // Chunks of columns move in pairs (32 bytes, what the transposing load takes of one k).
   static __device__ inline int spread(int k) { return SIDE >= 128 ? (k & 3) << 2 : (k & 2) << 1; }
 
-  // Reads the slice from k0 on (first: the tile's first row or column) into LDS.
+  // Reads slices from k0 on (first: the tile's first row or column) into LDS.
   struct Direct {
     int off[kPer];
-    int k[kPer];
     const char* p;
-    int64_t left, step;   // bytes from p to the operand's end; per slice
+    uint64_t left;        // bytes from p to the operand's end
+    int64_t step;         // bytes of a slice
+    static constexpr int kFar = 0x7ffffff0, kMost = 0x7fffff00;   // an offset out of any range
+    static __device__ inline int place(int i, int& r) {
+      const int q = threadIdx.x + i * kThreads;
+      r = q / kRow;
+      return unswizzle(q % kRow, r);
+    }
     __device__ inline void start(const T* base, int64_t ld, int64_t first, int n, int K, int k0) {
       const int64_t at = kCols ? k0 * ld + first : first * ld + k0;
       const int64_t all = kCols ? (K - 1) * ld + n : (n - 1) * ld + K;
       p = reinterpret_cast<const char*>(base + at);
-      left = (all - at) * static_cast<int64_t>(sizeof(T));
+      left = static_cast<uint64_t>((all - at) * static_cast<int64_t>(sizeof(T)));
       step = (kCols ? BK * ld : BK) * static_cast<int64_t>(sizeof(T));
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r);
+        int r;
+        const int c = place(i, r);
         off[i] = static_cast<int>(r * ld) * static_cast<int>(sizeof(T)) + 16 * c;
-        k[i] = kCols ? r : c * E;
       }
     }
-    // `have`: k values from here to the end; chunks past it are read as zero.
-    __device__ inline void issue(char* lds, int have) {
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0,
-                                                          static_cast<uint32_t>(max(min(left, int64_t{0x7fffff00}), int64_t{0})), 0x00020000);
-      char* dst = lds + (threadIdx.x / 64) * 1024;
+    // With `have` k values from here to the end, fewer than a slice: chunks past it are read as zero,
+    // in this and every later slice.
+    __device__ inline void end(int have) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int o = have >= BK || k[i] < have ? off[i] : 0x7ffffff0;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (LdsVoid*)(dst + i * kThreads * 16), 16, o, 0, 0, 0);
+        int r;
+        const int c = place(i, r);
+        if ((kCols ? r : c * E) >= have) off[i] = kFar;
       }
+    }
+    __device__ inline void issue(char* lds, int wave) {
+      const uint32_t range = left >= kMost ? kMost : static_cast<uint32_t>(left);
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, range, 0x00020000);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (LdsVoid*)(lds + wave * 1024 + i * kThreads * 16), 16, off[i], 0, 0, 0);
       p += step;
-      left -= step;
+      left -= static_cast<uint64_t>(step);
     }
     __device__ inline void commit(char*) {}
   };
@@ -132,6 +144,7 @@ struct Side {
     __device__ inline void start(const T* base, int64_t ld_, int64_t first_, int n_, int K_, int k0_) {
       p = base, ld = ld_, first = first_, n = n_, K = K_, k0 = k0_;
     }
+    __device__ inline void end(int) {}
     __device__ inline void issue(char*, int) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -152,6 +165,7 @@ struct Side {
     }
   };
 
+  static constexpr int kReads = kCols ? (sizeof(T) == 4 ? 4 : 2) : 1;   // LDS reads of a fragment
   // Fragment: 16 bytes a lane, k = 2E s + E (lane / 32) .., index at + lane % 32.
   static __device__ inline Chunk fragment(const char* lds, int at, int s, int lane) {
     const int h = lane >> 5;
@@ -203,6 +217,20 @@ __device__ inline void barrier_after_loads() {
   __syncthreads();
 }
 
+// Order for the instruction scheduler: N products, with R LDS reads and L loads spread between them.
+template <int I, int N, int R, int L>
+__device__ inline void mix_products() {
+  if constexpr (I < N) {
+    constexpr int reads = (I + 1) * R / N - I * R / N, loads = (I + 1) * L / N - I * L / N;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+    mix_products<I + 1, N, R, L>();
+  } else {
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // Tile of id (bands of eight tile rows, so that the tiles that run together share rows and columns).
 __device__ inline void place_tile(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int band = id / (8 * tiles_n), in = id - band * 8 * tiles_n, high = min(8, tiles_m - 8 * band);
@@ -212,6 +240,7 @@ __device__ inline void place_tile(int id, int tiles_m, int tiles_n, int& tm, int
 
 template <class T, int BM, int BN, int WM, int WN, bool kACols, bool kBCols, bool kDirect>
 __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs no body, and drops launch stubs over builtins it does not know
   constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, BK = slice<T>();
   constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
   using A = Side<T, BM, kACols, kThreads>;
@@ -240,9 +269,14 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     typename std::conditional<kDirect, typename B::Direct, typename B::Staged>::type lb;
     la.start(static_cast<const T*>(a.a), a.lda, m0, a.M, a.K, k0);
     lb.start(static_cast<const T*>(a.b), a.ldb, n0, a.N, a.K, k0);
-    const auto issue = [&](char* lds, int t) {
-      la.issue(lds, k1 - k0 - t * BK);
-      lb.issue(lds + A::kBytes, k1 - k0 - t * BK);
+    // Loads of slice t on their way (in order of t).
+    const auto prepare = [&](int t) {
+      const int have = k1 - k0 - t * BK;
+      if (kDirect && have < BK) la.end(have), lb.end(have);
+    };
+    const auto issue = [&](char* lds) {
+      la.issue(lds, wave);
+      lb.issue(lds + A::kBytes, wave);
     };
     const auto commit = [&](char* lds) {
       la.commit(lds);
@@ -255,34 +289,42 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
       for (int j = 0; j < NI; ++j) fb[s & 1][j] = B::fragment(lds + A::kBytes, wn * TN + 32 * j, s, lane);
 #pragma unroll
       for (int i = 0; i < MI; ++i) fa[s & 1][i] = A::fragment(lds, wm * TM + 32 * i, s, lane);
-      __builtin_amdgcn_sched_barrier(0);
     };
     const auto products = [&](int s) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = multiply<T>(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
     };
+    // Order of a step: LDS reads (and loads) between the products, so that the matrix pipe is never
+    // without work while they are issued.
+    constexpr int kProducts = MI * NI * (sizeof(T) == 4 ? 4 : 1);
+    constexpr int kReads = MI * A::kReads + NI * B::kReads, kLoads = A::kPer + B::kPer;
     // Slice t, whose first fragments are read already, from `cur`.  After its last ones are, one
     // barrier frees `cur` for slice t + 2 and opens slice t + 1, whose loads are a slice old by then.
     // What is read past the last slice is not used.
     const auto walk = [&](char* cur, char* nxt, int t) {
-      if (!kDirect) issue(nxt, t + 1);
+      prepare(t + 2);
+      if (!kDirect) issue(nxt);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 3; ++s) {
         read(cur, s + 1);
         products(s);
+        mix_products<0, kProducts, kReads, 0>();
       }
       if (!kDirect) commit(nxt);
       barrier_after_loads();
-      if (kDirect) issue(cur, t + 2);
+      if (kDirect) issue(cur);
       read(nxt, 0);
       products(3);
+      mix_products<0, kProducts, kReads, kDirect ? kLoads : 0>();
     };
-    issue(even, 0);
+    prepare(0);
+    issue(even);
     commit(even);
-    if (kDirect) issue(odd, 1);
+    prepare(1);
+    if (kDirect) issue(odd);
     barrier_after_loads();
     read(even, 0);
     int t = 0;
@@ -340,6 +382,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     }
     __syncthreads();
   }
+#endif
 }
 
 constexpr int kMaxGroups = 1 << 20;
