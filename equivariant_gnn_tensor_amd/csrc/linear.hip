@@ -46,8 +46,7 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(const SlopeArgs a, cons
       load<8, false>(static_cast<const T*>(a.y_bar) + r * a.ybs, c, a.cols, v);
       if (a.z != nullptr) {
         load<8, false>(static_cast<const T*>(a.z) + r * a.zs, c, a.cols, z);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= slope<sizeof(T) == 4>(z[k], a.act);
+        times_slope<sizeof(T) == 4>(v, z, a.act);
       }
       if (a.z_bar != nullptr) store<8, false>(static_cast<T*>(a.z_bar) + r * a.zbs, c, a.cols, v);
 #pragma unroll
@@ -149,8 +148,8 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
   const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
   const int64_t bk = 128 / size;
   if (split) {
-    s.tile = std::min(a.M, a.N) > 64 ? 128 : 64;
-    const int64_t want = std::max<int64_t>(1, 512 / tiles(s.tile)), most = std::max<int64_t>(1, a.K / 512);
+    s.tile = size == 2 && std::min(a.M, a.N) >= 256 ? 256 : std::min(a.M, a.N) > 64 ? 128 : 64;
+    const int64_t want = std::max<int64_t>(1, (s.tile == 256 ? 256 : 512) / tiles(s.tile)), most = std::max<int64_t>(1, a.K / 512);
     int64_t each = (a.K + std::min(want, most) - 1) / std::min(want, most);
     each = (each + bk - 1) / bk * bk;
     s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));

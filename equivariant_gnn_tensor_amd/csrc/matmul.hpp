@@ -406,7 +406,8 @@ hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
 template <class T>
 hipError_t launch(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s) {
   if (shape.direct) {
-    if (sizeof(T) == 2 && shape.tile == 256) return launch_tiles<T, sizeof(T) == 2 ? 256 : 128, sizeof(T) == 2 ? 256 : 128, sizeof(T) == 2 ? 2 : 2, sizeof(T) == 2 ? 4 : 2, true>(a, form, s);
+    if constexpr (sizeof(T) == 2)
+      if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, true>(a, form, s);
     if (shape.tile >= 128) return launch_tiles<T, 128, 128, 2, 2, true>(a, form, s);
     return launch_tiles<T, 64, 64, 2, 2, true>(a, form, s);
   }
