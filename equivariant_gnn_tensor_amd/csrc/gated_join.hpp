@@ -13,6 +13,7 @@
 // everything between load and store are fp32, and y comes from the unrounded h.
 #pragma once
 
+#include "activation.hpp"
 #include "gated_join_args.hpp"
 #include "layer_norm.hpp"
 
@@ -24,8 +25,7 @@ using norm::Span;
 // p = 1 / (1 + exp(-g)) and 1 - p, neither by a difference and from one exp that cannot overflow.
 template <bool kWide>
 __device__ inline void gate_pair(float g, float& p, float& q) {
-  const float e = kWide ? expf(-fabsf(g)) : __expf(-fabsf(g));
-  const float r = kWide ? 1.f / (1.f + e) : __frcp_rn(1.f + e), er = e * r;
+  const float e = exp_of<kWide>(-1.f, fabsf(g)), r = inverse<kWide>(1.f + e), er = e * r;
   p = g >= 0.f ? r : er;
   q = g >= 0.f ? er : r;
 }

@@ -440,7 +440,7 @@ typedef enum {
  * w + i * w_in_stride + o * w_out_stride, and one of the two strides is 1: weights stored either
  * way are read in place.  Sums are taken in fp32, y comes from the unrounded z, and each result is
  * rounded once.  n_in, n_out >= 1; n_rows n_in, n_rows n_out and n_in n_out < 2^56.  NaN stays NaN;
- * silu and gelu of -inf are -0. */
+ * silu and gelu of -inf are 0. */
 etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, const void* x, int64_t x_stride,
                         const void* w, int64_t w_in_stride, int64_t w_out_stride, const float* b, const void* residual,
                         int64_t residual_stride, int32_t act, void* y, int64_t y_stride, void* z, int64_t z_stride,
