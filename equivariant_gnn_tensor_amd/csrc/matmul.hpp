@@ -212,9 +212,18 @@ __device__ inline Acc multiply(const Chunk& b, const Chunk& a, Acc acc) {
 
 // Barrier after which every wave's loads into LDS are there: a barrier alone waits for a wave's
 // own LDS reads and writes, not for its loads on their way to LDS.
+template <int kPending = 0>   // youngest loads (and stores) that may still be under way
 __device__ inline void barrier_after_loads() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+  static_assert(kPending < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (kPending & 15) | (kPending >> 4) << 14);   // vmcnt
   __syncthreads();
+}
+
+// Where chunk c (four floats) of row r lies among a wave's 32 x TN results on their way out: writes
+// take one chunk of 16 rows at a time, reads all of one or two rows, both from all banks.
+template <int TN>
+__device__ inline int turn_at(int r, int c) {
+  return r * TN + ((c ^ (TN == 64 ? r & 15 : (r >> 1) & 7)) << 2);
 }
 
 // Order for the instruction scheduler: N products, with R LDS reads and L loads spread between them.
@@ -246,29 +255,39 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
   using A = Side<T, BM, kACols, kThreads>;
   using B = Side<T, BN, kBCols, kThreads>;
   constexpr int kStage = A::kBytes + B::kBytes;
-  constexpr int kPitch = TN + 4, kTurn = 32 * kPitch * 4;   // a wave's 32 rows on their way out
-  static_assert(kTurn * kWaves <= 2 * kStage && kWaves % 2 == 0, "the epilogue turns its rows over in the slices' space");
-  __shared__ __attribute__((aligned(16))) char even[kStage];
-  __shared__ __attribute__((aligned(16))) char odd[kStage];
+  static_assert(32 * TN * 4 * kWaves <= kStage, "the epilogue turns its rows over in the second slice's space");
+  constexpr int kVecs = TN / 8, kRows = 64 / kVecs;   // of the epilogue: vectors a row, rows a pass
+  constexpr int kStores = MI * 32 / kRows;
+  __shared__ __attribute__((aligned(16))) char one[kStage];
+  __shared__ __attribute__((aligned(16))) char two[kStage];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
   const int per = a.tiles_m * a.tiles_n, total = per * a.splits;
   const int h = lane >> 5;
-  for (int id = gridDim.x == static_cast<unsigned>(total) ? node_block(blockIdx.x, gridDim.x) : blockIdx.x; id < total;
-       id += gridDim.x) {
+  typename std::conditional<kDirect, typename A::Direct, typename A::Staged>::type la;
+  typename std::conditional<kDirect, typename B::Direct, typename B::Staged>::type lb;
+  int64_t m0, n0;
+  int k0, k1;
+  // A tile's place, and its first slice's loads on their way to `one`.
+  const auto open = [&](int id) {
     const int split = id / per;
     int tm, tn;
     place_tile(id - split * per, a.tiles_m, a.tiles_n, tm, tn);
-    const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
-    const int k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
-    const int slices = (k1 - k0 + BK - 1) / BK;
-
-    Acc acc[MI][NI] = {};
-    typename std::conditional<kDirect, typename A::Direct, typename A::Staged>::type la;
-    typename std::conditional<kDirect, typename B::Direct, typename B::Staged>::type lb;
+    m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
+    k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
     la.start(static_cast<const T*>(a.a), a.lda, m0, a.M, a.K, k0);
     lb.start(static_cast<const T*>(a.b), a.ldb, n0, a.N, a.K, k0);
+    if (kDirect && k1 - k0 < BK) la.end(k1 - k0), lb.end(k1 - k0);
+    la.issue(one, wave);
+    lb.issue(one + A::kBytes, wave);
+  };
+  int id = node_block(blockIdx.x, gridDim.x);
+  open(id);
+  bool whole = false;   // the tile before lay inside C as a whole: each wave issued kStores stores at least for y (and z)
+  for (;;) {
+    const int slices = (k1 - k0 + BK - 1) / BK;
+    Acc acc[MI][NI] = {};
     // Loads of slice t on their way (in order of t).
     const auto prepare = [&](int t) {
       const int have = k1 - k0 - t * BK;
@@ -320,26 +339,31 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
       products(3);
       mix_products<0, kProducts, kReads, kDirect ? kLoads : 0>();
     };
-    prepare(0);
-    issue(even);
-    commit(even);
+    commit(one);
     prepare(1);
-    if (kDirect) issue(odd);
-    barrier_after_loads();
-    read(even, 0);
+    if (kDirect) issue(two);
+    // The first slice has come; the second, and what the epilogue before stored, may be under way.
+    constexpr int kPending = kDirect ? kLoads : 0;
+    if (!whole) barrier_after_loads<kPending>();
+    else if (a.z == nullptr) barrier_after_loads<kPending + kStores>();
+    else barrier_after_loads<kPending + 2 * kStores>();
+    read(one, 0);
     int t = 0;
     for (; t + 2 <= slices; t += 2) {
-      walk(even, odd, t);
-      walk(odd, even, t + 1);
+      walk(one, two, t);
+      walk(two, one, t + 1);
     }
-    if (t < slices) walk(even, odd, t);
+    if (t < slices) walk(one, two, t);
     barrier_after_loads();
 
-    // ---- epilogue
-    char* const space = wave < kWaves / 2 ? even + wave * kTurn : odd + (wave - kWaves / 2) * kTurn;
-    float* const turn = reinterpret_cast<float*>(space);
-    constexpr int kVecs = TN / 8, kRows = 64 / kVecs;   // vectors a row, rows a pass
+    // ---- epilogue, while the next tile's first slice is under way
+    const int64_t me = m0 + wm * TM;
     const int n = static_cast<int>(n0) + wn * TN + (lane % kVecs) * 8;
+    const int64_t part_row = static_cast<int64_t>(k0 / a.k_split) * a.M;
+    whole = a.part == nullptr && m0 + BM <= a.M && n0 + BN <= a.N;
+    id += gridDim.x;
+    if (kDirect && id < total) open(id);
+    float* const turn = reinterpret_cast<float*>(two) + wave * 32 * TN;
     float bias[8] = {};
     if (a.bias != nullptr && n < a.N) load<8, false>(a.bias, n, a.N, bias);
 #pragma unroll
@@ -349,20 +373,19 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const VecN<float, 4> v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          *reinterpret_cast<VecN<float, 4>*>(turn + (lane & 31) * kPitch + 32 * j + 8 * q + 4 * h) = v;
+          *reinterpret_cast<VecN<float, 4>*>(turn + turn_at<TN>(lane & 31, 8 * j + 2 * q + h)) = v;
         }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
       for (int p = 0; p < 32 / kRows; ++p) {
         const int r = p * kRows + lane / kVecs;
-        const int64_t m = m0 + wm * TM + 32 * i + r;
+        const int64_t m = me + 32 * i + r;
         if (m < a.M && n < a.N) {
           float v[8];
-          const float* src = turn + r * kPitch + (lane % kVecs) * 8;
-          __builtin_memcpy(v, src, 16);
-          __builtin_memcpy(v + 4, src + 4, 16);
+          __builtin_memcpy(v, turn + turn_at<TN>(r, lane % kVecs * 2), 16);
+          __builtin_memcpy(v + 4, turn + turn_at<TN>(r, lane % kVecs * 2 + 1), 16);
           if (a.part != nullptr) {
-            store<8, false>(a.part + (static_cast<int64_t>(split) * a.M + m) * a.N, n, a.N, v);
+            store<8, false>(a.part + (part_row + m) * a.N, n, a.N, v);
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += bias[k];
@@ -380,12 +403,14 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
       }
       __builtin_amdgcn_wave_barrier();
     }
+    if (id >= total) break;
     __syncthreads();
+    if (!kDirect) open(id);
   }
 #endif
 }
 
-constexpr int kMaxGroups = 1 << 20;
+constexpr int kCus = 256;
 
 template <class T, int BM, int BN, int WM, int WN, bool kDirect>
 hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
@@ -393,7 +418,9 @@ hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
   a.tiles_n = (a.N + BN - 1) / BN;
   const int64_t total = static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.splits;
   if (total >= int64_t{1} << 31) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(total, kMaxGroups))), block(64 * WM * WN);
+  // as many workgroups as LDS holds at once, each walking its tiles
+  constexpr int resident = 160 * 1024 / (2 * 128 * (BM + BN));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(total, kCus * resident))), block(64 * WM * WN);
   if (form == MatmulForm::kRowsCols)
     matmul_kernel<T, BM, BN, WM, WN, false, true, kDirect><<<grid, block, 0, s>>>(a);
   else if (form == MatmulForm::kRowsRows)
