@@ -71,6 +71,20 @@ __device__ inline Chunk fetch_chunk(const T* __restrict__ row, int c, int n) {
   return t;
 }
 
+// 16 bytes a lane from base + off (zeros past the range) to LDS from `lds` on, lane after lane.  In
+// assembly, so that the compiler's own counting of loads does not wait for more of them (and of the
+// epilogue's stores among them) than barrier_after_loads; nothing but LDS and m0 is written (the
+// compiler keeps nothing in m0: it sets it before each use); the wait states cover m0 and scalars that
+// a vector instruction has just written.  What it counts itself is only waited
+// for earlier by that.
+typedef int Range __attribute__((ext_vector_type(4)));
+__device__ inline void load_lds(uint32_t lds, const Range& range, int off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(range));
+}
+__device__ inline uint32_t lds_address(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+
 // One operand's slice: SIDE rows (columns) of the tile by one slice of k.
 template <class T, int SIDE, bool kCols, int kThreads>
 struct Side {
@@ -124,14 +138,16 @@ struct Side {
         if ((kCols ? r : c * E) >= have) off[i] = kFar;
       }
     }
-    __device__ inline void issue(char* lds, int wave) {
-      const uint32_t range = left >= kMost ? kMost : static_cast<uint32_t>(left);
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, range, 0x00020000);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (LdsVoid*)(lds + wave * 1024 + i * kThreads * 16), 16, off[i], 0, 0, 0);
-      p += step;
-      left -= static_cast<uint64_t>(step);
+    // Load i of the slice; the last one moves on to the next slice.
+    __device__ inline void issue(char* lds, int wave, int i) {
+      const uint64_t at = reinterpret_cast<uint64_t>(p);
+      const Range range = {static_cast<int>(at), static_cast<int>(at >> 32 & 0xffff),
+                           left >= kMost ? kMost : static_cast<int>(left), 0x00020000};
+      load_lds(lds_address(lds) + wave * 1024 + i * kThreads * 16, range, off[i]);
+      if (i == kPer - 1) {
+        p += step;
+        left -= static_cast<uint64_t>(step);
+      }
     }
     __device__ inline void commit(char*) {}
   };
@@ -145,7 +161,8 @@ struct Side {
       p = base, ld = ld_, first = first_, n = n_, K = K_, k0 = k0_;
     }
     __device__ inline void end(int) {}
-    __device__ inline void issue(char*, int) {
+    __device__ inline void issue(char*, int, int last) {
+      if (last != kPer - 1) return;   // all at once
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r) * E;
@@ -165,7 +182,6 @@ struct Side {
     }
   };
 
-  static constexpr int kReads = kCols ? (sizeof(T) == 4 ? 4 : 2) : 1;   // LDS reads of a fragment
   // Fragment: 16 bytes a lane, k = 2E s + E (lane / 32) .., index at + lane % 32.
   static __device__ inline Chunk fragment(const char* lds, int at, int s, int lane) {
     const int h = lane >> 5;
@@ -210,34 +226,26 @@ __device__ inline Acc multiply(const Chunk& b, const Chunk& a, Acc acc) {
   }
 }
 
-// Barrier after which every wave's loads into LDS are there: a barrier alone waits for a wave's
-// own LDS reads and writes, not for its loads on their way to LDS.
-template <int kPending = 0>   // youngest loads (and stores) that may still be under way
+// Barrier after which every wave's loads into LDS, but for its kPending youngest loads and stores,
+// have arrived, and its reads and writes of LDS are done.  (The library's barrier would wait for
+// loads into LDS in some places and for all loads in others.)
+template <int kPending>
 __device__ inline void barrier_after_loads() {
   static_assert(kPending < 64, "six bits");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (kPending & 15) | (kPending >> 4) << 14);   // vmcnt
-  __syncthreads();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (kPending & 15) | (kPending >> 4) << 14);   // vmcnt(kPending) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
+
+__device__ inline void barrier_after_reads() { barrier_after_loads<63>(); }
 
 // Where chunk c (four floats) of row r lies among a wave's 32 x TN results on their way out: writes
 // take one chunk of 16 rows at a time, reads all of one or two rows, both from all banks.
 template <int TN>
 __device__ inline int turn_at(int r, int c) {
   return r * TN + ((c ^ (TN == 64 ? r & 15 : (r >> 1) & 7)) << 2);
-}
-
-// Order for the instruction scheduler: N products, with R LDS reads and L loads spread between them.
-template <int I, int N, int R, int L>
-__device__ inline void mix_products() {
-  if constexpr (I < N) {
-    constexpr int reads = (I + 1) * R / N - I * R / N, loads = (I + 1) * L / N - I * L / N;
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
-    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
-    mix_products<I + 1, N, R, L>();
-  } else {
-    __builtin_amdgcn_sched_barrier(0);
-  }
 }
 
 // Tile of id (bands of eight tile rows, so that the tiles that run together share rows and columns).
@@ -257,7 +265,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
   constexpr int kStage = A::kBytes + B::kBytes;
   static_assert(32 * TN * 4 * kWaves <= kStage, "the epilogue turns its rows over in the second slice's space");
   constexpr int kVecs = TN / 8, kRows = 64 / kVecs;   // of the epilogue: vectors a row, rows a pass
-  constexpr int kStores = MI * 32 / kRows;
+  constexpr int kPasses = 32 / kRows, kStores = MI * kPasses;
   __shared__ __attribute__((aligned(16))) char one[kStage];
   __shared__ __attribute__((aligned(16))) char two[kStage];
 
@@ -269,8 +277,17 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
   typename std::conditional<kDirect, typename B::Direct, typename B::Staged>::type lb;
   int64_t m0, n0;
   int k0, k1;
+  constexpr int kLoads = A::kPer + B::kPer;
+  const auto issue_one = [&](char* lds, int i) __attribute__((always_inline)) {
+    if (i < A::kPer) la.issue(lds, wave, i);
+    else lb.issue(lds + A::kBytes, wave, i - A::kPer);
+  };
+  const auto issue = [&](char* lds) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) issue_one(lds, i);
+  };
   // A tile's place, and its first slice's loads on their way to `one`.
-  const auto open = [&](int id) {
+  const auto open = [&](int id) __attribute__((always_inline)) {
     const int split = id / per;
     int tm, tn;
     place_tile(id - split * per, a.tiles_m, a.tiles_n, tm, tn);
@@ -279,8 +296,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     la.start(static_cast<const T*>(a.a), a.lda, m0, a.M, a.K, k0);
     lb.start(static_cast<const T*>(a.b), a.ldb, n0, a.N, a.K, k0);
     if (kDirect && k1 - k0 < BK) la.end(k1 - k0), lb.end(k1 - k0);
-    la.issue(one, wave);
-    lb.issue(one + A::kBytes, wave);
+    issue(one);
   };
   int id = node_block(blockIdx.x, gridDim.x);
   open(id);
@@ -289,56 +305,54 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     const int slices = (k1 - k0 + BK - 1) / BK;
     Acc acc[MI][NI] = {};
     // Loads of slice t on their way (in order of t).
-    const auto prepare = [&](int t) {
+    const auto prepare = [&](int t) __attribute__((always_inline)) {
       const int have = k1 - k0 - t * BK;
       if (kDirect && have < BK) la.end(have), lb.end(have);
     };
-    const auto issue = [&](char* lds) {
-      la.issue(lds, wave);
-      lb.issue(lds + A::kBytes, wave);
-    };
-    const auto commit = [&](char* lds) {
+    const auto commit = [&](char* lds) __attribute__((always_inline)) {
       la.commit(lds);
       lb.commit(lds + A::kBytes);
     };
     // Fragments are read one step of k ahead of their products.
     Chunk fa[2][MI], fb[2][NI];
-    const auto read = [&](const char* lds, int s) {
-#pragma unroll
-      for (int j = 0; j < NI; ++j) fb[s & 1][j] = B::fragment(lds + A::kBytes, wn * TN + 32 * j, s, lane);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[s & 1][i] = A::fragment(lds, wm * TM + 32 * i, s, lane);
+    const auto read_one = [&](const char* lds, int s, int i) __attribute__((always_inline)) {
+      if (i < NI) fb[s & 1][i] = B::fragment(lds + A::kBytes, wn * TN + 32 * i, s, lane);
+      else fa[s & 1][i - NI] = A::fragment(lds, wm * TM + 32 * (i - NI), s, lane);
     };
-    const auto products = [&](int s) {
+    // The products of step s, with the reads of step `next` of `from` and, with kLoad, the loads to
+    // `to` spread between them: the matrix pipe is never without work while those are issued.
+    const auto step = [&](int s, const char* from, int next, auto load, char* to) __attribute__((always_inline)) {
+      constexpr int kReads = MI + NI, kProducts = MI * NI;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < kProducts; ++i) {
+        const int m = i / NI, n = m & 1 ? NI - 1 - i % NI : i % NI;
+        acc[m][n] = multiply<T>(fb[s & 1][n], fa[s & 1][m], acc[m][n]);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = multiply<T>(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
+        for (int r = i * kReads / kProducts; r < (i + 1) * kReads / kProducts; ++r) read_one(from, next, r);
+        if (decltype(load)::value)
+#pragma unroll
+          for (int l = i * kLoads / kProducts; l < (i + 1) * kLoads / kProducts; ++l) issue_one(to, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
-    // Order of a step: LDS reads (and loads) between the products, so that the matrix pipe is never
-    // without work while they are issued.
-    constexpr int kProducts = MI * NI * (sizeof(T) == 4 ? 4 : 1);
-    constexpr int kReads = MI * A::kReads + NI * B::kReads, kLoads = A::kPer + B::kPer;
     // Slice t, whose first fragments are read already, from `cur`.  After its last ones are, one
     // barrier frees `cur` for slice t + 2 and opens slice t + 1, whose loads are a slice old by then.
     // What is read past the last slice is not used.
-    const auto walk = [&](char* cur, char* nxt, int t) {
+    const auto walk = [&](char* cur, char* nxt, int t) __attribute__((always_inline)) {
       prepare(t + 2);
       if (!kDirect) issue(nxt);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        read(cur, s + 1);
-        products(s);
-        mix_products<0, kProducts, kReads, 0>();
-      }
+      for (int s = 0; s < 3; ++s) step(s, cur, s + 1, std::false_type{}, cur);
       if (!kDirect) commit(nxt);
-      barrier_after_loads();
-      if (kDirect) issue(cur);
-      read(nxt, 0);
-      products(3);
-      mix_products<0, kProducts, kReads, kDirect ? kLoads : 0>();
+      barrier_after_loads<0>();
+      step(3, nxt, 0, std::integral_constant<bool, kDirect>{}, cur);
     };
+    float bias[8] = {};
+    {
+      const int n = static_cast<int>(n0) + wn * TN + (lane % kVecs) * 8;
+      if (a.bias != nullptr && n < a.N) load<8, false>(a.bias, n, a.N, bias);
+    }
     commit(one);
     prepare(1);
     if (kDirect) issue(two);
@@ -347,14 +361,15 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     if (!whole) barrier_after_loads<kPending>();
     else if (a.z == nullptr) barrier_after_loads<kPending + kStores>();
     else barrier_after_loads<kPending + 2 * kStores>();
-    read(one, 0);
+#pragma unroll
+    for (int r = 0; r < MI + NI; ++r) read_one(one, 0, r);
     int t = 0;
     for (; t + 2 <= slices; t += 2) {
       walk(one, two, t);
       walk(two, one, t + 1);
     }
     if (t < slices) walk(one, two, t);
-    barrier_after_loads();
+    barrier_after_loads<0>();
 
     // ---- epilogue, while the next tile's first slice is under way
     const int64_t me = m0 + wm * TM;
@@ -363,9 +378,11 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     whole = a.part == nullptr && m0 + BM <= a.M && n0 + BN <= a.N;
     id += gridDim.x;
     if (kDirect && id < total) open(id);
+    asm volatile("" ::: "memory");   // the stores below are younger than those loads
+    __builtin_amdgcn_sched_barrier(0);
     float* const turn = reinterpret_cast<float*>(two) + wave * 32 * TN;
-    float bias[8] = {};
-    if (a.bias != nullptr && n < a.N) load<8, false>(a.bias, n, a.N, bias);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) asm volatile("" ::"v"(bias[k]));   // arrived long ago: nothing after has to wait for it
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -376,35 +393,37 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
           *reinterpret_cast<VecN<float, 4>*>(turn + turn_at<TN>(lane & 31, 8 * j + 2 * q + h)) = v;
         }
       __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-      for (int p = 0; p < 32 / kRows; ++p) {
-        const int r = p * kRows + lane / kVecs;
-        const int64_t m = me + 32 * i + r;
-        if (m < a.M && n < a.N) {
-          float v[8];
-          __builtin_memcpy(v, turn + turn_at<TN>(r, lane % kVecs * 2), 16);
-          __builtin_memcpy(v + 4, turn + turn_at<TN>(r, lane % kVecs * 2 + 1), 16);
-          if (a.part != nullptr) {
-            store<8, false>(a.part + (part_row + m) * a.N, n, a.N, v);
-          } else {
+      float v[kPasses][8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += bias[k];
-            if (a.z != nullptr) store<8, false>(static_cast<T*>(a.z) + m * a.ldz, n, a.N, v);
-            if (a.act != ETPC_ACT_NONE) activate<sizeof(T) == 4>(v, a.act);
-            if (a.res != nullptr) {
-              float w[8];
-              load<8, false>(static_cast<const T*>(a.res) + m * a.ldres, n, a.N, w);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] += w[k];
-            }
-            store<8, false>(static_cast<T*>(a.c) + m * a.ldc, n, a.N, v);
-          }
-        }
+      for (int p = 0; p < kPasses; ++p) {
+        const int r = p * kRows + lane / kVecs, c = lane % kVecs * 2;
+        __builtin_memcpy(v[p], turn + turn_at<TN>(r, c), 16);
+        __builtin_memcpy(v[p] + 4, turn + turn_at<TN>(r, c + 1), 16);
       }
       __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int64_t m = me + 32 * i + p * kRows + lane / kVecs;
+        if (m >= a.M || n >= a.N) continue;
+        if (a.part != nullptr) {
+          store<8, false>(a.part + (part_row + m) * a.N, n, a.N, v[p]);
+          continue;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[p][k] += bias[k];
+        if (a.z != nullptr) stream<8>(static_cast<T*>(a.z) + m * a.ldz, n, a.N, v[p]);
+        if (a.act != ETPC_ACT_NONE) activate<sizeof(T) == 4>(v[p], a.act);
+        if (a.res != nullptr) {
+          float w[8];
+          load<8, false>(static_cast<const T*>(a.res) + m * a.ldres, n, a.N, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[p][k] += w[k];
+        }
+        stream<8>(static_cast<T*>(a.c) + m * a.ldc, n, a.N, v[p]);
+      }
     }
     if (id >= total) break;
-    __syncthreads();
+    barrier_after_reads();
     if (!kDirect) open(id);
   }
 #endif

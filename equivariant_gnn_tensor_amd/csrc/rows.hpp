@@ -84,6 +84,27 @@ __device__ inline void store(T* __restrict__ p, int c, int n, const float (&v)[N
   }
 }
 
+// The same for a result that is as large as the caches or larger and read by a later kernel: whole
+// vectors go out past L2 (65408 x 4096 bf16 results of a product: 566 us with store, 542 with this,
+// since what L2 keeps instead are the product's operands).
+template <int N, class T>
+__device__ inline void stream(T* __restrict__ p, int c, int n, const float (&v)[N]) {
+  typedef T Piece __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+  constexpr int E = 16 / sizeof(T);
+  static_assert(N % E == 0, "whole 16-byte pieces");
+  if (c + N <= n) {
+#pragma unroll
+    for (int i = 0; i < N; i += E) {
+      Piece t;
+#pragma unroll
+      for (int k = 0; k < E; ++k) t[k] = static_cast<T>(v[i + k]);
+      __builtin_nontemporal_store(t, reinterpret_cast<Piece*>(p + c + i));
+    }
+  } else {
+    store<N, false>(p, c, n, v);
+  }
+}
+
 // v + its value in the lane 16 (32) away: the swap instructions exchange 16-lane rows
 // (wave halves) between two registers, so the sum of both results is the pair's sum.
 __device__ inline float add_lane16(float v) {
