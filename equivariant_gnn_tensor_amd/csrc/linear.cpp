@@ -3,6 +3,7 @@
 
 #include "kernels.hpp"
 #include "linear.hpp"
+#include "narrow_args.hpp"
 #include "operands.hpp"
 #include "profile.hpp"
 
@@ -56,6 +57,11 @@ MatmulArgs weight_product(int64_t rows, int64_t n_in, int64_t n_out, bool by_out
 // The same whatever the layout of w, the addresses and the wanted outputs.
 LinearSpace linear_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act) {
   LinearSpace s{};
+  if (narrow::fits_bwd(n_in, n_out)) {
+    s.b_part = round256(static_cast<size_t>(narrow::bwd_groups(rows)) * static_cast<size_t>(n_in * n_out + n_out) * sizeof(float));
+    s.bytes = s.b_part;
+    return s;
+  }
   const int64_t size = size_of(dtype);
   s.z_bar_stride = (n_out + 7) / 8 * 8;
   s.z_bar = act != ETPC_ACT_NONE ? round256(static_cast<size_t>(rows * s.z_bar_stride * size)) : 0;
@@ -94,6 +100,15 @@ etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dty
   ETPC_TRY(check_floats({ob}));
   ETPC_TRY(check_apart({{my, n_rows, n_out, size}, {mz, n_rows, n_out, size}},
                        {{mx, n_rows, n_in, size}, operand(mw, size), {mr, n_rows, n_out, size}, ob}));
+  if (n_in <= narrow::kMost && n_out <= narrow::kMost) {
+    narrow::FwdArgs a{};
+    a.x = x, a.w = w, a.b = b, a.res = residual, a.y = y, a.z = z;
+    a.xs = x_stride, a.ldw = mw.m.stride, a.ress = residual_stride, a.ys = y_stride, a.zs = z_stride;
+    a.rows = static_cast<int32_t>(n_rows), a.n_in = static_cast<int32_t>(n_in), a.n_out = static_cast<int32_t>(n_out);
+    a.act = act, a.by_out = mw.by_out;
+    ETPC_LAUNCH(ETPC_KIND_NODEWISE, narrow::run_fwd(a, dtype, s));
+    return ETPC_OK;
+  }
   MatmulArgs a{};
   a.a = x, a.b = w, a.c = y, a.z = z, a.res = residual, a.bias = b;
   a.lda = x_stride, a.ldb = mw.m.stride, a.ldc = y_stride, a.ldz = z_stride, a.ldres = residual_stride;
@@ -127,7 +142,7 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
   if (n_rows == 0) {
     ETPC_TRY(check_apart({operand(mwb, size), obb}, {}));
     if (w_bar != nullptr)
-      ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_sum_parts(nullptr, 0, mwb.rows, mwb.cols, w_bar, mwb.m.stride, dtype, s));
+      ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_sum_parts(nullptr, 0, mwb.rows, mwb.cols, w_bar, mwb.m.stride, nullptr, 0, dtype, s));
     if (b_bar != nullptr) ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_fill(b_bar, n_out, 0.f, s));
     return ETPC_OK;
   }
@@ -150,6 +165,20 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
                         {mz, n_rows, act != ETPC_ACT_NONE ? n_out : 0, size}}));
   if (!any) return ETPC_OK;
 
+  if (narrow::fits_bwd(n_in, n_out)) {
+    narrow::BwdArgs a{};
+    const bool sums = w_bar != nullptr || b_bar != nullptr;
+    a.x = x, a.w = w, a.y_bar = y_bar, a.z = act != ETPC_ACT_NONE ? z : nullptr, a.x_bar = x_bar;
+    if (sums) a.part = static_cast<float*>(ws);
+    a.xs = x_stride, a.ldw = mw.m.stride, a.ybs = y_bar_stride, a.zs = z_stride, a.xbs = x_bar_stride;
+    a.rows = static_cast<int32_t>(n_rows), a.n_in = static_cast<int32_t>(n_in), a.n_out = static_cast<int32_t>(n_out);
+    a.act = act, a.by_out = mw.by_out, a.wb_by_out = mwb.by_out, a.w_sums = w_bar != nullptr;
+    ETPC_LAUNCH(ETPC_KIND_NODEWISE, narrow::run_bwd(a, dtype, s));
+    if (sums)
+      ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_sum_parts(a.part, narrow::bwd_groups(n_rows), mwb.by_out ? n_in : n_out,
+                                                       mwb.by_out ? n_out : n_in, w_bar, mwb.m.stride, b_bar, n_out, dtype, s));
+    return ETPC_OK;
+  }
   char* const at = static_cast<char*>(ws);
   float* const w_part = reinterpret_cast<float*>(at + space.z_bar);
   float* const b_part = reinterpret_cast<float*>(at + space.z_bar + space.w_part);
@@ -168,7 +197,7 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
     ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_slope(a, dtype, s));
     if (b_bar != nullptr)
       ETPC_LAUNCH(ETPC_KIND_NODEWISE,
-                  launch_sum_parts(b_part, slope_parts(rows, out), 1, n_out, b_bar, n_out, ETPC_F32, s));
+                  launch_sum_parts(b_part, slope_parts(rows, out), 1, n_out, b_bar, n_out, nullptr, 0, ETPC_F32, s));
   }
   if (x_bar != nullptr) {
     MatmulArgs a{};
@@ -186,7 +215,7 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
     if (shape.splits > 1) a.part = w_part;
     ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_matmul(a, MatmulForm::kColsCols, dtype, shape, s));
     if (shape.splits > 1)
-      ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_sum_parts(w_part, shape.splits, a.M, a.N, w_bar, a.ldc, dtype, s));
+      ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_sum_parts(w_part, shape.splits, a.M, a.N, w_bar, a.ldc, nullptr, 0, dtype, s));
   }
   return ETPC_OK;
 }

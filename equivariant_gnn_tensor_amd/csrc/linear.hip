@@ -4,6 +4,7 @@
 
 #include "activation.hpp"
 #include "linear.hpp"
+#include "narrow_args.hpp"
 #include "rows.hpp"
 
 namespace etpc {
@@ -70,10 +71,11 @@ __global__ __launch_bounds__(kThreads) void slope_kernel(const SlopeArgs a, cons
 // in order.
 template <class T, int kSlices>
 __global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float* __restrict__ part, int parts, int64_t rows,
-                                                             int64_t cols, T* __restrict__ out, int64_t ld) {
+                                                             int64_t cols, T* __restrict__ out, int64_t ld,
+                                                             float* __restrict__ tail, int64_t tail_n) {
   constexpr int kNumbers = kThreads / kSlices;
   __shared__ float lds[kSlices][kNumbers];
-  const int64_t total = rows * cols;
+  const int64_t total = rows * cols + tail_n;
   const int lane = threadIdx.x % kNumbers, slice = threadIdx.x / kNumbers;
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * kNumbers; first < total;
        first += static_cast<int64_t>(gridDim.x) * kNumbers) {
@@ -89,23 +91,30 @@ __global__ __launch_bounds__(kThreads) void sum_parts_kernel(const float* __rest
       }
     }
     if (slice == 0 && i < total) {
-      const int64_t r = i / cols;
-      out[r * ld + (i - r * cols)] = static_cast<T>(s);
+      if (i >= rows * cols) {
+        if (tail != nullptr) tail[i - rows * cols] = s;
+      } else if (out != nullptr) {
+        const int64_t r = i / cols;
+        out[r * ld + (i - r * cols)] = static_cast<T>(s);
+      }
     }
     if (kSlices > 1) __syncthreads();
   }
 }
 
 template <class T>
-hipError_t sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, hipStream_t s) {
-  const int64_t total = rows * cols;
+hipError_t sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, float* tail,
+                     int64_t tail_n, hipStream_t s) {
+  const int64_t total = rows * cols + tail_n;
   if (total == 0) return hipSuccess;
   const int slices = parts >= 16 ? 16 : 1, numbers = kThreads / slices;
   const dim3 grid(static_cast<unsigned>(std::min((total + numbers - 1) / numbers, kMaxGroups)));
   if (slices == 16)
-    sum_parts_kernel<T, 16><<<grid, kThreads, 0, s>>>(part, parts, rows, cols, static_cast<T*>(out), ld);
+    sum_parts_kernel<T, 16><<<grid, kThreads, 0, s>>>(part, parts, rows, cols, static_cast<T*>(out), ld, tail,
+                                                        tail_n);
   else
-    sum_parts_kernel<T, 1><<<grid, kThreads, 0, s>>>(part, parts, rows, cols, static_cast<T*>(out), ld);
+    sum_parts_kernel<T, 1><<<grid, kThreads, 0, s>>>(part, parts, rows, cols, static_cast<T*>(out), ld, tail,
+                                                        tail_n);
   return hipGetLastError();
 }
 
@@ -133,12 +142,37 @@ hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, int dtype,
-                            hipStream_t s) {
-  return dtype == ETPC_F32    ? sum_parts<float>(part, parts, rows, cols, out, ld, s)
-         : dtype == ETPC_BF16 ? sum_parts<Bf16>(part, parts, rows, cols, out, ld, s)
-                              : sum_parts<F16>(part, parts, rows, cols, out, ld, s);
+hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, float* tail,
+                            int64_t tail_n, int dtype, hipStream_t s) {
+  return dtype == ETPC_F32    ? sum_parts<float>(part, parts, rows, cols, out, ld, tail, tail_n, s)
+         : dtype == ETPC_BF16 ? sum_parts<Bf16>(part, parts, rows, cols, out, ld, tail, tail_n, s)
+                              : sum_parts<F16>(part, parts, rows, cols, out, ld, tail, tail_n, s);
 }
+
+// ---- narrow rows: whole chunks for every row of every operand?
+namespace narrow {
+namespace {
+bool whole(const void* p, int64_t stride, int64_t n, int64_t size) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0 && n * size % 16 == 0);
+}
+}  // namespace
+
+int bwd_groups(int64_t rows) { return static_cast<int>(std::min<int64_t>((rows + 255) / 256, 256)); }
+
+hipError_t run_fwd(const FwdArgs& a, int dtype, hipStream_t s) {
+  const bool even = whole(a.x, a.xs, a.n_in, dtype == ETPC_F32 ? 4 : 2);
+  const int groups = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(a.rows) + 127) / 128, 256 * 4));
+  return dtype == ETPC_F32 ? fwd_f32(a, even, groups, s) : dtype == ETPC_BF16 ? fwd_bf16(a, even, groups, s) : fwd_f16(a, even, groups, s);
+}
+
+hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s) {
+  const int64_t size = dtype == ETPC_F32 ? 4 : 2;
+  const bool even = whole(a.part != nullptr ? a.x : nullptr, a.xs, a.n_in, size) && whole(a.y_bar, a.ybs, a.n_out, size) &&
+                    whole(a.z, a.zs, a.n_out, size);
+  const int groups = bwd_groups(a.rows);
+  return dtype == ETPC_F32 ? bwd_f32(a, even, groups, s) : dtype == ETPC_BF16 ? bwd_bf16(a, even, groups, s) : bwd_f16(a, even, groups, s);
+}
+}  // namespace narrow
 
 MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split) {
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;

@@ -50,9 +50,10 @@ struct SlopeArgs {
 int slope_parts(int32_t rows, int32_t cols);
 hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t s);
 
-// out[r ld + c] = sum_{p < parts} part[p][rows][cols], in a fixed order, rounded to the dtype once.
-// No parts: zeros.
-hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, int dtype,
-                            hipStream_t s);
+// out[r ld + c] = sum_{p < parts} part[p][r cols + c], rounded to the dtype once, and tail[i] = the sums
+// of the tail_n numbers that follow in each part; in a fixed order.  out, tail: null skips.  No
+// parts: zeros.
+hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t cols, void* out, int64_t ld, float* tail,
+                            int64_t tail_n, int dtype, hipStream_t s);
 
 }  // namespace etpc

@@ -1,0 +1,397 @@
+// The dense layer between narrow rows (up to 128 numbers), forward and backward (templates; narrow_*.hip
+// hold the instantiations of one element type each).
+//
+//   forward:  z = x w + b, y = act(z) + residual
+//   backward: z_bar = y_bar act'(z), x_bar = z_bar w^T, w_bar = x^T z_bar, b_bar = column sums of z_bar
+//
+// Memory bound (214980 rows of 64: 20 flop a byte), so every row is read once, the weights stay in
+// LDS, and a wave works through 32 rows at a time on its own, without a barrier: lane r (and r + 32)
+// loads row r's 16-byte chunks straight into the fragments of the matrix instructions, the next
+// rows' while these are worked on.  With the weights' fragment first, a lane gets four adjacent
+// columns of one row; swapping wave halves makes that eight, which are loaded and stored as one.
+//
+// The backward pass is one kernel: z_bar is a fragment for x_bar as it stands; for w_bar, whose
+// contraction runs over rows, it and x go through a few KB of LDS of the wave and are read
+// transposed.  w_bar's and b_bar's sums stay in registers over all of a wave's rows, are added up
+// over the workgroup's waves in LDS and leave one partial sum a workgroup, added in a fixed order
+// by a second launch.
+#pragma once
+
+#include "activation.hpp"
+#include "fragments.hpp"
+#include "narrow_args.hpp"
+#include "rows.hpp"
+
+namespace etpc {
+namespace narrow {
+
+using mm::Acc;
+using mm::Chunk;
+
+// Chunks of 32-byte steps: a step holds two chunks of a row, one for each half of the wave.
+template <class T>
+constexpr int steps(int tiles) {
+  return tiles * static_cast<int>(sizeof(T));
+}
+// LDS of weights as rows of 128-byte slices, chunk c of row r at c ^ (r / 2 mod 8) (see matmul.hpp).
+template <class T>
+constexpr int slices(int tiles) {
+  return (steps<T>(tiles) + 3) / 4;
+}
+__device__ inline int weight_at(int rows, int r, int chunk) {
+  return (chunk >> 3) * rows * 128 + r * 128 + (((chunk & 7) ^ ((r >> 1) & 7)) << 4);
+}
+
+// Row r, numbers k .. of the weights: w[r ld + k] (`along`) or w[k ld + r]; zero past n rows, K numbers.
+template <class T>
+__device__ inline void fill_weights(char* lds, int rows, int chunks, const T* __restrict__ w, int64_t ld, bool along,
+                                    int n, int K) {
+  constexpr int E = 16 / sizeof(T);
+  for (int q = threadIdx.x; q < rows * chunks; q += blockDim.x) {
+    const int r = q % rows, c = q / rows;
+    Chunk t = {};
+    if (r < n) {
+      if (along) {
+        t = mm::fetch_chunk(w + r * ld, c * E, K);
+      } else {
+        T e[E] = {};
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (c * E + k < K) e[k] = w[(c * E + k) * ld + r];
+        __builtin_memcpy(&t, e, 16);
+      }
+    }
+    *reinterpret_cast<Chunk*>(lds + weight_at(rows, r, c)) = t;
+  }
+}
+
+// The chunks of a row that a lane holds: chunk 2 s + h of row r for each step s.
+template <class T, int S, bool kEven>
+struct RowChunks {
+  Chunk c[S];
+  __device__ inline void read(const void* p, int64_t at, int n, int h) {
+    constexpr int E = 16 / sizeof(T);
+    const T* row = static_cast<const T*>(p) + at;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int k = (2 * s + h) * E;
+      if (kEven) {
+        c[s] = Chunk{};
+        if (k < n) __builtin_memcpy(&c[s], row + k, 16);
+      } else {
+        c[s] = mm::fetch_chunk(row, k, n);
+      }
+    }
+  }
+};
+
+// Eight adjacent columns of a lane's row from the results of one 32-column tile: g = 0, 1 are columns
+// 16 g + 8 h ...  Halves of the wave hold four columns each; lanes 0 to 31 keep the first eight of
+// sixteen, lanes 32 to 63 the others.
+__device__ inline void eight(const Acc& acc, int g, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_int(acc[8 * g + k]), __float_as_int(acc[8 * g + 4 + k]), false, false);
+    v[k] = __int_as_float(r[0]);
+    v[4 + k] = __int_as_float(r[1]);
+  }
+}
+
+constexpr int kFwdThreads = 256;
+
+template <class T, int IT, int OT, bool kEven>
+__global__ __launch_bounds__(kFwdThreads) void fwd_kernel(const FwdArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int S = steps<T>(IT), kRows = 32 * OT;
+  __shared__ __attribute__((aligned(16))) char w[slices<T>(IT) * kRows * 128];
+  __shared__ __attribute__((aligned(16))) float bias[kRows];
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int64_t tiles = (static_cast<int64_t>(a.rows) + 31) / 32, step = static_cast<int64_t>(gridDim.x) * (kFwdThreads / 64);
+  int64_t tile = static_cast<int64_t>(blockIdx.x) * (kFwdThreads / 64) + (threadIdx.x >> 6);
+  const auto row_of = [&](int64_t t) __attribute__((always_inline)) {
+    return min(t * 32 + (lane & 31), static_cast<int64_t>(a.rows) - 1);
+  };
+  RowChunks<T, S, kEven> next;
+  if (tile < tiles) next.read(a.x, row_of(tile) * a.xs, a.n_in, h);
+  fill_weights(w, kRows, 2 * S, static_cast<const T*>(a.w), a.ldw, !a.by_out, a.n_out, a.n_in);
+  for (int o = threadIdx.x; o < kRows; o += kFwdThreads) bias[o] = a.b != nullptr && o < a.n_out ? a.b[o] : 0.f;
+  __syncthreads();
+  for (; tile < tiles; tile += step) {
+    const RowChunks<T, S, kEven> now = next;
+    if (tile + step < tiles) next.read(a.x, row_of(tile + step) * a.xs, a.n_in, h);
+    if (IT * OT * sizeof(T) > 8) asm volatile("" ::: "memory");   // the weights stay in LDS: registers do not hold them
+    Acc acc[OT] = {};
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < OT; ++j) {
+        const Chunk f = *reinterpret_cast<const Chunk*>(w + weight_at(kRows, 32 * j + (lane & 31), 2 * s + h));
+        acc[j] = mm::multiply<T>(f, now.c[s], acc[j]);
+      }
+    const int64_t m = tile * 32 + (lane & 31);
+    if (m >= a.rows) continue;
+#pragma unroll
+    for (int j = 0; j < OT; ++j)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int n = 32 * j + 16 * g + 8 * h;
+        float v[8], b[8];
+        eight(acc[j], g, v);
+        if (n >= a.n_out) continue;
+        __builtin_memcpy(b, bias + n, 32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += b[k];
+        if (a.z != nullptr) store<8, false>(static_cast<T*>(a.z) + m * a.zs, n, a.n_out, v);
+        if (a.act != ETPC_ACT_NONE) activate<sizeof(T) == 4>(v, a.act);
+        if (a.res != nullptr) {
+          load<8, false>(static_cast<const T*>(a.res) + m * a.ress, n, a.n_out, b);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] += b[k];
+        }
+        store<8, false>(static_cast<T*>(a.y) + m * a.ys, n, a.n_out, v);
+      }
+  }
+#endif
+}
+
+// ---------------------------------------------------------------- backward
+// A wave's 32 rows of C chunks on their way through LDS.  Written a chunk of 16 rows at a time; read
+// transposed, four rows of two 32-byte blocks (16 bits) or two rows of 32 numbers (fp32): the
+// exclusive or spreads the first over half the banks, the others over all (fp32 rows of 32: half).
+template <class T, int C>
+__device__ inline int tile_at(int r, int c) {
+  const int f = sizeof(T) == 2 ? (C == 8 ? (r & 2) << 1 | (r & 4) >> 1 : (r & 3) << 2 | (r & 4) >> 1)
+                : C == 8       ? (r >> 1) & 7
+                               : (r & 3) | (r & 4) << 1 | (r & 8) >> 1;
+  return r * (C * 16) + ((c ^ f) << 4);
+}
+// Fragment of columns at .. at + 31 with rows as k (rows 16 s .. for 16 bits, 8 s .. for fp32).
+template <class T, int C>
+__device__ inline Chunk column_fragment(const char* lds, int at, int s, int lane) {
+  Chunk t;
+  if constexpr (sizeof(T) == 2) {
+    const int k = 16 * s + 8 * (lane >> 5) + ((lane & 15) >> 2), col = at + (lane & 16) + (lane & 3) * 4;
+    const mm::Tr4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm::LdsTr4*)(lds + tile_at<T, C>(k, col >> 3) + (col & 7) * 2));
+    const mm::Tr4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm::LdsTr4*)(lds + tile_at<T, C>(k + 4, col >> 3) + (col & 7) * 2));
+    __builtin_memcpy(&t, &lo, 8);
+    __builtin_memcpy(reinterpret_cast<char*>(&t) + 8, &hi, 8);
+  } else {
+    const int col = at + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      t[j] = *reinterpret_cast<const uint32_t*>(lds + tile_at<T, C>(8 * s + 4 * (lane >> 5) + j, col >> 2) + (col & 3) * 4);
+  }
+  return t;
+}
+
+// Eight waves, two a SIMD with 256 registers each; fp32 rows fill LDS with four.
+template <class T>
+constexpr int bwd_threads() {
+  return sizeof(T) == 4 ? 256 : 512;
+}
+
+template <class T, int IT, int OT, bool kEven>
+__global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int SI = steps<T>(IT), SO = steps<T>(OT), kWaves = bwd_threads<T>() / 64, E = 16 / sizeof(T);
+  constexpr int kRows = 32 * IT;
+  constexpr int CI = 2 * SI < 8 ? 8 : 2 * SI, CO = 2 * SO < 8 ? 8 : 2 * SO;   // chunks of a row in LDS
+  constexpr int kWeights = slices<T>(OT) * kRows * 128, kTile = 32 * 16 * (CI + CO);
+  constexpr int kSums = IT * OT * 32 * 32 + OT * 32;   // numbers of a partial sum (padded)
+  constexpr int kTiles = kTile * kWaves, kHalf = kSums * 4 * (kWaves / 2);
+  __shared__ __attribute__((aligned(16))) char w[kWeights];
+  __shared__ __attribute__((aligned(16))) char space[kTiles > kHalf ? kTiles : kHalf];
+  const int lane = threadIdx.x & 63, h = lane >> 5, wave = threadIdx.x >> 6;
+  char* const xt = space + wave * kTile;
+  char* const zt = xt + 32 * 16 * CI;
+  const int64_t tiles = (static_cast<int64_t>(a.rows) + 31) / 32, step = static_cast<int64_t>(gridDim.x) * kWaves;
+  int64_t tile = static_cast<int64_t>(blockIdx.x) * kWaves + wave;
+  const bool sums = a.part != nullptr, w_sums = a.w_sums;
+  struct Rows {
+    RowChunks<T, SI, kEven> x;
+    RowChunks<T, SO, kEven> y_bar, z;
+  } next;
+  const auto read = [&](int64_t t) __attribute__((always_inline)) {
+    const int64_t r = min(t * 32 + (lane & 31), static_cast<int64_t>(a.rows) - 1);
+    next.y_bar.read(a.y_bar, r * a.ybs, a.n_out, h);
+    if (a.z != nullptr) next.z.read(a.z, r * a.zs, a.n_out, h);
+    if (w_sums) next.x.read(a.x, r * a.xs, a.n_in, h);
+  };
+  if (tile < tiles) read(tile);
+  if (a.x_bar != nullptr)
+    fill_weights(w, kRows, 2 * SO, static_cast<const T*>(a.w), a.ldw, a.by_out, a.n_in, a.n_out);
+  __syncthreads();
+  Acc wb[IT][OT] = {};
+  float bb[SO][E] = {};   // sums over this lane's rows of its chunks
+  for (; tile < tiles; tile += step) {
+    const Rows now = next;
+    if (tile + step < tiles) read(tile + step);
+    asm volatile("" ::: "memory");   // the weights stay in LDS
+    const bool row = tile * 32 + (lane & 31) < a.rows;
+    Chunk zb[SO];
+#pragma unroll
+    for (int s = 0; s < SO; ++s) {
+      T e[E], ez[E];
+      float v[E], z[E];
+      __builtin_memcpy(e, &now.y_bar.c[s], 16);
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = row ? static_cast<float>(e[k]) : 0.f;   // rows past the end count as zero
+      if (a.z != nullptr) {
+        __builtin_memcpy(ez, &now.z.c[s], 16);
+#pragma unroll
+        for (int k = 0; k < E; ++k) z[k] = row ? static_cast<float>(ez[k]) : 0.f;
+        times_slope<sizeof(T) == 4>(v, z, a.act);
+      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        bb[s][k] += v[k];
+        e[k] = static_cast<T>(v[k]);
+      }
+      __builtin_memcpy(&zb[s], e, 16);
+    }
+    if (w_sums) {
+      // a row past the end repeats the last one's x, against zeros of z_bar: cleared, as it may hold infinities
+#pragma unroll
+      for (int s = 0; s < SI; ++s) *reinterpret_cast<Chunk*>(xt + tile_at<T, CI>(lane & 31, 2 * s + h)) = row ? now.x.c[s] : Chunk{};
+#pragma unroll
+      for (int s = 0; s < SO; ++s) *reinterpret_cast<Chunk*>(zt + tile_at<T, CO>(lane & 31, 2 * s + h)) = zb[s];
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int s = 0; s < static_cast<int>(sizeof(T)); ++s) {
+        Chunk fx[IT], fz[OT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) fx[i] = column_fragment<T, CI>(xt, 32 * i, s, lane);
+#pragma unroll
+        for (int o = 0; o < OT; ++o) fz[o] = column_fragment<T, CO>(zt, 32 * o, s, lane);
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+          for (int o = 0; o < OT; ++o) wb[i][o] = mm::multiply<T>(fz[o], fx[i], wb[i][o]);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (a.x_bar != nullptr) {
+      const int64_t m = tile * 32 + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        Acc acc = {};
+#pragma unroll
+        for (int s = 0; s < SO; ++s) {
+          const Chunk f = *reinterpret_cast<const Chunk*>(w + weight_at(kRows, 32 * i + (lane & 31), 2 * s + h));
+          acc = mm::multiply<T>(f, zb[s], acc);
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int n = 32 * i + 16 * g + 8 * h;
+          float v[8];
+          eight(acc, g, v);
+          if (row && n < a.n_in) store<8, false>(static_cast<T*>(a.x_bar) + m * a.xbs, n, a.n_in, v);
+        }
+      }
+    }
+  }
+  if (!sums) return;
+
+  // ---- the workgroup's sums: the upper half of the waves hands its own to the lower half, and again
+  const auto each = [&](float* at, bool add) __attribute__((always_inline)) {   // registers to LDS, or LDS added to them
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int o = 0; o < OT; ++o)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float* p = at + ((i * OT + o) * 4 + q) * 256 + 4 * lane;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (add) wb[i][o][4 * q + k] += p[k];
+            else p[k] = wb[i][o][4 * q + k];
+          }
+        }
+    float* p = at + IT * OT * 1024;
+    if ((lane & 31) == 0)
+#pragma unroll
+      for (int s = 0; s < SO; ++s)
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          if (add) bb[s][k] += p[(2 * s + h) * E + k];
+          else p[(2 * s + h) * E + k] = bb[s][k];
+        }
+  };
+#pragma unroll
+  for (int s = 0; s < SO; ++s)
+#pragma unroll
+    for (int k = 0; k < E; ++k) bb[s][k] = lane_sum<32>(bb[s][k]);
+#pragma unroll
+  for (int by = kWaves / 2; by > 0; by /= 2) {
+    __syncthreads();
+    float* const at = reinterpret_cast<float*>(space);
+    if (wave >= by && wave < 2 * by) each(at + (wave - by) * kSums, false);
+    __syncthreads();
+    if (wave < by) each(at + wave * kSums, true);
+  }
+  if (wave != 0) return;
+  // part[workgroup]: [n_in][n_out] (or [n_out][n_in] with !wb_by_out), then [n_out]
+  float* const out = a.part + static_cast<int64_t>(blockIdx.x) * (a.n_in * a.n_out + a.n_out);
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int o = 0; o < OT; ++o) {
+      const int in = 32 * i + (lane & 31);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int on = 32 * o + 8 * (r / 4) + 4 * h + r % 4;
+        if (in < a.n_in && on < a.n_out) out[a.wb_by_out ? in * a.n_out + on : on * a.n_in + in] = wb[i][o][r];
+      }
+    }
+  if ((lane & 31) == 0)
+#pragma unroll
+    for (int s = 0; s < SO; ++s)
+#pragma unroll
+      for (int k = 0; k < E; ++k)
+        if ((2 * s + h) * E + k < a.n_out) out[a.n_in * a.n_out + (2 * s + h) * E + k] = bb[s][k];
+#endif
+}
+
+// ---------------------------------------------------------------- launches
+inline int tiles_of(int n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; }
+
+template <class T, int IT, int OT>
+hipError_t launch_fwd(const FwdArgs& a, bool even, int groups, hipStream_t s) {
+  if (even) fwd_kernel<T, IT, OT, true><<<dim3(groups), dim3(kFwdThreads), 0, s>>>(a);
+  else fwd_kernel<T, IT, OT, false><<<dim3(groups), dim3(kFwdThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+template <class T, int IT, int OT>
+hipError_t launch_bwd(const BwdArgs& a, bool even, int groups, hipStream_t s) {
+  if (even) bwd_kernel<T, IT, OT, true><<<dim3(groups), dim3(bwd_threads<T>()), 0, s>>>(a);
+  else bwd_kernel<T, IT, OT, false><<<dim3(groups), dim3(bwd_threads<T>()), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t forward(const FwdArgs& a, bool even, int groups, hipStream_t s) {
+  switch (tiles_of(a.n_in) * 8 + tiles_of(a.n_out)) {
+    case 9: return launch_fwd<T, 1, 1>(a, even, groups, s);
+    case 10: return launch_fwd<T, 1, 2>(a, even, groups, s);
+    case 12: return launch_fwd<T, 1, 4>(a, even, groups, s);
+    case 17: return launch_fwd<T, 2, 1>(a, even, groups, s);
+    case 18: return launch_fwd<T, 2, 2>(a, even, groups, s);
+    case 20: return launch_fwd<T, 2, 4>(a, even, groups, s);
+    case 33: return launch_fwd<T, 4, 1>(a, even, groups, s);
+    case 34: return launch_fwd<T, 4, 2>(a, even, groups, s);
+    default: return launch_fwd<T, 4, 4>(a, even, groups, s);
+  }
+}
+template <class T>
+hipError_t backward(const BwdArgs& a, bool even, int groups, hipStream_t s) {
+  switch (tiles_of(a.n_in) * 8 + tiles_of(a.n_out)) {
+    case 9: return launch_bwd<T, 1, 1>(a, even, groups, s);
+    case 10: return launch_bwd<T, 1, 2>(a, even, groups, s);
+    case 17: return launch_bwd<T, 2, 1>(a, even, groups, s);
+    case 18: return launch_bwd<T, 2, 2>(a, even, groups, s);
+    default: return launch_bwd<T, 4, 1>(a, even, groups, s);
+  }
+}
+
+}  // namespace narrow
+}  // namespace etpc
