@@ -161,8 +161,7 @@ int bwd_groups(int64_t rows) { return static_cast<int>(std::min<int64_t>((rows +
 
 hipError_t run_fwd(const FwdArgs& a, int dtype, hipStream_t s) {
   const bool even = whole(a.x, a.xs, a.n_in, dtype == ETPC_F32 ? 4 : 2);
-  const int groups = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(a.rows) + 127) / 128, 256 * 4));
-  return dtype == ETPC_F32 ? fwd_f32(a, even, groups, s) : dtype == ETPC_BF16 ? fwd_bf16(a, even, groups, s) : fwd_f16(a, even, groups, s);
+  return dtype == ETPC_F32 ? fwd_f32(a, even, s) : dtype == ETPC_BF16 ? fwd_bf16(a, even, s) : fwd_f16(a, even, s);
 }
 
 hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s) {

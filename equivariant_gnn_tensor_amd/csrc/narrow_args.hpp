@@ -41,9 +41,9 @@ int bwd_groups(int64_t rows);
 hipError_t run_fwd(const FwdArgs& a, int dtype, hipStream_t s);
 hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s);
 
-hipError_t fwd_f32(const FwdArgs& a, bool even, int groups, hipStream_t s);
-hipError_t fwd_bf16(const FwdArgs& a, bool even, int groups, hipStream_t s);
-hipError_t fwd_f16(const FwdArgs& a, bool even, int groups, hipStream_t s);
+hipError_t fwd_f32(const FwdArgs& a, bool even, hipStream_t s);
+hipError_t fwd_bf16(const FwdArgs& a, bool even, hipStream_t s);
+hipError_t fwd_f16(const FwdArgs& a, bool even, hipStream_t s);
 hipError_t bwd_f32(const BwdArgs& a, bool even, int groups, hipStream_t s);
 hipError_t bwd_bf16(const BwdArgs& a, bool even, int groups, hipStream_t s);
 hipError_t bwd_f16(const BwdArgs& a, bool even, int groups, hipStream_t s);
