@@ -119,25 +119,39 @@ struct Side {
     __device__ inline void commit(char*) {}
   };
 
+  // Slices that lie inside the operand as a whole are plain 16-byte loads of any alignment; others go
+  // chunk by chunk, ends masked.
   struct Staged {
     Chunk t[kPer];
+    int64_t off[kPer];
     const T* p;
     int64_t ld, first;
     int n, K, k0;
     __device__ inline void start(const T* base, int64_t ld_, int64_t first_, int n_, int K_, int k0_) {
       p = base, ld = ld_, first = first_, n = n_, K = K_, k0 = k0_;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r) * E;
+        off[i] = kCols ? r * ld + first + c : (first + r) * ld + c;
+      }
     }
     __device__ inline void end(int) {}
     __device__ inline void issue(char*, int, int last) {
       if (last != kPer - 1) return;   // all at once
+      const T* const at = p + (kCols ? k0 * ld : k0);
+      if (k0 + BK <= K && first + SIDE <= n) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r) * E;
-        t[i] = Chunk{};
-        if (kCols) {
-          if (k0 + r < K) t[i] = fetch_chunk(p + (k0 + r) * ld, static_cast<int>(first) + c, n);
-        } else {
-          if (first + r < n) t[i] = fetch_chunk(p + (first + r) * ld, k0 + c, K);
+        for (int i = 0; i < kPer; ++i) __builtin_memcpy(&t[i], at + off[i], 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int q = threadIdx.x + i * kThreads, r = q / kRow, c = unswizzle(q % kRow, r) * E;
+          t[i] = Chunk{};
+          if (kCols) {
+            if (k0 + r < K) t[i] = fetch_chunk(p + (k0 + r) * ld, static_cast<int>(first) + c, n);
+          } else {
+            if (first + r < n) t[i] = fetch_chunk(p + (first + r) * ld, k0 + c, K);
+          }
         }
       }
       k0 += BK;

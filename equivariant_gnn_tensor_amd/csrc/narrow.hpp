@@ -388,17 +388,24 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
 // ---------------------------------------------------------------- launches
 inline int tiles_of(int n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; }
 
-// As many workgroups as are resident (by LDS, four at most), fewer where that gives every wave the same
-// number of tiles (214980 x 64 -> 64 bf16: 24.1 us with four a CU where three are resident, 21.1 with three).
+// As many workgroups as are resident, fewer where that gives every wave the same number of tiles
+// (214980 x 64 -> 64 bf16: 24.1 us with four a CU where three are resident, 21.1 with three).
+template <class T, int IT, int OT, bool kEven>
+hipError_t launch_fwd(const FwdArgs& a, hipStream_t s) {
+  static const int resident = [] {
+    int n = 0;
+    const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fwd_kernel<T, IT, OT, kEven>, kFwdThreads, 0);
+    return e == hipSuccess && n > 0 ? 256 * n : 256;
+  }();
+  const int64_t units = (static_cast<int64_t>(a.rows) + 32 * kFwdThreads / 64 - 1) / (32 * kFwdThreads / 64);
+  const int64_t rounds = (units + resident - 1) / resident;
+  const unsigned groups = static_cast<unsigned>((units + rounds - 1) / rounds);
+  fwd_kernel<T, IT, OT, kEven><<<dim3(groups), dim3(kFwdThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
 template <class T, int IT, int OT>
 hipError_t launch_fwd(const FwdArgs& a, bool even, hipStream_t s) {
-  constexpr int kWaves = kFwdThreads / 64, kLds = slices<T>(IT) * 32 * OT * 128 + RowsOut<OT>::kBytes * kWaves;
-  constexpr int64_t kResident = 256 * std::min(4, 160 * 1024 / kLds);
-  const int64_t units = (static_cast<int64_t>(a.rows) + 32 * kWaves - 1) / (32 * kWaves), rounds = (units + kResident - 1) / kResident;
-  const unsigned groups = static_cast<unsigned>((units + rounds - 1) / rounds);
-  if (even) fwd_kernel<T, IT, OT, true><<<dim3(groups), dim3(kFwdThreads), 0, s>>>(a);
-  else fwd_kernel<T, IT, OT, false><<<dim3(groups), dim3(kFwdThreads), 0, s>>>(a);
-  return hipGetLastError();
+  return even ? launch_fwd<T, IT, OT, true>(a, s) : launch_fwd<T, IT, OT, false>(a, s);
 }
 template <class T, int IT, int OT>
 hipError_t launch_bwd(const BwdArgs& a, bool even, int groups, hipStream_t s) {
