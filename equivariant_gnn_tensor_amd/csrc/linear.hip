@@ -118,12 +118,14 @@ hipError_t sum_parts(const float* part, int parts, int64_t rows, int64_t cols, v
   return hipGetLastError();
 }
 
-// Whether an operand can go straight into LDS: whole aligned chunks, offsets inside a tile in 31 bits.
-// n: its other index; cols: contiguous along that one.
-bool direct(const void* p, int64_t ld, int64_t n, int64_t k, bool cols, int64_t size) {
-  const int64_t e = 16 / size, row = cols ? n : k;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % e == 0 && row % e == 0 && ld >= row &&
-         256 * ld * size < 0x70000000;
+// Bytes a lane with which an operand can go straight into LDS (0: it cannot): whole aligned pieces,
+// offsets inside a tile in 31 bits.  n: its other index; cols: contiguous along that one.
+int grain_of(const void* p, int64_t ld, int64_t n, int64_t k, bool cols, int64_t size) {
+  const int64_t row = cols ? n : k;
+  if (ld < row || 256 * ld * size >= 0x70000000) return 0;
+  for (const int g : {16, 4})
+    if (reinterpret_cast<uintptr_t>(p) % g == 0 && ld * size % g == 0 && row * size % g == 0) return g;
+  return 0;
 }
 
 }  // namespace
@@ -175,9 +177,9 @@ hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s) {
 
 MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split) {
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;
-  MatmulShape s{64, false, 1, a.K};
-  s.direct = direct(a.a, a.lda, a.M, a.K, form == MatmulForm::kColsCols, size) &&
-             direct(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size);
+  MatmulShape s{64, 0, 1, a.K};
+  s.grain = std::min(grain_of(a.a, a.lda, a.M, a.K, form == MatmulForm::kColsCols, size),
+                     grain_of(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size));
   const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
   const int64_t bk = 128 / size;
   if (split) {
@@ -190,6 +192,7 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
   } else {
     s.tile = size == 2 && tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
   }
+  if (s.tile == 256 && s.grain != 16) s.tile = 128;
   return s;
 }
 

@@ -25,7 +25,7 @@ enum class MatmulForm { kRowsCols, kRowsRows, kColsCols };   // A by rows (k), B
 
 struct MatmulShape {
   int tile;        // side of a workgroup's tile
-  bool direct;     // slices go straight into LDS
+  int grain;       // bytes a lane of the loads straight into LDS (16, 4), or 0: through registers
   int splits, k_split;
 };
 // The shape for a product; `split` allows ranges of k.  Operands' addresses do not matter to the splits.

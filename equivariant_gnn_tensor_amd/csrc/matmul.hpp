@@ -17,9 +17,10 @@
 //   with the transposing LDS load, 32 bytes of each of four k and two neighbouring blocks at a
 //   time, which an exclusive or of the block with k spreads over all banks.  fp32 fragments are
 //   one number a lane.
-// Slices come in by loads that write LDS directly where both operands are aligned to 16 bytes
-// and hold whole chunks (kDirect): no registers, and what lies past the end is cleared by the
-// loads' range check.  Anything else goes through registers, chunk by chunk, ends masked.
+// Slices come in by loads that write LDS directly, kGrain bytes a lane: 16 where both operands are
+// aligned to it and hold whole chunks, 4 where they allow that (fp32 always, 16-bit rows of even
+// length and stride).  They need no registers, and what lies past the end is cleared by their range
+// check.  Anything else (kGrain 0) goes through registers, chunk by chunk, ends masked.
 //
 // v_mfma_f32_32x32x16 (16 bits) and v_mfma_f32_32x32x2 (fp32) take B's fragment first, so a
 // lane ends up with four adjacent columns of one row at a time; the epilogue turns them over
@@ -38,15 +39,19 @@
 namespace etpc {
 namespace mm {
 
-// 16 bytes a lane from base + off (zeros past the range) to LDS from `lds` on, lane after lane.  In
+// kGrain bytes a lane from base + off (zeros past the range) to LDS from `lds` on, lane after lane.  In
 // assembly, so that the compiler's own counting of loads does not wait for more of them (and of the
 // epilogue's stores among them) than barrier_after_loads; nothing but LDS and m0 is written (the
 // compiler keeps nothing in m0: it sets it before each use); the wait states cover m0 and scalars that
 // a vector instruction has just written.  What it counts itself is only waited
 // for earlier by that.
 typedef int Range __attribute__((ext_vector_type(4)));
+template <int kGrain>
 __device__ inline void load_lds(uint32_t lds, const Range& range, int off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(range));
+  if (kGrain == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(range));
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(range));
 }
 __device__ inline uint32_t lds_address(const char* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
@@ -71,16 +76,19 @@ struct Side {
   static __device__ inline int spread(int k) { return SIDE >= 128 ? (k & 3) << 2 : (k & 2) << 1; }
 
   // Reads slices from k0 on (first: the tile's first row or column) into LDS.
+  template <int kGrain>
   struct Direct {
-    int off[kPer];
+    static constexpr int kLoads = kPer * 16 / kGrain;
+    int off[kLoads];
     const char* p;
     uint64_t left;        // bytes from p to the operand's end
     int64_t step;         // bytes of a slice
     static constexpr int kFar = 0x7ffffff0, kMost = 0x7fffff00;   // an offset out of any range
+    // Row r in LDS and first element in it of load i.
     static __device__ inline int place(int i, int& r) {
-      const int q = threadIdx.x + i * kThreads;
+      const int g = threadIdx.x + i * kThreads, q = g / (16 / kGrain);
       r = q / kRow;
-      return unswizzle(q % kRow, r);
+      return unswizzle(q % kRow, r) * E + g % (16 / kGrain) * (kGrain / static_cast<int>(sizeof(T)));
     }
     __device__ inline void start(const T* base, int64_t ld, int64_t first, int n, int K, int k0) {
       const int64_t at = kCols ? k0 * ld + first : first * ld + k0;
@@ -89,20 +97,20 @@ struct Side {
       left = static_cast<uint64_t>((all - at) * static_cast<int64_t>(sizeof(T)));
       step = (kCols ? BK * ld : BK) * static_cast<int64_t>(sizeof(T));
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
+      for (int i = 0; i < kLoads; ++i) {
         int r;
         const int c = place(i, r);
-        off[i] = static_cast<int>(r * ld) * static_cast<int>(sizeof(T)) + 16 * c;
+        off[i] = (static_cast<int>(r * ld) + c) * static_cast<int>(sizeof(T));
       }
     }
     // With `have` k values from here to the end, fewer than a slice: chunks past it are read as zero,
     // in this and every later slice.
     __device__ inline void end(int have) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
+      for (int i = 0; i < kLoads; ++i) {
         int r;
         const int c = place(i, r);
-        if ((kCols ? r : c * E) >= have) off[i] = kFar;
+        if ((kCols ? r : c) >= have) off[i] = kFar;
       }
     }
     // Load i of the slice; the last one moves on to the next slice.
@@ -110,8 +118,8 @@ struct Side {
       const uint64_t at = reinterpret_cast<uint64_t>(p);
       const Range range = {static_cast<int>(at), static_cast<int>(at >> 32 & 0xffff),
                            left >= kMost ? kMost : static_cast<int>(left), 0x00020000};
-      load_lds(lds_address(lds) + wave * 1024 + i * kThreads * 16, range, off[i]);
-      if (i == kPer - 1) {
+      load_lds<kGrain>(lds_address(lds) + wave * 64 * kGrain + i * kThreads * kGrain, range, off[i]);
+      if (i == kLoads - 1) {
         p += step;
         left -= static_cast<uint64_t>(step);
       }
@@ -122,6 +130,7 @@ struct Side {
   // Slices that lie inside the operand as a whole are plain 16-byte loads of any alignment; others go
   // chunk by chunk, ends masked.
   struct Staged {
+    static constexpr int kLoads = 1;   // all at once
     Chunk t[kPer];
     int64_t off[kPer];
     const T* p;
@@ -136,8 +145,7 @@ struct Side {
       }
     }
     __device__ inline void end(int) {}
-    __device__ inline void issue(char*, int, int last) {
-      if (last != kPer - 1) return;   // all at once
+    __device__ inline void issue(char*, int, int) {
       const T* const at = p + (kCols ? k0 * ld : k0);
       if (k0 + BK <= K && first + SIDE <= n) {
 #pragma unroll
@@ -218,9 +226,10 @@ __device__ inline void place_tile(int id, int tiles_m, int tiles_n, int& tm, int
   tm = 8 * band + in - tn * high;
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool kACols, bool kBCols, bool kDirect>
+template <class T, int BM, int BN, int WM, int WN, bool kACols, bool kBCols, int kGrain>
 __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs no body, and drops launch stubs over builtins it does not know
+  constexpr bool kDirect = kGrain > 0;
   constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, BK = slice<T>();
   constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
   using A = Side<T, BM, kACols, kThreads>;
@@ -236,14 +245,16 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
   const int wm = wave % WM, wn = wave / WM;
   const int per = a.tiles_m * a.tiles_n, total = per * a.splits;
   const int h = lane >> 5;
-  typename std::conditional<kDirect, typename A::Direct, typename A::Staged>::type la;
-  typename std::conditional<kDirect, typename B::Direct, typename B::Staged>::type lb;
+  using LoadA = typename std::conditional<kDirect, typename A::template Direct<kDirect ? kGrain : 16>, typename A::Staged>::type;
+  using LoadB = typename std::conditional<kDirect, typename B::template Direct<kDirect ? kGrain : 16>, typename B::Staged>::type;
+  LoadA la;
+  LoadB lb;
   int64_t m0, n0;
   int k0, k1;
-  constexpr int kLoads = A::kPer + B::kPer;
+  constexpr int kLoads = LoadA::kLoads + LoadB::kLoads;
   const auto issue_one = [&](char* lds, int i) __attribute__((always_inline)) {
-    if (i < A::kPer) la.issue(lds, wave, i);
-    else lb.issue(lds + A::kBytes, wave, i - A::kPer);
+    if (i < LoadA::kLoads) la.issue(lds, wave, i);
+    else lb.issue(lds + A::kBytes, wave, i - LoadA::kLoads);
   };
   const auto issue = [&](char* lds) __attribute__((always_inline)) {
 #pragma unroll
@@ -394,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
 
 constexpr int kCus = 256;
 
-template <class T, int BM, int BN, int WM, int WN, bool kDirect>
+template <class T, int BM, int BN, int WM, int WN, int kGrain>
 hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_n = (a.N + BN - 1) / BN;
@@ -404,24 +415,23 @@ hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
   constexpr int resident = 160 * 1024 / (2 * 128 * (BM + BN));
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(total, kCus * resident))), block(64 * WM * WN);
   if (form == MatmulForm::kRowsCols)
-    matmul_kernel<T, BM, BN, WM, WN, false, true, kDirect><<<grid, block, 0, s>>>(a);
+    matmul_kernel<T, BM, BN, WM, WN, false, true, kGrain><<<grid, block, 0, s>>>(a);
   else if (form == MatmulForm::kRowsRows)
-    matmul_kernel<T, BM, BN, WM, WN, false, false, kDirect><<<grid, block, 0, s>>>(a);
+    matmul_kernel<T, BM, BN, WM, WN, false, false, kGrain><<<grid, block, 0, s>>>(a);
   else
-    matmul_kernel<T, BM, BN, WM, WN, true, true, kDirect><<<grid, block, 0, s>>>(a);
+    matmul_kernel<T, BM, BN, WM, WN, true, true, kGrain><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s) {
-  if (shape.direct) {
-    if constexpr (sizeof(T) == 2)
-      if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, true>(a, form, s);
-    if (shape.tile >= 128) return launch_tiles<T, 128, 128, 2, 2, true>(a, form, s);
-    return launch_tiles<T, 64, 64, 2, 2, true>(a, form, s);
-  }
-  if (shape.tile >= 128) return launch_tiles<T, 128, 128, 2, 2, false>(a, form, s);
-  return launch_tiles<T, 64, 64, 2, 2, false>(a, form, s);
+  if constexpr (sizeof(T) == 2)
+    if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, 16>(a, form, s);
+  if (shape.grain == 16)
+    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 16>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 16>(a, form, s);
+  if (shape.grain == 4)
+    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 4>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 4>(a, form, s);
+  return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 0>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 0>(a, form, s);
 }
 
 }  // namespace mm
