@@ -1,0 +1,36 @@
+// Launches of the dense layer for up to eight rows.
+#include "few_rows.hpp"
+
+namespace etpc {
+namespace {
+
+template <class T, int M>
+hipError_t launch(const MatmulArgs& a, bool along, hipStream_t s) {
+  if (along) {
+    // one output a wave until there are enough waves for every CU
+    if (a.N <= 4096)
+      few::along_kernel<T, M, 1><<<dim3((a.N + 3u) / 4u), dim3(few::kAlongThreads), 0, s>>>(a);
+    else
+      few::along_kernel<T, M, 4><<<dim3((a.N + 15u) / 16u), dim3(few::kAlongThreads), 0, s>>>(a);
+  } else {
+    constexpr unsigned cols = 8 * 16 / sizeof(T);
+    few::across_kernel<T, M><<<dim3((a.N + cols - 1) / cols), dim3(few::kAcrossThreads), 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch(const MatmulArgs& a, bool along, hipStream_t s) {
+  return a.M == 1 ? launch<T, 1>(a, along, s) : a.M == 2 ? launch<T, 2>(a, along, s)
+         : a.M <= 4 ? launch<T, 4>(a, along, s) : launch<T, 8>(a, along, s);
+}
+
+}  // namespace
+
+hipError_t launch_few_rows(const MatmulArgs& a, bool along, int dtype, hipStream_t s) {
+  return dtype == ETPC_F32    ? launch<float>(a, along, s)
+         : dtype == ETPC_BF16 ? launch<Bf16>(a, along, s)
+                              : launch<F16>(a, along, s);
+}
+
+}  // namespace etpc

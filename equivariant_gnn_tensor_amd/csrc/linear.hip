@@ -177,7 +177,7 @@ hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s) {
 
 MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split) {
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;
-  MatmulShape s{64, 0, 1, a.K};
+  MatmulShape s{64, 0, 1, a.K, false};
   s.grain = std::min(grain_of(a.a, a.lda, a.M, a.K, form == MatmulForm::kColsCols, size),
                      grain_of(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size));
   const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
@@ -193,10 +193,13 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
     s.tile = size == 2 && tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
   }
   if (s.tile == 256 && s.grain != 16) s.tile = 128;
+  s.deep = tiles(64) * s.splits <= 512;
   return s;
 }
 
 hipError_t launch_matmul(const MatmulArgs& args, MatmulForm form, int dtype, const MatmulShape& shape, hipStream_t s) {
+  if (args.M <= kFewRows && form != MatmulForm::kColsCols && args.part == nullptr)
+    return launch_few_rows(args, form == MatmulForm::kRowsRows, dtype, s);
   MatmulArgs a = args;
   a.splits = shape.splits;
   a.k_split = shape.k_split;

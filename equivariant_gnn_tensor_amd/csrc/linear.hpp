@@ -27,10 +27,14 @@ struct MatmulShape {
   int tile;        // side of a workgroup's tile
   int grain;       // bytes a lane of the loads straight into LDS (16, 4), or 0: through registers
   int splits, k_split;
+  bool deep;       // five slices on their way instead of two
 };
 // The shape for a product; `split` allows ranges of k.  Operands' addresses do not matter to the splits.
 MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split);
 hipError_t launch_matmul(const MatmulArgs& a, MatmulForm form, int dtype, const MatmulShape& shape, hipStream_t s);
+// Up to two rows: C(m, n) with B contiguous along k (`along`) or along n.  launch_matmul takes it.
+constexpr int kFewRows = 2;
+hipError_t launch_few_rows(const MatmulArgs& a, bool along, int dtype, hipStream_t s);
 namespace mm {
 hipError_t launch_f32(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s);
 hipError_t launch_bf16(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s);

@@ -226,7 +226,7 @@ __device__ inline void place_tile(int id, int tiles_m, int tiles_n, int& tm, int
   tm = 8 * band + in - tn * high;
 }
 
-template <class T, int BM, int BN, int WM, int WN, bool kACols, bool kBCols, int kGrain>
+template <class T, int BM, int BN, int WM, int WN, int kStages, bool kACols, bool kBCols, int kGrain>
 __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host's pass needs no body, and drops launch stubs over builtins it does not know
   constexpr bool kDirect = kGrain > 0;
@@ -238,8 +238,10 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
   static_assert(32 * TN * 4 * kWaves <= kStage, "the epilogue turns its rows over in the second slice's space");
   constexpr int kVecs = TN / 8, kRows = 64 / kVecs;   // of the epilogue: vectors a row, rows a pass
   constexpr int kPasses = 32 / kRows, kStores = MI * kPasses;
-  __shared__ __attribute__((aligned(16))) char one[kStage];
-  __shared__ __attribute__((aligned(16))) char two[kStage];
+  static_assert(kDirect || kStages == 2, "registers hold one slice");
+  __shared__ __attribute__((aligned(16))) char ring[kStages * kStage];
+  char* const one = ring;
+  char* const two = ring + kStage;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -310,16 +312,16 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
       }
     };
     // Slice t, whose first fragments are read already, from `cur`.  After its last ones are, one
-    // barrier frees `cur` for slice t + 2 and opens slice t + 1, whose loads are a slice old by then.
-    // What is read past the last slice is not used.
+    // barrier frees `cur` for slice t + kStages and opens slice t + 1, whose loads are kStages - 1
+    // slices old by then.  What is read past the last slice is not used.
     const auto walk = [&](char* cur, char* nxt, int t) __attribute__((always_inline)) {
-      prepare(t + 2);
+      prepare(t + kStages);
       if (!kDirect) issue(nxt);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 3; ++s) step(s, cur, s + 1, std::false_type{}, cur);
       if (!kDirect) commit(nxt);
-      barrier_after_loads<0>();
+      barrier_after_loads<kDirect ? (kStages - 2) * kLoads : 0>();
       step(3, nxt, 0, std::integral_constant<bool, kDirect>{}, cur);
     };
     float bias[8] = {};
@@ -328,21 +330,24 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
       if (a.bias != nullptr && n < a.N) load<8, false>(a.bias, n, a.N, bias);
     }
     commit(one);
-    prepare(1);
-    if (kDirect) issue(two);
-    // The first slice has come; the second, and what the epilogue before stored, may be under way.
-    constexpr int kPending = kDirect ? kLoads : 0;
+    if (kDirect)
+#pragma unroll
+      for (int j = 1; j < kStages; ++j) {
+        prepare(j);
+        issue(ring + j * kStage);
+      }
+    // The first slice has come; the others, and what the epilogue before stored, may be under way.
+    constexpr int kPending = kDirect ? (kStages - 1) * kLoads : 0;
     if (!whole) barrier_after_loads<kPending>();
     else if (a.z == nullptr) barrier_after_loads<kPending + kStores>();
     else barrier_after_loads<kPending + 2 * kStores>();
 #pragma unroll
     for (int r = 0; r < MI + NI; ++r) read_one(one, 0, r);
-    int t = 0;
-    for (; t + 2 <= slices; t += 2) {
-      walk(one, two, t);
-      walk(two, one, t + 1);
+    for (int t = 0, cur = 0; t < slices; ++t) {
+      const int nxt = cur + kStage == kStages * kStage ? 0 : cur + kStage;
+      walk(ring + cur, ring + nxt, t);
+      cur = nxt;
     }
-    if (t < slices) walk(one, two, t);
     barrier_after_loads<0>();
 
     // ---- epilogue, while the next tile's first slice is under way
@@ -405,33 +410,35 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
 
 constexpr int kCus = 256;
 
-template <class T, int BM, int BN, int WM, int WN, int kGrain>
+template <class T, int BM, int BN, int WM, int WN, int kStages, int kGrain>
 hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_n = (a.N + BN - 1) / BN;
   const int64_t total = static_cast<int64_t>(a.tiles_m) * a.tiles_n * a.splits;
   if (total >= int64_t{1} << 31) return hipErrorInvalidValue;
   // as many workgroups as LDS holds at once, each walking its tiles
-  constexpr int resident = 160 * 1024 / (2 * 128 * (BM + BN));
+  constexpr int resident = 160 * 1024 / (kStages * 128 * (BM + BN));
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(total, kCus * resident))), block(64 * WM * WN);
   if (form == MatmulForm::kRowsCols)
-    matmul_kernel<T, BM, BN, WM, WN, false, true, kGrain><<<grid, block, 0, s>>>(a);
+    matmul_kernel<T, BM, BN, WM, WN, kStages, false, true, kGrain><<<grid, block, 0, s>>>(a);
   else if (form == MatmulForm::kRowsRows)
-    matmul_kernel<T, BM, BN, WM, WN, false, false, kGrain><<<grid, block, 0, s>>>(a);
+    matmul_kernel<T, BM, BN, WM, WN, kStages, false, false, kGrain><<<grid, block, 0, s>>>(a);
   else
-    matmul_kernel<T, BM, BN, WM, WN, true, true, kGrain><<<grid, block, 0, s>>>(a);
+    matmul_kernel<T, BM, BN, WM, WN, kStages, true, true, kGrain><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, 16>(a, form, s);
+    if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, 2, 16>(a, form, s);
   if (shape.grain == 16)
-    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 16>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 16>(a, form, s);
+    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 16>(a, form, s)
+           : shape.deep      ? launch_tiles<T, 64, 64, 2, 2, 5, 16>(a, form, s)
+                             : launch_tiles<T, 64, 64, 2, 2, 2, 16>(a, form, s);
   if (shape.grain == 4)
-    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 4>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 4>(a, form, s);
-  return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 0>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 0>(a, form, s);
+    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 4>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 4>(a, form, s);
+  return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 0>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 0>(a, form, s);
 }
 
 }  // namespace mm
