@@ -17,7 +17,7 @@ from ._binding import (  # noqa: F401
     etpc_dropout_add_layer_norm, etpc_dropout_add_layer_norm_backward,
     etpc_irreps_dims, etpc_irreps_dropout, etpc_irreps_norm, etpc_irreps_norm_backward,
     etpc_irreps_norm_workspace_size,
-    etpc_linear, etpc_linear_backward, etpc_linear_workspace_size,
+    etpc_linear, etpc_linear_backward, etpc_linear_workspace_size, etpc_linear_backward_workspace_size,
     etpc_norm_gate_add_norm, etpc_norm_gate_add_norm_backward, etpc_norm_gate_add_norm_workspace_size,
     etpc_clip_grad_norm, etpc_grad_norm, etpc_grad_norm_workspace_size,
 )

@@ -82,7 +82,7 @@ SYMBOLS = (
     "etpc_dropout", "etpc_layer_norm", "etpc_layer_norm_workspace_size", "etpc_layer_norm_backward",
     "etpc_dropout_add_layer_norm", "etpc_dropout_add_layer_norm_backward", "etpc_irreps_dims", "etpc_irreps_dropout",
     "etpc_irreps_norm", "etpc_irreps_norm_workspace_size", "etpc_irreps_norm_backward",
-    "etpc_linear", "etpc_linear_workspace_size", "etpc_linear_backward",
+    "etpc_linear", "etpc_linear_workspace_size", "etpc_linear_backward", "etpc_linear_backward_workspace_size",
     "etpc_norm_gate_add_norm", "etpc_norm_gate_add_norm_workspace_size", "etpc_norm_gate_add_norm_backward",
     "etpc_grad_norm_workspace_size", "etpc_grad_norm", "etpc_clip_grad_norm",
 )
@@ -135,8 +135,9 @@ def _load():
         "etpc_irreps_norm": [i32, ir, i32, vp, vp, vp, f32, vp, vp, vp],
         "etpc_irreps_norm_workspace_size": [i32, ir, i32, P(sz)],
         "etpc_irreps_norm_backward": [i32, ir, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
-        "etpc_linear": [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, i64, vp],
-        "etpc_linear_workspace_size": [i64, i64, i64, i32, i32, P(sz)],
+        "etpc_linear": [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, i64, vp, sz, vp],
+        "etpc_linear_workspace_size": [i64, i64, i64, i32, P(sz)],
+        "etpc_linear_backward_workspace_size": [i64, i64, i64, i32, i32, P(sz)],
         "etpc_linear_backward": [i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i64,
                                  vp, vp, sz, vp],
         "etpc_norm_gate_add_norm": [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, f32, vp, i64, vp, i64, vp,
@@ -1014,7 +1015,7 @@ def _new_rows(lead, cols, like, stream) -> torch.Tensor:
         return torch.empty((*lead, cols), dtype=like.dtype, device=like.device)
 
 
-def etpc_linear(x, w, b=None, residual=None, act: str = "none", y=None, z=None, keep_z: bool = True, stream=None):
+def etpc_linear(x, w, b=None, residual=None, act: str = "none", y=None, z=None, keep_z: bool = True, ws=None, stream=None):
     """(y, z): z = x w + b, y = act(z) + residual over the rows x [..., n_in]; w [n_in, n_out] with
     either axis contiguous (a transposed view of [n_out, n_in] weights goes in place), b f32.  act:
     "none", "relu", "silu", "gelu" or "tanh".  z is what the backward pass reads; it is None for
@@ -1039,24 +1040,41 @@ def etpc_linear(x, w, b=None, residual=None, act: str = "none", y=None, z=None, 
     else:
         zp, zs = None, 0
     rp, rs = (None, 0) if residual is None else _rows_of("residual", residual, lead, n_out, x)
+    need = _linear_ws(rows, n_in, n_out, dtype)
+    wsp, wsn, _keep = _scratch(ws, need, dev, stream) if need else (None, 0, None)
     st = lib.etpc_linear(rows, n_in, n_out, dtype, xp, xs, wp, wi, wo, _vector("b", b, n_out, dev), rp, rs, code, yp, ys,
-                         zp, zs, handle)
+                         zp, zs, wsp, wsn, handle)
     if st:
         _check(st)
     return y, z
 
 
 @functools.lru_cache(maxsize=512)
-def _linear_ws(n_rows: int, n_in: int, n_out: int, dtype: int, act: int) -> int:
+def _linear_ws(n_rows: int, n_in: int, n_out: int, dtype: int) -> int:
     b = C.c_size_t()
-    _check(lib.etpc_linear_workspace_size(n_rows, n_in, n_out, dtype, act, b))
+    _check(lib.etpc_linear_workspace_size(n_rows, n_in, n_out, dtype, b))
     return b.value
 
 
-def etpc_linear_workspace_size(n_rows: int, n_in: int, n_out: int, dtype=torch.float32, act: str = "none") -> int:
+@functools.lru_cache(maxsize=512)
+def _linear_backward_ws(n_rows: int, n_in: int, n_out: int, dtype: int, act: int) -> int:
+    b = C.c_size_t()
+    _check(lib.etpc_linear_backward_workspace_size(n_rows, n_in, n_out, dtype, act, b))
+    return b.value
+
+
+def _row_type_code(dtype) -> int:
     if dtype not in _ROW_TYPES:
         raise TypeError(f"rows must be float32, bfloat16 or float16, got {dtype}")
-    return _linear_ws(n_rows, n_in, n_out, _ROW_TYPES[dtype], _act_code(act))
+    return _ROW_TYPES[dtype]
+
+
+def etpc_linear_workspace_size(n_rows: int, n_in: int, n_out: int, dtype=torch.float32) -> int:
+    return _linear_ws(n_rows, n_in, n_out, _row_type_code(dtype))
+
+
+def etpc_linear_backward_workspace_size(n_rows: int, n_in: int, n_out: int, dtype=torch.float32, act: str = "none") -> int:
+    return _linear_backward_ws(n_rows, n_in, n_out, _row_type_code(dtype), _act_code(act))
 
 
 def etpc_linear_backward(x, w, y_bar, z=None, act: str = "none", want=("x", "w", "b"), outs=None, ws=None, stream=None):
@@ -1089,7 +1107,7 @@ def etpc_linear_backward(x, w, y_bar, z=None, act: str = "none", want=("x", "w",
     else:
         w_bar = None
     b_bar, bbp = _bar_vector("b_bar", want, "b", outs, 2, n_out, dev, stream)
-    wsp, wsn, _keep = _scratch(ws, _linear_ws(rows, n_in, n_out, dtype, code), dev, stream)
+    wsp, wsn, _keep = _scratch(ws, _linear_backward_ws(rows, n_in, n_out, dtype, code), dev, stream)
     st = lib.etpc_linear_backward(rows, n_in, n_out, dtype, xp, xs, wp, wi, wo, yp, ys, zp, zs, code, xbp, xbs, wbp, wbi,
                                   wbo, bbp, wsp, wsn, handle)
     if st:

@@ -40,7 +40,7 @@ Operand operand(const Weights& w, int64_t size) { return Operand{w.m, w.rows, w.
 
 // Regions of the backward pass's workspace, each a multiple of 256 bytes.
 struct LinearSpace {
-  size_t z_bar, w_part, b_part, bytes;
+  size_t z_bar, w_part, b_part, x_part, bytes;
   int64_t z_bar_stride;
 };
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -52,6 +52,27 @@ MatmulArgs weight_product(int64_t rows, int64_t n_in, int64_t n_out, bool by_out
   a.N = static_cast<int32_t>(by_out ? n_out : n_in);
   a.K = static_cast<int32_t>(rows);
   return a;
+}
+
+// Partial sums of a layer's product [rows][k] x [k][cols], when it is split: the same whatever the layout.
+size_t product_space(int64_t rows, int64_t k, int64_t cols, int32_t dtype) {
+  MatmulArgs a{};
+  a.M = static_cast<int32_t>(rows), a.N = static_cast<int32_t>(cols), a.K = static_cast<int32_t>(k);
+  const int splits = matmul_shape(a, MatmulForm::kRowsCols, dtype, false).splits;
+  return splits > 1 ? round256(static_cast<size_t>(splits) * static_cast<size_t>(rows * cols) * sizeof(float)) : 0;
+}
+size_t forward_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
+  return n_in <= narrow::kMost && n_out <= narrow::kMost ? 0 : product_space(rows, n_in, n_out, dtype);
+}
+
+// A layer's product, split when its shape is.
+hipError_t run_product(MatmulArgs a, MatmulForm form, int32_t dtype, void* space, hipStream_t s) {
+  const MatmulShape shape = matmul_shape(a, form, dtype, false);
+  if (shape.splits == 1) return launch_matmul(a, form, dtype, shape, s);
+  a.part = static_cast<float*>(space);
+  const hipError_t e = launch_matmul(a, form, dtype, shape, s);
+  a.splits = shape.splits;
+  return e != hipSuccess ? e : launch_layer_parts(a, dtype, s);
 }
 
 // The same whatever the layout of w, the addresses and the wanted outputs.
@@ -71,7 +92,8 @@ LinearSpace linear_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtyp
   s.w_part = splits > 1 ? round256(static_cast<size_t>(splits) * static_cast<size_t>(n_in * n_out) * sizeof(float)) : 0;
   const int parts = slope_parts(static_cast<int32_t>(rows), static_cast<int32_t>(n_out));
   s.b_part = round256(static_cast<size_t>(parts) * static_cast<size_t>(n_out) * sizeof(float));
-  s.bytes = s.z_bar + s.w_part + s.b_part;
+  s.x_part = product_space(rows, n_out, n_in, dtype);
+  s.bytes = s.z_bar + s.w_part + s.b_part + s.x_part;
   return s;
 }
 
@@ -85,7 +107,7 @@ extern "C" {
 etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, const void* x, int64_t x_stride,
                         const void* w, int64_t w_in_stride, int64_t w_out_stride, const float* b, const void* residual,
                         int64_t residual_stride, int32_t act, void* y, int64_t y_stride, void* z, int64_t z_stride,
-                        hipStream_t s) {
+                        void* ws, size_t ws_bytes, hipStream_t s) {
   ETPC_TRY(check_layer(n_rows, n_in, n_out, dtype, act));
   if (n_rows == 0) return ETPC_OK;
   const int64_t size = size_of(dtype);
@@ -98,7 +120,10 @@ etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dty
   if (z != nullptr) ETPC_TRY(check_mat(mz, n_rows, n_out, dtype, true));
   const Operand ob{"b", b, 4 * n_out};
   ETPC_TRY(check_floats({ob}));
-  ETPC_TRY(check_apart({{my, n_rows, n_out, size}, {mz, n_rows, n_out, size}},
+  const size_t need = forward_space(n_rows, n_in, n_out, dtype);
+  ETPC_TRY(check_parts(ws, ws_bytes, need));
+  ETPC_TRY(check_apart({{my, n_rows, n_out, size}, {mz, n_rows, n_out, size},
+                        {"the workspace", need > 0 ? ws : nullptr, static_cast<int64_t>(need)}},
                        {{mx, n_rows, n_in, size}, operand(mw, size), {mr, n_rows, n_out, size}, ob}));
   if (n_in <= narrow::kMost && n_out <= narrow::kMost) {
     narrow::FwdArgs a{};
@@ -115,12 +140,19 @@ etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dty
   a.M = static_cast<int32_t>(n_rows), a.N = static_cast<int32_t>(n_out), a.K = static_cast<int32_t>(n_in);
   a.act = act;
   const MatmulForm form = mw.by_out ? MatmulForm::kRowsCols : MatmulForm::kRowsRows;
-  ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_matmul(a, form, dtype, matmul_shape(a, form, dtype, false), s));
+  ETPC_LAUNCH(ETPC_KIND_NODEWISE, run_product(a, form, dtype, ws, s));
   return ETPC_OK;
 }
 
-etpc_status etpc_linear_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act,
-                                       size_t* bytes) {
+etpc_status etpc_linear_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, size_t* bytes) {
+  if (bytes == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null output");
+  ETPC_TRY(check_layer(n_rows, n_in, n_out, dtype, ETPC_ACT_NONE));
+  *bytes = n_rows > 0 ? forward_space(n_rows, n_in, n_out, dtype) : 0;
+  return ETPC_OK;
+}
+
+etpc_status etpc_linear_backward_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act,
+                                                size_t* bytes) {
   if (bytes == nullptr) ETPC_FAIL(ETPC_ERR_INVALID_ARG, "null output");
   ETPC_TRY(check_layer(n_rows, n_in, n_out, dtype, act));
   *bytes = n_rows > 0 ? linear_space(n_rows, n_in, n_out, dtype, act).bytes : 0;
@@ -182,6 +214,7 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
   char* const at = static_cast<char*>(ws);
   float* const w_part = reinterpret_cast<float*>(at + space.z_bar);
   float* const b_part = reinterpret_cast<float*>(at + space.z_bar + space.w_part);
+  void* const x_part = at + space.z_bar + space.w_part + space.b_part;
   const int32_t rows = static_cast<int32_t>(n_rows), in = static_cast<int32_t>(n_in), out = static_cast<int32_t>(n_out);
   const void* z_bar = y_bar;
   int64_t z_bar_stride = y_bar_stride;
@@ -204,7 +237,7 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
     a.a = z_bar, a.lda = z_bar_stride, a.b = w, a.ldb = mw.m.stride, a.c = x_bar, a.ldc = x_bar_stride;
     a.M = rows, a.N = in, a.K = out;
     const MatmulForm form = mw.by_out ? MatmulForm::kRowsRows : MatmulForm::kRowsCols;
-    ETPC_LAUNCH(ETPC_KIND_NODEWISE, launch_matmul(a, form, dtype, matmul_shape(a, form, dtype, false), s));
+    ETPC_LAUNCH(ETPC_KIND_NODEWISE, run_product(a, form, dtype, x_part, s));
   }
   if (w_bar != nullptr) {
     MatmulArgs a = weight_product(n_rows, n_in, n_out, mwb.by_out);

@@ -118,6 +118,46 @@ hipError_t sum_parts(const float* part, int parts, int64_t rows, int64_t cols, v
   return hipGetLastError();
 }
 
+// ---- the layer's epilogue over partial sums: four columns a thread
+template <class T>
+__global__ __launch_bounds__(kThreads) void layer_parts_kernel(const MatmulArgs a) {
+  const int64_t per = (a.N + 3) / 4, total = per * a.M, size = static_cast<int64_t>(a.M) * a.N;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t m = i / per;
+    const int n = static_cast<int>(i - m * per) * 4;
+    float v[4] = {}, w[4];
+    int p = 0;
+    for (; p + 4 <= a.splits; p += 4) {   // four loads on their way
+      float u[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load<4, false>(a.part + (p + j) * size + m * a.N, n, a.N, u[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += u[j][k];
+    }
+    for (; p < a.splits; ++p) {
+      load<4, false>(a.part + p * size + m * a.N, n, a.N, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += w[k];
+    }
+    if (a.bias != nullptr) {
+      load<4, false>(a.bias, n, a.N, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += w[k];
+    }
+    if (a.z != nullptr) store<4, false>(static_cast<T*>(a.z) + m * a.ldz, n, a.N, v);
+    if (a.act != ETPC_ACT_NONE) activate<sizeof(T) == 4>(v, a.act);
+    if (a.res != nullptr) {
+      load<4, false>(static_cast<const T*>(a.res) + m * a.ldres, n, a.N, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += w[k];
+    }
+    store<4, false>(static_cast<T*>(a.c) + m * a.ldc, n, a.N, v);
+  }
+}
+
 // Bytes a lane with which an operand can go straight into LDS (0: it cannot): whole aligned pieces,
 // offsets inside a tile in 31 bits.  n: its other index; cols: contiguous along that one.
 int grain_of(const void* p, int64_t ld, int64_t n, int64_t k, bool cols, int64_t size) {
@@ -151,6 +191,18 @@ hipError_t launch_sum_parts(const float* part, int parts, int64_t rows, int64_t 
                               : sum_parts<F16>(part, parts, rows, cols, out, ld, tail, tail_n, s);
 }
 
+hipError_t launch_layer_parts(const MatmulArgs& a, int dtype, hipStream_t s) {
+  const int64_t units = ((a.N + 3) / 4 * static_cast<int64_t>(a.M) + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(std::min(units, kMaxGroups)));
+  if (dtype == ETPC_F32)
+    layer_parts_kernel<float><<<grid, kThreads, 0, s>>>(a);
+  else if (dtype == ETPC_BF16)
+    layer_parts_kernel<Bf16><<<grid, kThreads, 0, s>>>(a);
+  else
+    layer_parts_kernel<F16><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 // ---- narrow rows: whole chunks for every row of every operand?
 namespace narrow {
 namespace {
@@ -175,23 +227,27 @@ hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s) {
 }
 }  // namespace narrow
 
-MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split) {
+MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool sums) {
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;
   MatmulShape s{64, 0, 1, a.K, false};
   s.grain = std::min(grain_of(a.a, a.lda, a.M, a.K, form == MatmulForm::kColsCols, size),
                      grain_of(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size));
   const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
-  const int64_t bk = 128 / size;
-  if (split) {
+  const int64_t bk = 128 / size, slices = (a.K + bk - 1) / bk;
+  int64_t splits = 1;
+  if (sums) {
+    // one round of the largest tile that C fills, two of the others; at least 512 rows each
     s.tile = size == 2 && std::min(a.M, a.N) >= 256 ? 256 : std::min(a.M, a.N) > 64 ? 128 : 64;
-    const int64_t want = std::max<int64_t>(1, (s.tile == 256 ? 256 : 512) / tiles(s.tile)), most = std::max<int64_t>(1, a.K / 512);
-    int64_t each = (a.K + std::min(want, most) - 1) / std::min(want, most);
-    each = (each + bk - 1) / bk * bk;
-    s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));
-    s.splits = static_cast<int>((a.K + each - 1) / each);
+    splits = std::min(std::max<int64_t>(1, (s.tile == 256 ? 256 : 512) / tiles(s.tile)), std::max<int64_t>(1, a.K / 512));
   } else {
     s.tile = size == 2 && tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+    // Few tiles and a long k: a tile's products take longer than the second launch that adds ranges of k
+    // (a slice takes a CU about 0.45 us in fp32, 0.3 in 16 bits).
+    if (a.M > kFewRows && tiles(64) <= 128 && slices >= (size == 4 ? 12 : 20)) splits = std::min(512 / tiles(64), slices / 4);
   }
+  const int64_t each = (slices + splits - 1) / splits * bk;
+  s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));
+  s.splits = static_cast<int>((a.K + each - 1) / each);
   if (s.tile == 256 && s.grain != 16) s.tile = 128;
   s.deep = tiles(64) * s.splits <= 512;
   return s;

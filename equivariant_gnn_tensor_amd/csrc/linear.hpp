@@ -29,8 +29,9 @@ struct MatmulShape {
   int splits, k_split;
   bool deep;       // five slices on their way instead of two
 };
-// The shape for a product; `split` allows ranges of k.  Operands' addresses do not matter to the splits.
-MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool split);
+// The shape for a product; `sums`: of rows (a weight gradient).  Operands' addresses and strides do not
+// matter to the splits.
+MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool sums);
 hipError_t launch_matmul(const MatmulArgs& a, MatmulForm form, int dtype, const MatmulShape& shape, hipStream_t s);
 // Up to two rows: C(m, n) with B contiguous along k (`along`) or along n.  launch_matmul takes it.
 constexpr int kFewRows = 2;
@@ -53,6 +54,9 @@ struct SlopeArgs {
 };
 int slope_parts(int32_t rows, int32_t cols);
 hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t s);
+
+// The epilogue of a product over its partial sums a.part[a.splits][M][N].
+hipError_t launch_layer_parts(const MatmulArgs& a, int dtype, hipStream_t s);
 
 // out[r ld + c] = sum_{p < parts} part[p][r cols + c], rounded to the dtype once, and tail[i] = the sums
 // of the tail_n numbers that follow in each part; in a fixed order.  out, tail: null skips.  No

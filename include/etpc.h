@@ -444,10 +444,12 @@ typedef enum {
 etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, const void* x, int64_t x_stride,
                         const void* w, int64_t w_in_stride, int64_t w_out_stride, const float* b, const void* residual,
                         int64_t residual_stride, int32_t act, void* y, int64_t y_stride, void* z, int64_t z_stride,
-                        hipStream_t stream);
-/* Workspace of the backward call: the gradient before the activation, and partial sums. */
-etpc_status etpc_linear_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act,
-                                       size_t* bytes);
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+/* Workspaces: partial sums of the forward call (few rows of long inputs; 0 otherwise), and the
+ * gradient before the activation and partial sums of the backward call. */
+etpc_status etpc_linear_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, size_t* bytes);
+etpc_status etpc_linear_backward_workspace_size(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act,
+                                                size_t* bytes);
 /* Gradients of <y_bar, y>: with z_bar = y_bar act'(z), x_bar = z_bar w^T, w_bar = x^T z_bar and
  * b_bar = the column sums of z_bar; the residual's is y_bar itself.  x_bar and w_bar have the
  * rows' type (z_bar is rounded to it where it enters their products), b_bar is fp32, summed from

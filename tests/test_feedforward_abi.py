@@ -19,8 +19,8 @@ def message():
 
 
 def linear(rows=4, n_in=8, n_out=16, dtype=F32, x=A, xs=8, w=B, wi=16, wo=1, b=None, res=None, rs=16, act=0, y=D, ys=16, z=None,
-           zs=16):
-    return lib.etpc_linear(rows, n_in, n_out, dtype, x, xs, w, wi, wo, b, res, rs, act, y, ys, z, zs, None)
+           zs=16, ws=None, n=0):
+    return lib.etpc_linear(rows, n_in, n_out, dtype, x, xs, w, wi, wo, b, res, rs, act, y, ys, z, zs, ws, n, None)
 
 
 @pytest.mark.parametrize("kwargs,status,word", [
@@ -37,6 +37,8 @@ def linear(rows=4, n_in=8, n_out=16, dtype=F32, x=A, xs=8, w=B, wi=16, wo=1, b=N
     (dict(res=E, rs=15), INVALID, "stride"), (dict(z=E, zs=15), INVALID, "stride"), (dict(xs=1 << 60), OVERFLOW, "stride"),
     (dict(y=A), INVALID, "overlap"), (dict(y=B + 8), INVALID, "overlap"), (dict(res=D), INVALID, "overlap"),
     (dict(z=D + 32), INVALID, "overlap"), (dict(b=D), INVALID, "overlap"),
+    (dict(n_in=4096, xs=4096), WORKSPACE, "null"), (dict(n_in=4096, xs=4096, ws=E, n=64), WORKSPACE, "too small"),
+    (dict(n_in=4096, xs=4096, ws=D, n=1 << 20), INVALID, "overlap"), (dict(n_in=4096, xs=4096, ws=E + 1, n=1 << 20), WORKSPACE, "aligned"),
 ])
 def test_linear_refusals(kwargs, status, word):
     assert linear(**kwargs) == status and word in message()
@@ -70,11 +72,15 @@ def test_no_rows_is_no_work():
 
 def test_linear_workspace():
     n = C.c_size_t()
-    assert lib.etpc_linear_workspace_size(4, 8, 16, F32, 0, None) == INVALID
-    assert lib.etpc_linear_workspace_size(0, 8, 16, F32, 0, C.byref(n)) == OK and n.value == 0
-    assert lib.etpc_linear_workspace_size(1 << 30, 1 << 26, 8, F32, 0, C.byref(n)) == OVERFLOW
-    assert etpc.etpc_linear_workspace_size(1000, 64, 64, torch.bfloat16, "silu") >= 1000 * 64 * 2
-    assert etpc.etpc_linear_workspace_size(1000, 64, 64, torch.bfloat16) < 1000 * 64 * 2
+    assert lib.etpc_linear_workspace_size(4, 8, 16, F32, None) == INVALID
+    assert lib.etpc_linear_workspace_size(4, 8, 16, F32, C.byref(n)) == OK and n.value == 0
+    assert lib.etpc_linear_backward_workspace_size(4, 8, 16, F32, 0, None) == INVALID
+    assert lib.etpc_linear_backward_workspace_size(0, 8, 16, F32, 0, C.byref(n)) == OK and n.value == 0
+    assert lib.etpc_linear_backward_workspace_size(1 << 30, 1 << 26, 8, F32, 0, C.byref(n)) == OVERFLOW
+    assert etpc.etpc_linear_workspace_size(16, 4096, 64, torch.bfloat16) >= 16 * 64 * 4
+    assert etpc.etpc_linear_workspace_size(100000, 4096, 4096, torch.bfloat16) == 0
+    plain = etpc.etpc_linear_backward_workspace_size(1000, 256, 256, torch.bfloat16)
+    assert etpc.etpc_linear_backward_workspace_size(1000, 256, 256, torch.bfloat16, "silu") >= plain + 1000 * 256 * 2
 
 
 def test_binding_refusals():
