@@ -8,6 +8,7 @@ raises ImportError: there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import functools
 import operator
@@ -1214,39 +1215,52 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _grad_list(grads):
-    """(pointers, sizes, dtypes) as C arrays of a list of dense tensors on one device."""
-    n = len(grads)
-    ptrs, sizes, dtypes = (C.c_void_p * n)(), (C.c_int64 * n)(), (C.c_int32 * n)()
-    dev = grads[0].device if n else None
-    for k, t in enumerate(grads):
-        code = _ROW_TYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"tensor {k} must be float32, bfloat16 or float16, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"tensor {k} is on {t.device}, expected {dev}")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"tensor {k} must be one block of memory")
-        ptrs[k], sizes[k], dtypes[k] = t.data_ptr() or None, t.numel(), code
-    return ptrs, sizes, dtypes
+def _grad_list(grads, current: int):
+    """(pointers, sizes, dtypes, all contiguous) of a list of dense tensors on the current device.  Lists of hundreds of
+    tensors are usual, so each property is fetched for all of them in one pass."""
+    kinds = [t.dtype for t in grads]
+    codes = list(map(_ROW_TYPES.get, kinds))
+    if None in codes:
+        k = codes.index(None)
+        raise TypeError(f"tensor {k} must be float32, bfloat16 or float16, got {kinds[k]}")
+    devices = [t.get_device() for t in grads]
+    if devices.count(current) != len(devices):
+        k = next(k for k, d in enumerate(devices) if d != current)
+        raise ValueError(f"tensor {k} must live on the GPU, on the current device, got {grads[k].device}")
+    rows = all([t.is_contiguous() for t in grads])
+    if not rows:
+        for k, t in enumerate(grads):
+            if not _dense(t):
+                raise ValueError(f"tensor {k} must be one block of memory")
+    return [t.data_ptr() for t in grads], [t.numel() for t in grads], codes, rows
+
+
+def _c_list(kind, code: str, values):
+    return (kind * len(values)).from_buffer(array.array(code, values))
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_ws_most(n: int) -> int:
+    """Workspace that is enough for any n tensors: for n large ones, and 2048 partial sums where some of
+    them being empty leaves fewer launches."""
+    b = C.c_size_t()
+    _check(lib.etpc_grad_norm_workspace_size(n, (C.c_int64 * n)(*[(1 << 46) // max(n, 1 << 16)] * n), b))
+    return max(b.value, 2048 * 8)
 
 
 def _norm_call(grads, ord, norm, ws, stream):
-    grads = list(grads)
     if ord not in _NORM_ORDS:
         raise ValueError(f"ord must be 2 or inf, got {ord!r}")
-    if grads:
-        handle, dev = _check_device("tensor 0", grads[0], stream), grads[0].device
-    else:
-        dev = torch.device("cuda", torch.cuda.current_device()) if norm is None else norm.device
-        handle = _stream(stream)
-    ptrs, sizes, dtypes = _grad_list(grads)
+    grads = grads if type(grads) is list else list(grads)
+    current = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    ptrs, sizes, codes, rows = _grad_list(grads, current if current >= 0 else -2)
+    dev = grads[0].device if grads else torch.device("cuda", current)
+    handle = torch._C._cuda_getCurrentRawStream(current) if stream is None else _stream(stream)
     if norm is None:
         norm = _new((), dev, stream)
-    need = C.c_size_t()
-    _check(lib.etpc_grad_norm_workspace_size(len(grads), sizes, need))
-    wsp, wsn, keep = _scratch(ws, need.value, dev, stream)
-    return grads, ptrs, sizes, dtypes, _NORM_ORDS[ord], norm, _vector("norm", norm, 1, dev), wsp, wsn, keep, handle
+    wsp, wsn, keep = _scratch(ws, _norm_ws_most(len(grads)), dev, stream)
+    lists = (_c_list(C.c_int64, "q", ptrs), _c_list(C.c_int64, "q", sizes), _c_list(C.c_int32, "i", codes))
+    return grads, (sizes, codes, rows), lists, _NORM_ORDS[ord], norm, _vector("norm", norm, 1, dev), wsp, wsn, keep, handle
 
 
 def etpc_grad_norm_workspace_size(sizes) -> int:
@@ -1260,7 +1274,7 @@ def etpc_grad_norm_workspace_size(sizes) -> int:
 def etpc_grad_norm(grads, ord=2, norm=None, ws=None, stream=None) -> torch.Tensor:
     """The global norm of a list of tensors (f32, bf16 and f16 may be mixed; any dense layout) as
     one f32 number on the GPU: ord 2, or inf for the largest magnitude."""
-    grads, ptrs, sizes, dtypes, code, norm, np_, wsp, wsn, _keep, handle = _norm_call(grads, ord, norm, ws, stream)
+    grads, _, (ptrs, sizes, dtypes), code, norm, np_, wsp, wsn, _keep, handle = _norm_call(grads, ord, norm, ws, stream)
     st = lib.etpc_grad_norm(len(grads), ptrs, sizes, dtypes, code, np_, wsp, wsn, handle)
     if st:
         _check(st)
@@ -1269,21 +1283,24 @@ def etpc_grad_norm(grads, ord=2, norm=None, ws=None, stream=None) -> torch.Tenso
 
 def etpc_clip_grad_norm(grads, max_norm: float, ord=2, outs=None, norm=None, ws=None, stream=None) -> torch.Tensor:
     """The global norm, and every tensor times min(1, max_norm / (norm + 1e-6)), in place or into
-    `outs` (tensors of the same shapes, strides and types).  A norm that is not finite leaves the
+    `outs` (of the same types and sizes, element for element in memory: the same shapes and strides where
+    a tensor is not contiguous).  A norm that is not finite leaves the
     gradients as they are."""
-    grads, ptrs, sizes, dtypes, code, norm, np_, wsp, wsn, _keep, handle = _norm_call(grads, ord, norm, ws, stream)
-    if outs is None:
-        op = None
-    else:
-        outs = list(outs)
+    grads, (numels, codes, rows), (ptrs, sizes, dtypes), code, norm, np_, wsp, wsn, _keep, handle = _norm_call(grads, ord, norm, ws, stream)
+    op = None
+    if outs is not None:
+        outs = outs if type(outs) is list else list(outs)
         if len(outs) != len(grads):
             raise ValueError(f"{len(grads)} tensors and {len(outs)} outs")
-        for k, (o, g) in enumerate(zip(outs, grads)):
-            if o.shape != g.shape or o.dtype != g.dtype or o.device != g.device:
-                raise ValueError(f"outs {k} must be like its tensor")
-            if o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()):
-                raise ValueError(f"outs {k} must have its tensor's strides")
-        op = (C.c_void_p * len(outs))(*[o.data_ptr() or None for o in outs])
+        to, to_numels, to_codes, to_rows = _grad_list(outs, torch.cuda.current_device())
+        if to_numels != numels or to_codes != codes:
+            k = next(k for k in range(len(grads)) if to_numels[k] != numels[k] or to_codes[k] != codes[k])
+            raise ValueError(f"outs {k} must be like its tensor")
+        if not (rows and to_rows):
+            for k, (o, g) in enumerate(zip(outs, grads)):
+                if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+                    raise ValueError(f"outs {k} must have its tensor's shape and strides")
+        op = _c_list(C.c_int64, "q", to)
     st = lib.etpc_clip_grad_norm(len(grads), ptrs, op, sizes, dtypes, code, max_norm, np_, wsp, wsn, handle)
     if st:
         _check(st)

@@ -4,12 +4,12 @@
 //
 // Memory bound: the gradients are read once for the norm, and read and written once more to be
 // clipped.  Pointers and sizes travel in the launch's arguments (no copy to the device, so the
-// calls can be captured), and the tensors are cut into pieces of one size so that large and small
-// ones share the chip evenly.  Squares are exact in 64 bits and their sums neither overflow nor
-// lose small tensors beside large ones; the conversions and multiply-adds in 64 bits stay hidden
-// behind the loads.  A workgroup leaves one partial result; there are few enough (2048, more only
-// with thousands of tensors) that every workgroup of the clipping launch adds them all up itself,
-// in one order, instead of a launch between.
+// calls can be captured).  The tensors are one long row of units, dealt in equal runs to the
+// workgroups: large and small tensors share the chip evenly, and a workgroup looks for its place
+// once.  Squares are exact in 64 bits and their sums neither overflow nor lose small tensors beside
+// large ones; the conversions and multiply-adds in 64 bits stay hidden behind the loads.  A
+// workgroup leaves one partial result.  Up to 1024 of them every workgroup of the clipping launch
+// adds up itself, in one order, instead of a launch between; more take that launch.
 #include <algorithm>
 
 #include "grad_norm.hpp"
@@ -25,39 +25,50 @@ struct Table {
   struct Entry {
     const void* p;
     void* out;
-    int64_t n;
-    int32_t first;      // its first piece among the launch's
-    int32_t dtype;
+    int64_t first;      // its first unit among the launch's
+    int64_t n_dtype;    // elements, and the dtype from bit 56 on
   };
   Entry t[kTensors];
-  int32_t n, pieces, chunk;
+  int64_t units;
+  int32_t n;
 };
 static_assert(sizeof(Table) + 64 <= 4096, "arguments of a launch");
 
-// The tensor a piece belongs to: the last that starts at or before it (empty ones hold none).
-__device__ inline int find(const Table& a, int piece) {
-  int lo = 0, hi = a.n - 1;
+// f(entry, first element, elements) for each tensor's part of this workgroup's run of units.
+template <class F>
+__device__ inline void for_run(const Table& a, F&& f) {
+  const int64_t each = a.units / gridDim.x, more = a.units % gridDim.x, b = blockIdx.x;
+  int64_t u = b * each + (b < more ? b : more);
+  const int64_t end = u + each + (b < more ? 1 : 0);
+  int lo = 0, hi = a.n - 1;   // the last tensor that starts at or before u
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (a.t[mid].first <= piece) lo = mid;
+    if (a.t[mid].first <= u) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  for (; u < end; ++lo) {
+    const Table::Entry& e = a.t[lo];
+    const int64_t next = lo + 1 < a.n ? min(a.t[lo + 1].first, end) : end, size = e.n_dtype & ((int64_t{1} << 56) - 1);
+    const int64_t from = (u - e.first) * kUnit, to = min(size, (next - e.first) * kUnit);
+    f(e, from, to - from);
+    u = next;
+  }
 }
 
 template <class T, class F>
-__device__ inline void for_vectors(const T* __restrict__ p, int n, F&& f) {
-  int c = 8 * threadIdx.x;
+__device__ inline void for_vectors(const T* __restrict__ p, int64_t n, F&& f) {
+  int64_t c = 8 * threadIdx.x;
   for (; c + 8 * kThreads * (kUnroll - 1) + 8 <= n; c += 8 * kThreads * kUnroll) {
     float v[kUnroll][8];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) load<8, true>(p, c + i * 8 * kThreads, n, v[i]);
+    for (int i = 0; i < kUnroll; ++i) load<8, true>(p + c, i * 8 * kThreads, 8 * kThreads * kUnroll, v[i]);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) f(c + i * 8 * kThreads, v[i]);
   }
-  for (; c < n; c += 8 * kThreads) {
+  for (; c < n; c += 8 * kThreads) {   // the last vector of a part shorter than eight goes by elements
+    const int64_t at = c + 8 <= n || n < 8 ? c : n - 8;
     float v[8];
-    load<8, false>(p, c, n, v);
+    load<8, false>(p + at, static_cast<int>(c - at), static_cast<int>(min(n - at, int64_t{8})), v);
     f(c, v);
   }
 }
@@ -82,18 +93,18 @@ __device__ inline double reduce(double v, bool max) {
 }
 
 template <class T>
-__device__ inline double piece_norm(const T* p, int n, bool max) {
+__device__ inline double piece_norm(const T* p, int64_t n, bool max) {
   double s = 0.0;
   if (max) {
     uint32_t m = 0;
-    for_vectors(p, n, [&](int, const float (&v)[8]) {
+    for_vectors(p, n, [&](int64_t, const float (&v)[8]) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = std::max(m, __float_as_uint(v[k]) & 0x7fffffffu);
     });
     s = fabs(static_cast<double>(__uint_as_float(m)));
   } else {
     double t[4] = {};
-    for_vectors(p, n, [&](int, const float (&v)[8]) {
+    for_vectors(p, n, [&](int64_t, const float (&v)[8]) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) t[k & 3] = fma(static_cast<double>(v[k]), static_cast<double>(v[k]), t[k & 3]);
     });
@@ -104,15 +115,13 @@ __device__ inline double piece_norm(const T* p, int n, bool max) {
 
 __global__ __launch_bounds__(kThreads) void norm_kernel(const Table a, bool max, double* __restrict__ parts) {
   double s = 0.0;
-  for (int piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
-    const Table::Entry& e = a.t[find(a, piece)];
-    const int64_t at = static_cast<int64_t>(piece - e.first) * a.chunk;
-    const int n = static_cast<int>(std::min<int64_t>(e.n - at, a.chunk));
-    const double v = e.dtype == ETPC_F32    ? piece_norm(static_cast<const float*>(e.p) + at, n, max)
-                     : e.dtype == ETPC_BF16 ? piece_norm(static_cast<const Bf16*>(e.p) + at, n, max)
-                                            : piece_norm(static_cast<const F16*>(e.p) + at, n, max);
+  for_run(a, [&](const Table::Entry& e, int64_t at, int64_t n) {
+    const int dtype = static_cast<int>(e.n_dtype >> 56);
+    const double v = dtype == ETPC_F32    ? piece_norm(static_cast<const float*>(e.p) + at, n, max)
+                     : dtype == ETPC_BF16 ? piece_norm(static_cast<const Bf16*>(e.p) + at, n, max)
+                                          : piece_norm(static_cast<const F16*>(e.p) + at, n, max);
     s = join(s, v, max);
-  }
+  });
   s = reduce(s, max);
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
@@ -131,34 +140,37 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const double* __restri
 }
 
 template <class T>
-__device__ inline void scale_piece(const T* p, T* out, int n, float by) {
+__device__ inline void scale_piece(const T* p, T* out, int64_t n, float by) {
   // in place: a thread reads a vector before it writes it, and no other thread's
-  for_vectors(p, n, [&](int c, float (&v)[8]) {
+  for_vectors(p, n, [&](int64_t c, float (&v)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= by;
-    store<8, false>(out, c, n, v);
+    store<8, false>(out + c, 0, static_cast<int>(min(n - c, int64_t{8})), v);
   });
 }
 
+// parts: the norm is taken from them and written by the first workgroup; null: it is in *norm.
 __global__ __launch_bounds__(kThreads) void clip_kernel(const Table a, bool max, float max_norm,
                                                         const double* __restrict__ parts, int64_t count, float* norm) {
-  const double v = total(parts, count, max);
-  const float rounded = static_cast<float>(v);
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = rounded;
-  const bool finite = fabsf(rounded) <= 3.4028234e38f;
-  const float by = finite ? static_cast<float>(fmin(1.0, static_cast<double>(max_norm) / (v + 1e-6))) : 1.f;
-  for (int piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
-    const Table::Entry& e = a.t[find(a, piece)];
-    if (by == 1.f && e.out == e.p) continue;
-    const int64_t at = static_cast<int64_t>(piece - e.first) * a.chunk;
-    const int n = static_cast<int>(std::min<int64_t>(e.n - at, a.chunk));
-    if (e.dtype == ETPC_F32)
+  float value;
+  if (parts != nullptr) {
+    value = static_cast<float>(total(parts, count, max));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = value;
+  } else {
+    value = *norm;
+  }
+  const bool finite = fabsf(value) <= 3.4028234e38f;
+  const float by = finite ? static_cast<float>(fmin(1.0, static_cast<double>(max_norm) / (value + 1e-6))) : 1.f;
+  for_run(a, [&](const Table::Entry& e, int64_t at, int64_t n) {
+    if (by == 1.f && e.out == e.p) return;
+    const int dtype = static_cast<int>(e.n_dtype >> 56);
+    if (dtype == ETPC_F32)
       scale_piece(static_cast<const float*>(e.p) + at, static_cast<float*>(e.out) + at, n, by);
-    else if (e.dtype == ETPC_BF16)
+    else if (dtype == ETPC_BF16)
       scale_piece(static_cast<const Bf16*>(e.p) + at, static_cast<Bf16*>(e.out) + at, n, by);
     else
       scale_piece(static_cast<const F16*>(e.p) + at, static_cast<F16*>(e.out) + at, n, by);
-  }
+  });
 }
 
 // The launches' tables one after another.
@@ -166,19 +178,17 @@ template <class F>
 hipError_t for_tables(int32_t n, const void* const* grads, void* const* outs, const int64_t* sizes,
                       const int32_t* dtypes, const NormPlan& plan, F&& launch) {
   Table a;
-  a.chunk = plan.chunk;
   for (int32_t k = 0; k < n;) {
     a.n = 0;
-    int64_t pieces = 0;
+    a.units = 0;
     for (; k < n && a.n < kTensors; ++k) {
       if (sizes[k] == 0) continue;
-      a.t[a.n++] = Table::Entry{grads[k], outs != nullptr ? outs[k] : const_cast<void*>(grads[k]), sizes[k],
-                                static_cast<int32_t>(pieces), dtypes[k]};
-      pieces += (sizes[k] + plan.chunk - 1) / plan.chunk;
+      a.t[a.n++] = Table::Entry{grads[k], outs != nullptr ? outs[k] : const_cast<void*>(grads[k]), a.units,
+                                sizes[k] | static_cast<int64_t>(dtypes[k]) << 56};
+      a.units += (sizes[k] + kUnit - 1) / kUnit;
     }
     if (a.n == 0) break;
-    a.pieces = static_cast<int32_t>(pieces);
-    const hipError_t e = launch(a, static_cast<unsigned>(std::min<int64_t>(pieces, plan.groups)));
+    const hipError_t e = launch(a, static_cast<unsigned>(std::min<int64_t>(a.units, plan.groups)));
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -187,20 +197,18 @@ hipError_t for_tables(int32_t n, const void* const* grads, void* const* outs, co
 }  // namespace
 
 NormPlan norm_plan(int32_t n, const int64_t* sizes) {
-  int64_t total = 0, full = 0;
-  for (int32_t k = 0; k < n; ++k) total += sizes[k], full += sizes[k] > 0;
+  int64_t full = 0;
+  for (int32_t k = 0; k < n; ++k) full += sizes[k] > 0;
   NormPlan p{};
-  p.chunk = 2048;
-  while (p.chunk < (1 << 20) && total / p.chunk > 4096) p.chunk *= 2;
   p.launches = static_cast<int32_t>((full + kTensors - 1) / kTensors);
-  p.groups = p.launches > 0 ? std::max(64, 2048 / p.launches) : 0;
-  int64_t pieces = 0, held = 0;
+  p.groups = p.launches > 0 ? std::min(2048, std::max(64, 6144 / p.launches)) : 0;
+  int64_t units = 0, held = 0;
   for (int32_t k = 0; k < n; ++k) {
     if (sizes[k] == 0) continue;
-    pieces += (sizes[k] + p.chunk - 1) / p.chunk;
-    if (++held == kTensors) p.parts += std::min<int64_t>(pieces, p.groups), pieces = held = 0;
+    units += (sizes[k] + kUnit - 1) / kUnit;
+    if (++held == kTensors) p.parts += std::min<int64_t>(units, p.groups), units = held = 0;
   }
-  p.parts += std::min<int64_t>(pieces, p.groups);
+  p.parts += std::min<int64_t>(units, p.groups);
   return p;
 }
 
@@ -221,9 +229,13 @@ hipError_t launch_norm_finish(const double* parts, int64_t count, bool max, floa
 hipError_t launch_clip(int32_t n, const void* const* grads, void* const* outs, const int64_t* sizes,
                        const int32_t* dtypes, bool max, float max_norm, const double* parts, float* norm, hipStream_t s) {
   const NormPlan plan = norm_plan(n, sizes);
+  if (plan.parts > 1024) {
+    const hipError_t e = launch_norm_finish(parts, plan.parts, max, norm, s);
+    if (e != hipSuccess) return e;
+    parts = nullptr;
+  }
   return for_tables(n, grads, outs, sizes, dtypes, plan, [&](const Table& a, unsigned groups) {
     clip_kernel<<<dim3(groups), dim3(kThreads), 0, s>>>(a, max, max_norm, parts, plan.parts, norm);
-    norm = nullptr;   // the first launch writes it
     return hipGetLastError();
   });
 }
