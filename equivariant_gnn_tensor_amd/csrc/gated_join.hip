@@ -4,9 +4,9 @@
 namespace etpc {
 namespace {
 
-// A workgroup sums 16 adjacent columns of `part`: 64 slices of the parts, each in order, then the
-// slices in order.
-constexpr int kCols = 16, kSlices = 64;
+// A workgroup sums 64 adjacent columns of `part`: 16 slices of the parts, each in order, then the
+// slices in order (512 parts of 5 x 2047 sums: 6.3 us; 10.9 with 16 columns and 64 slices).
+constexpr int kCols = 64, kSlices = 16;
 struct Bars5 {
   float* out[5];
 };
