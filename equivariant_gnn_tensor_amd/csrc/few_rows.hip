@@ -1,4 +1,6 @@
-// Launches of the dense layer for up to eight rows.
+// Launches of the dense layer for one or two rows.
+#include <algorithm>
+
 #include "few_rows.hpp"
 
 namespace etpc {
@@ -6,23 +8,24 @@ namespace {
 
 template <class T, int M>
 hipError_t launch(const MatmulArgs& a, bool along, hipStream_t s) {
+  const auto groups = [&](unsigned outputs, unsigned most) { return dim3(std::min((a.N + outputs - 1) / outputs, most)); };
   if (along) {
     // one output a wave until there are enough waves for every CU
     if (a.N <= 4096)
-      few::along_kernel<T, M, 1><<<dim3((a.N + 3u) / 4u), dim3(few::kAlongThreads), 0, s>>>(a);
+      few::along_kernel<T, M, 1><<<groups(4, 1 << 20), dim3(few::kAlongThreads), 0, s>>>(a);
     else
-      few::along_kernel<T, M, 4><<<dim3((a.N + 15u) / 16u), dim3(few::kAlongThreads), 0, s>>>(a);
+      few::along_kernel<T, M, 4><<<groups(16, 1 << 20), dim3(few::kAlongThreads), 0, s>>>(a);
   } else {
     constexpr unsigned cols = 8 * 16 / sizeof(T);
-    few::across_kernel<T, M><<<dim3((a.N + cols - 1) / cols), dim3(few::kAcrossThreads), 0, s>>>(a);
+    few::across_kernel<T, M><<<groups(cols, 1 << 18), dim3(few::kAcrossThreads), 0, s>>>(a);
   }
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch(const MatmulArgs& a, bool along, hipStream_t s) {
-  return a.M == 1 ? launch<T, 1>(a, along, s) : a.M == 2 ? launch<T, 2>(a, along, s)
-         : a.M <= 4 ? launch<T, 4>(a, along, s) : launch<T, 8>(a, along, s);
+  static_assert(kFewRows == 2, "the rows below");
+  return a.M == 1 ? launch<T, 1>(a, along, s) : launch<T, 2>(a, along, s);
 }
 
 }  // namespace

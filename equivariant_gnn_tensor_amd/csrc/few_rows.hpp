@@ -1,6 +1,6 @@
-// The dense layer for up to eight rows (templates; few_rows.hip holds the launches).
+// The dense layer for one or two rows (templates; few_rows.hip holds the launches).
 //
-//   C(m, n) = epilogue(sum_k A(m, k) B(k, n)),  m < 8
+//   C(m, n) = epilogue(sum_k A(m, k) B(k, n)),  m < 2
 //
 // The weights are read once and nothing else counts, so this is about having enough of them on
 // their way at once: no matrix instructions, no slices, one pass with up to eight 16-byte loads a lane in
@@ -9,7 +9,8 @@
 //           sums are added over the wave at the end.
 //   across: weights contiguous in n.  Eight lanes take 128 bytes of n of one k, a wave eight k and a
 //           workgroup 128; the sums are added over lanes, then over waves in LDS.
-// fp32 sums in a fixed order.  1 x 1024 -> 1024 fp32 (4 MB of weights, across): XXX us.
+// fp32 sums in a fixed order.  From three rows on the tiles of matmul.hpp are faster (eight rows of 4096 ->
+// 4096 bf16: 56 and 74 us here, along and across, where conversions and multiply-adds count; 14 there).  1 x 1024 -> 1024 fp32 (4 MB of weights, across): 4.6 us.
 #pragma once
 
 #include "activation.hpp"
@@ -46,38 +47,41 @@ __global__ __launch_bounds__(kAlongThreads) void along_kernel(const MatmulArgs a
   constexpr int E = 16 / sizeof(T);
   __shared__ float rows[M][kBlock];
   const int lane = threadIdx.x & 63;
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * (kAlongThreads / 64) + (threadIdx.x >> 6)) * kOwn;
-  float sum[kOwn][M] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kBlock) {
-    if (k0 > 0) __syncthreads();
-    stage<T, M>(rows, a, k0);
-    __syncthreads();
-    const int n = min(kBlock, a.K - k0);
+  constexpr int kGroup = kAlongThreads / 64 * kOwn;   // outputs of a workgroup, which walks on past a launch's most
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kGroup; first < a.N; first += static_cast<int64_t>(gridDim.x) * kGroup) {
+    const int64_t n0 = first + (threadIdx.x >> 6) * kOwn;
+    float sum[kOwn][M] = {};
+    for (int k0 = 0; k0 < a.K; k0 += kBlock) {
+      __syncthreads();
+      stage<T, M>(rows, a, k0);
+      __syncthreads();
+      const int n = min(kBlock, a.K - k0);
 #pragma unroll 2
-    for (int k = lane * E; k < n; k += 64 * E) {
-      float w[kOwn][E];
+      for (int k = lane * E; k < n; k += 64 * E) {
+        float w[kOwn][E];
 #pragma unroll
-      for (int o = 0; o < kOwn; ++o) {
-        const int64_t row = min(n0 + o, static_cast<int64_t>(a.N) - 1);
-        load<E, false>(static_cast<const T*>(a.b) + row * a.ldb, k0 + k, a.K, w[o]);
-      }
-#pragma unroll
-      for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float x = rows[m][k + e];
-#pragma unroll
-          for (int o = 0; o < kOwn; ++o) sum[o][m] = fmaf(x, w[o][e], sum[o][m]);
+        for (int o = 0; o < kOwn; ++o) {
+          const int64_t row = min(n0 + o, static_cast<int64_t>(a.N) - 1);
+          load<E, false>(static_cast<const T*>(a.b) + row * a.ldb, k0 + k, a.K, w[o]);
         }
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float x = rows[m][k + e];
+#pragma unroll
+            for (int o = 0; o < kOwn; ++o) sum[o][m] = fmaf(x, w[o][e], sum[o][m]);
+          }
+      }
     }
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const float v = lane_sum<64>(sum[o][m]);
+        if (lane == o * M + m && m < a.M && n0 + o < a.N) finish<T>(a, m, static_cast<int>(n0) + o, v);
+      }
   }
-#pragma unroll
-  for (int o = 0; o < kOwn; ++o)
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const float v = lane_sum<64>(sum[o][m]);
-      if (lane == o * M + m && m < a.M && n0 + o < a.N) finish<T>(a, m, static_cast<int>(n0) + o, v);
-    }
 }
 
 constexpr int kAcrossThreads = 1024;
@@ -88,45 +92,47 @@ __global__ __launch_bounds__(kAcrossThreads) void across_kernel(const MatmulArgs
   __shared__ float lds[kStaged > kSums ? kStaged : kSums];
   float(*const rows)[kBlock] = reinterpret_cast<float(*)[kBlock]>(lds);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols;
-  const int n = static_cast<int>(n0) + lane % 8 * E, mine = wave * 8 + lane / 8;
-  float sum[M][E] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kBlock) {
-    if (k0 > 0) __syncthreads();
-    stage<T, M>(rows, a, k0);
-    __syncthreads();
-    const int count = min(kBlock, a.K - k0);
+  const int mine = wave * 8 + lane / 8;
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols; n0 < a.N; n0 += static_cast<int64_t>(gridDim.x) * kCols) {
+    const int n = static_cast<int>(n0) + lane % 8 * E;
+    float sum[M][E] = {};
+    for (int k0 = 0; k0 < a.K; k0 += kBlock) {
+      __syncthreads();
+      stage<T, M>(rows, a, k0);
+      __syncthreads();
+      const int count = min(kBlock, a.K - k0);
 #pragma unroll 8
-    for (int k = mine; k < count; k += kWaves * 8) {
-      float w[E];
-      load<E, false>(static_cast<const T*>(a.b) + (k0 + k) * a.ldb, n, a.N, w);
+      for (int k = mine; k < count; k += kWaves * 8) {
+        float w[E];
+        load<E, false>(static_cast<const T*>(a.b) + (k0 + k) * a.ldb, n, a.N, w);
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const float x = rows[m][k];
+        for (int m = 0; m < M; ++m) {
+          const float x = rows[m][k];
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[m][e] = fmaf(x, w[e], sum[m][e]);
+          for (int e = 0; e < E; ++e) sum[m][e] = fmaf(x, w[e], sum[m][e]);
+        }
       }
     }
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll
-  for (int m = 0; m < M; ++m)
+    for (int m = 0; m < M; ++m)
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      // over the eight k of the wave: lanes 8, 16 and 32 apart
-      float v = sum[m][e];
-      v += dpp_f<0x128>(v);   // rotation by eight in each row of sixteen
-      v = add_lane16(v);
-      v = add_lane32(v);
-      if (lane < 8) lds[(wave * M + m) * kCols + lane * E + e] = v;
+      for (int e = 0; e < E; ++e) {
+        // over the eight k of the wave: lanes 8, 16 and 32 apart
+        float v = sum[m][e];
+        v += dpp_f<0x128>(v);   // rotation by eight in each row of sixteen
+        v = add_lane16(v);
+        v = add_lane32(v);
+        if (lane < 8) lds[(wave * M + m) * kCols + lane * E + e] = v;
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < M * kCols; i += kAcrossThreads) {
+      const int m = i / kCols, c = i % kCols;
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) v += lds[(q * M + m) * kCols + c];
+      if (m < a.M && n0 + c < a.N) finish<T>(a, m, static_cast<int>(n0) + c, v);
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < M * kCols; i += kAcrossThreads) {
-    const int m = i / kCols, c = i % kCols;
-    float v = 0.f;
-#pragma unroll
-    for (int q = 0; q < kWaves; ++q) v += lds[(q * M + m) * kCols + c];
-    if (m < a.M && n0 + c < a.N) finish<T>(a, m, static_cast<int>(n0) + c, v);
   }
 }
 

@@ -65,14 +65,30 @@ size_t forward_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
   return n_in <= narrow::kMost && n_out <= narrow::kMost ? 0 : product_space(rows, n_in, n_out, dtype);
 }
 
-// A layer's product, split when its shape is.
+// A layer's product, split when its shape is.  One or two rows past the last whole tile are left to the
+// kernel for few rows where they would cost some CUs one tile more than all others have (4097 x 2047
+// -> 511 fp32: 65 x 8 tiles on 256 CUs are three rounds instead of two; 112 us with them, 96 without).
 hipError_t run_product(MatmulArgs a, MatmulForm form, int32_t dtype, void* space, hipStream_t s) {
   const MatmulShape shape = matmul_shape(a, form, dtype, false);
-  if (shape.splits == 1) return launch_matmul(a, form, dtype, shape, s);
-  a.part = static_cast<float*>(space);
+  if (shape.splits > 1) {
+    a.part = static_cast<float*>(space);
+    const hipError_t e = launch_matmul(a, form, dtype, shape, s);
+    a.splits = shape.splits;
+    return e != hipSuccess ? e : launch_layer_parts(a, dtype, s);
+  }
+  const int32_t over = a.M % shape.tile, whole = a.M - over;
+  const int64_t across = (a.N + shape.tile - 1) / shape.tile, down = whole / shape.tile;
+  if (over == 0 || over > kFewRows || whole == 0 || (down * across + 255) / 256 == ((down + 1) * across + 255) / 256)
+    return launch_matmul(a, form, dtype, shape, s);
+  const int64_t size = size_of(dtype);
+  const auto from = [&](const void* p, int64_t stride) { return p == nullptr ? p : static_cast<const char*>(p) + whole * stride * size; };
+  MatmulArgs rest = a;
+  rest.M = over;
+  rest.a = from(a.a, a.lda), rest.res = from(a.res, a.ldres);
+  rest.c = const_cast<void*>(from(a.c, a.ldc)), rest.z = const_cast<void*>(from(a.z, a.ldz));
+  a.M = whole;
   const hipError_t e = launch_matmul(a, form, dtype, shape, s);
-  a.splits = shape.splits;
-  return e != hipSuccess ? e : launch_layer_parts(a, dtype, s);
+  return e != hipSuccess ? e : launch_matmul(rest, form, dtype, matmul_shape(rest, form, dtype, false), s);
 }
 
 // The same whatever the layout of w, the addresses and the wanted outputs.

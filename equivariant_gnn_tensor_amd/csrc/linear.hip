@@ -23,13 +23,13 @@ struct SlopeShape {
   int parts;
 };
 SlopeShape slope_shape(int32_t rows, int32_t cols) {
-  const int vecs = (cols + 7) / 8;
+  const int vecs = cols / 8 + (cols % 8 != 0);
   SlopeShape s{8, 1, 1};
   while (s.g < kThreads && s.g < vecs) s.g *= 2;
   s.groups = (vecs + s.g - 1) / s.g;
   const int per = kThreads / s.g;
-  const int units = (rows + per - 1) / per;
-  s.parts = std::max(1, std::min((units + 3) / 4, 1024 / s.groups));
+  const int64_t units = (static_cast<int64_t>(rows) + per - 1) / per;
+  s.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((units + 3) / 4, 1024 / s.groups)));
   return s;
 }
 
@@ -229,7 +229,7 @@ hipError_t run_bwd(const BwdArgs& a, int dtype, hipStream_t s) {
 
 MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool sums) {
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;
-  MatmulShape s{64, 0, 1, a.K, false};
+  MatmulShape s{64, 0, 1, a.K, 2};
   s.grain = std::min(grain_of(a.a, a.lda, a.M, a.K, form == MatmulForm::kColsCols, size),
                      grain_of(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size));
   const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
@@ -249,7 +249,9 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
   s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));
   s.splits = static_cast<int>((a.K + each - 1) / each);
   if (s.tile == 256 && s.grain != 16) s.tile = 128;
-  s.deep = tiles(64) * s.splits <= 512;
+  // As many slices on their way as LDS holds when every CU has its share of the tiles at once.
+  const int64_t small = tiles(64) * s.splits;
+  s.stages = small <= 512 ? 5 : small <= 768 ? 3 : 2;
   return s;
 }
 

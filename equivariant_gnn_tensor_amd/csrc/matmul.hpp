@@ -8,7 +8,7 @@
 // of the four pairs (MatmulForm).
 //
 // A workgroup owns a BM x BN tile of C and walks k in slices of 128 bytes (64 elements of 16
-// bits, 32 of 32), two slices in LDS in turn.
+// bits, 32 of 32) through a ring of slices in LDS.
 //   LDS, rows: [row][8 chunks of 16 bytes], chunk c of row r at c ^ (r / 2 mod 8).  The 64 banks
 //   hold two rows, and a fragment read takes one chunk of each of 16 rows at a time: the exclusive
 //   or puts those of the eight even (odd) rows on different banks (with r mod 8 half of all LDS
@@ -26,6 +26,13 @@
 // lane ends up with four adjacent columns of one row at a time; the epilogue turns them over
 // to whole row segments through LDS and is then plain row code: bias, pre-activation,
 // activation, residual, one rounding, 16-byte accesses of any alignment.
+//
+// Tiles: 256 x 256 by eight waves of 128 x 64 (16 bits), 128 x 128 by four of 64 x 64, 64 x 64 by four of
+// 32 x 32; matmul_shape chooses.  8192 x 8192 -> 8192 f16: 880 us, 1250 TFLOP/s with the first
+// (LDS busy a quarter of the time, the matrix pipes 76 %, the clock held at about 1.6 GHz by power),
+// 1057 with the second; 256 x 128 tiles of half slices, two workgroups a CU, 971.
+// 65408 x 1024 -> 4096 bf16 501 us (1095), 65408 x 1024 -> 1024 fp32 989 us (139; the matrix
+// instructions' peak is 157).  The large tile's results cost 50 us of the 501 (LDS) and 25 (stores).
 #pragma once
 
 #include <algorithm>
@@ -43,8 +50,7 @@ namespace mm {
 // assembly, so that the compiler's own counting of loads does not wait for more of them (and of the
 // epilogue's stores among them) than barrier_after_loads; nothing but LDS and m0 is written (the
 // compiler keeps nothing in m0: it sets it before each use); the wait states cover m0 and scalars that
-// a vector instruction has just written.  What it counts itself is only waited
-// for earlier by that.
+// a vector instruction has just written.  What the compiler counts itself is only waited for earlier.
 typedef int Range __attribute__((ext_vector_type(4)));
 template <int kGrain>
 __device__ inline void load_lds(uint32_t lds, const Range& range, int off) {
@@ -134,8 +140,8 @@ struct Side {
     Chunk t[kPer];
     int64_t off[kPer];
     const T* p;
-    int64_t ld, first;
-    int n, K, k0;
+    int64_t ld, first, k0;
+    int n, K;
     __device__ inline void start(const T* base, int64_t ld_, int64_t first_, int n_, int K_, int k0_) {
       p = base, ld = ld_, first = first_, n = n_, K = K_, k0 = k0_;
 #pragma unroll
@@ -158,7 +164,7 @@ struct Side {
           if (kCols) {
             if (k0 + r < K) t[i] = fetch_chunk(p + (k0 + r) * ld, static_cast<int>(first) + c, n);
           } else {
-            if (first + r < n) t[i] = fetch_chunk(p + (first + r) * ld, k0 + c, K);
+            if (first + r < n) t[i] = fetch_chunk(p + (first + r) * ld, static_cast<int>(min<int64_t>(k0 + c, K)), K);
           }
         }
       }
@@ -278,12 +284,12 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
   open(id);
   bool whole = false;   // the tile before lay inside C as a whole: each wave issued kStores stores at least for y (and z)
   for (;;) {
-    const int slices = (k1 - k0 + BK - 1) / BK;
+    const int slices = (k1 - k0 - 1) / BK + 1;
     Acc acc[MI][NI] = {};
     // Loads of slice t on their way (in order of t).
     const auto prepare = [&](int t) __attribute__((always_inline)) {
-      const int have = k1 - k0 - t * BK;
-      if (kDirect && have < BK) la.end(have), lb.end(have);
+      const int64_t have = k1 - k0 - static_cast<int64_t>(t) * BK;
+      if (kDirect && have < BK) la.end(static_cast<int>(have)), lb.end(static_cast<int>(have));
     };
     const auto commit = [&](char* lds) __attribute__((always_inline)) {
       la.commit(lds);
@@ -433,11 +439,14 @@ hipError_t launch(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape
   if constexpr (sizeof(T) == 2)
     if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, 2, 16>(a, form, s);
   if (shape.grain == 16)
-    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 16>(a, form, s)
-           : shape.deep      ? launch_tiles<T, 64, 64, 2, 2, 5, 16>(a, form, s)
-                             : launch_tiles<T, 64, 64, 2, 2, 2, 16>(a, form, s);
+    return shape.tile >= 128   ? launch_tiles<T, 128, 128, 2, 2, 2, 16>(a, form, s)
+           : shape.stages == 5 ? launch_tiles<T, 64, 64, 2, 2, 5, 16>(a, form, s)
+           : shape.stages == 3 ? launch_tiles<T, 64, 64, 2, 2, 3, 16>(a, form, s)
+                               : launch_tiles<T, 64, 64, 2, 2, 2, 16>(a, form, s);
   if (shape.grain == 4)
-    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 4>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 4>(a, form, s);
+    return shape.tile >= 128   ? launch_tiles<T, 128, 128, 2, 2, 2, 4>(a, form, s)
+           : shape.stages >= 3 ? launch_tiles<T, 64, 64, 2, 2, 3, 4>(a, form, s)
+                               : launch_tiles<T, 64, 64, 2, 2, 2, 4>(a, form, s);
   return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 0>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 0>(a, form, s);
 }
 

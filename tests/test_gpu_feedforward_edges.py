@@ -269,6 +269,12 @@ def test_offsets_past_32_bits():
     few = etpc.etpc_norm_gate_add_norm(y[-300:], residual=y[-300:])
     assert torch.equal(out[-300:], few[0]) and torch.equal(h[-300:], few[1]) and torch.equal(stats[-300:], few[2])
     del out, h, y
+    note("one row of 33 million results")
+    n = (1 << 25) + 5
+    w = torch.randn(1, n, device="cuda").bfloat16()
+    for v in (w, w.t().contiguous().t()):   # both layouts of [1, n] weights
+        y, _ = etpc.etpc_linear(torch.full((1, 1), 2.0, dtype=torch.bfloat16, device="cuda"), v)
+        assert torch.equal(y, 2 * w)
     note("norm of 4.3 GB")
     g = torch.zeros((1 << 31) + 5, dtype=torch.bfloat16, device="cuda")
     g[-1], g[0] = 4.0, 3.0

@@ -132,7 +132,7 @@ def test_linear(kind, pitch, layout):
 @pytest.mark.parametrize("kind,rows,n_in,n_out,layout", [
     ("bf16", 5000, 64, 64, "io"), ("f16", 20011, 64, 64, "oi"), ("f32", 7001, 64, 64, "io"), ("bf16", 3000, 1024, 520, "oi"),
     ("f16", 4100, 512, 1032, "io"), ("f32", 2100, 264, 1000, "oi"), ("bf16", 30000, 8, 64, "io"), ("f16", 9000, 128, 16, "io"),
-    ("bf16", 8200, 256, 2056, "io"), ("f16", 8200, 1032, 2056, "oi")])
+    ("bf16", 8200, 256, 2056, "io"), ("f16", 8200, 1032, 2056, "oi"), ("f32", 4097, 300, 511, "io"), ("f16", 4098, 264, 520, "oi")])
 def test_linear_many_rows(kind, rows, n_in, n_out, layout):
     """More tiles than compute units, ranges of rows for the weight gradient, tiles that end outside."""
     run_case(rows, rows, n_in, n_out, kind, "silu", layout, 0)
