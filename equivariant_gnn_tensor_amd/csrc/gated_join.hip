@@ -32,6 +32,9 @@ __global__ __launch_bounds__(kCols* kSlices) void parts_kernel(const float* __re
   }
 }
 
+// Parts of the column sums: at least three rows' turns each, no more than are resident at once.  The call's
+// time so, with twice as many and one turn, and with half as many: 4097 x 2047 fp32 59.7, 72.1, 55.3 us;
+// 65408 x 1024 bf16 210, 246, 258.
 struct BwdGroups {
   int32_t rows;
   template <int G>

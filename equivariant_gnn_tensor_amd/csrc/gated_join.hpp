@@ -11,6 +11,11 @@
 // Memory bound, built like the layer norm (layer_norm.hpp): a group of G threads owns a row and
 // keeps it in registers, so the sums of both norms cost no second read; statistics, sums and
 // everything between load and store are fp32, and y comes from the unrounded h.
+// Forward: 65408 x 1024 bf16, five rows moved for each (670 MB), 126 us, 5.3 TB/s, what a copy of that
+// size reaches.  Backward: 4097 x 2047 fp32 (268 MB) 57 us, 4.7 TB/s, and 6.3 us for the second stage of
+// the column sums.  Its five rows and five column sums a thread are the registers; above 4096 columns
+// (a workgroup of 1024 to a row) four of the sums go to LDS: 8192 x 8192 bf16 243 us, 4.4 TB/s (549
+// with the registers spilled), fp32 504 (919).
 #pragma once
 
 #include "activation.hpp"
@@ -155,7 +160,8 @@ struct Row {
 };
 
 // One vector a thread.  Each group walks its rows, fetches the next one's operands ahead and
-// keeps its columns' five sums in registers; at the end the workgroup adds its groups in a fixed
+// keeps its columns' five sums in registers (all but one in LDS where 1024 threads leave 128
+// registers each); at the end the workgroup adds its groups in a fixed
 // order and writes one row of `part`, [5][cols] (or the results, when it is the only workgroup).
 template <class T, int G, bool kEven, bool kGate>
 __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const JoinBwdArgs a) {
@@ -163,7 +169,9 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const JoinBwdArgs
   constexpr bool kWide = sizeof(T) == 4;
   constexpr bool kKeep = G < 1024, kAhead = G < 1024;   // 1024 threads leave 128 registers each
   constexpr int kReduce = G > 64 ? 4 * G / 64 : 0;
+  constexpr bool kLdsSums = G >= 1024;
   __shared__ float lds[kReduce + (kRows > 1 ? 8 * kThreads : 1)];
+  __shared__ float own[kLdsSums ? 4 * 8 * kThreads : 1];   // [sums 1 to 4][2][threads][4], each thread its own
   const int lane = threadIdx.x % G, group = threadIdx.x / G, n = a.cols;
   const Span<G, 1, kEven> span(lane, n);
   const float inv_n = 1.f / static_cast<float>(n);
@@ -178,6 +186,12 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const JoinBwdArgs
     gains();
     span.load_or(a.w2, 0, 1.f, w2);
   }
+  const auto total = [&](int j, int k) -> float& {
+    return kLdsSums && j > 0 ? own[(((j - 1) * 2 + k / 4) * kThreads + threadIdx.x) * 4 + k % 4] : sum[j][k];
+  };
+  if (kLdsSums)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total(1 + i / 8, i % 8) = 0.f;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + norm::group_index<G>();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   Row<T, G, kEven, kGate> next;
@@ -192,8 +206,9 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const JoinBwdArgs
     for (int k = 0; k < 8; ++k) {
       const float y = static_cast<float>(now.y_bar[k]);
       hh[k] = (static_cast<float>(now.h[k]) - now.st[2]) * now.st[3];
-      sum[3][k] = fmaf(y, hh[k], sum[3][k]);
-      sum[4][k] += y;
+      float& s3 = total(3, k);
+      s3 = fmaf(y, hh[k], s3);
+      total(4, k) += y;
       d[k] = y * w2[k];
       const float c = span.counts(0, k) ? d[k] : 0.f;
       s[0] += c;
@@ -217,9 +232,10 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const JoinBwdArgs
       if (kGate) gate_pair<kWide>(static_cast<float>(now.gate[k]), p, q);
       const float m = fmaf(xh[k], w1[k], b1[k]), dp = d[k] * p, u = dp * sc[k];
       gb[k] = u * m * q;
-      sum[2][k] = fmaf(dp, m, sum[2][k]);
+      float& s2 = total(2, k);
+      s2 = fmaf(dp, m, s2);
       sum[0][k] = fmaf(u, xh[k], sum[0][k]);
-      sum[1][k] += u;
+      total(1, k) += u;
       d[k] = u * w1[k];
       const float c = span.counts(0, k) ? d[k] : 0.f;
       s[0] += c;
@@ -234,6 +250,9 @@ __global__ __launch_bounds__(bwd_threads<G>()) void bwd_kernel(const JoinBwdArgs
     span.store(static_cast<T*>(a.x_bar) + row * a.xbs, 0, d);
   }
   if (!a.sums) return;
+  if (kLdsSums)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[1 + i / 8][i % 8] = total(1 + i / 8, i % 8);
   const bool whole = gridDim.x == 1;
 #pragma unroll
   for (int j = 0; j < 5; ++j) {
