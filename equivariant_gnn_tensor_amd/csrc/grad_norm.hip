@@ -3,7 +3,7 @@
 //   norm = sqrt(sum g^2) or max |g|,  g *= min(1, max_norm / (norm + 1e-6))
 //
 // Memory bound: the gradients are read once for the norm, and read and written once more to be
-// clipped.  Pointers and sizes travel in the launch's arguments (no copy to the device, so the
+// clipped (201 M fp32, 805 MB: the norm 137 us, 5.9 TB/s).  Pointers and sizes travel in the launch's arguments (no copy to the device, so the
 // calls can be captured).  The tensors are one long row of units, dealt in equal runs to the
 // workgroups: large and small tensors share the chip evenly, and a workgroup looks for its place
 // once.  Squares are exact in 64 bits and their sums neither overflow nor lose small tensors beside
@@ -201,7 +201,9 @@ NormPlan norm_plan(int32_t n, const int64_t* sizes) {
   for (int32_t k = 0; k < n; ++k) full += sizes[k] > 0;
   NormPlan p{};
   p.launches = static_cast<int32_t>((full + kTensors - 1) / kTensors);
-  p.groups = p.launches > 0 ? std::min(2048, std::max(64, 6144 / p.launches)) : 0;
+  // 201 M fp32 clipped: 140 us with 1024, 143 with 2048 (and a launch between), 145 with 4096; 300 tensors of
+  // 200000 116, 120 and 119
+  p.groups = p.launches > 0 ? std::min(1024, std::max(64, 6144 / p.launches)) : 0;
   int64_t units = 0, held = 0;
   for (int32_t k = 0; k < n; ++k) {
     if (sizes[k] == 0) continue;

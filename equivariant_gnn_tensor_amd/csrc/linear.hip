@@ -16,7 +16,7 @@ constexpr int64_t kMaxGroups = int64_t{1} << 20;
 // ---- z_bar = y_bar act'(z) and its column sums
 // Memory bound: one pass, eight columns a thread, G threads along a row and 256 / G rows at a
 // time.  A workgroup keeps its columns' sums in registers over all its rows and leaves one row
-// of them; they are added up in a fixed order afterwards.
+// of them; they are added up in a fixed order afterwards (65408 x 1024 f16 sums alone 30 us, 4.5 TB/s).
 struct SlopeShape {
   int g;        // threads along a row
   int groups;   // workgroups along a row
@@ -236,22 +236,35 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
   const int64_t bk = 128 / size, slices = (a.K + bk - 1) / bk;
   int64_t splits = 1;
   if (sums) {
-    // one round of the largest tile that C fills, two of the others; at least 512 rows each
-    s.tile = size == 2 && std::min(a.M, a.N) >= 256 ? 256 : std::min(a.M, a.N) > 64 ? 128 : 64;
-    splits = std::min(std::max<int64_t>(1, (s.tile == 256 ? 256 : 512) / tiles(s.tile)), std::max<int64_t>(1, a.K / 512));
+    // One round of the largest tile, two of the others, each workgroup at least 512 rows; where that leaves CUs
+    // without work, the next smaller tile (16384 x 512 -> 512 bf16 37.0 us; 41.2 with the largest), and with
+    // the smallest down to 128 rows (1000 x 776 -> 336 fp32 18.6 us; 69.0 with 128 x 128 and 512 rows).
+    const auto ranges = [&](int64_t side, int64_t least) {
+      return std::min(std::max<int64_t>(1, (side == 256 ? 256 : 512) / tiles(side)), std::max<int64_t>(1, a.K / least));
+    };
+    const int64_t narrow = std::min(a.M, a.N);
+    s.tile = 64;
+    if (size == 2 && narrow >= 256 && tiles(256) * ranges(256, 512) >= 192) s.tile = 256;
+    else if (narrow > 64 && tiles(128) * ranges(128, 512) >= 192) s.tile = 128;
+    splits = ranges(s.tile, s.tile == 64 ? 128 : 512);
   } else {
+    // The largest tile that leaves no CU idle.  bf16: 16384 x 1024 -> 1024 (256 tiles of 256 x 256) 39.5 us
+    // and 44.3 with 128 x 128; 8192 x 1024 -> 1024 (128 of them) 31.8 and 22.9; 2048 x 1024 -> 2048 (256 of
+    // 128 x 128) 15.3 and 18.2 with 64 x 64; 4096 x 2048 -> 512 (128) 26.0 and 20.0.
     s.tile = size == 2 && tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
     // Few tiles and a long k: a tile's products take longer than the second launch that adds ranges of k
-    // (a slice takes a CU about 0.45 us in fp32, 0.3 in 16 bits).
+    // (a slice takes a CU about 0.45 us in fp32, 0.3 in 16 bits; 256 x 4096 -> 256 fp32 24.6 us, 78.6
+    // whole; bf16 15.2 and 25.6).
     if (a.M > kFewRows && tiles(64) <= 128 && slices >= (size == 4 ? 12 : 20)) splits = std::min(512 / tiles(64), slices / 4);
   }
   const int64_t each = (slices + splits - 1) / splits * bk;
   s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));
   s.splits = static_cast<int>((a.K + each - 1) / each);
   if (s.tile == 256 && s.grain != 16) s.tile = 128;
-  // As many slices on their way as LDS holds when every CU has its share of the tiles at once.
-  const int64_t small = tiles(64) * s.splits;
-  s.stages = small <= 512 ? 5 : small <= 768 ? 3 : 2;
+  // A third slice where every CU has all its 64 x 64 tiles at once, three at most, and waits for loads
+  // (2048 x 4096 -> 768 bf16 31.3 us; 36.3 with two); fp32 waits for its products (4096 x 2048 -> 512 80
+  // us with either).
+  s.stages = s.grain == 16 && size == 2 && tiles(64) * s.splits <= 768 ? 3 : 2;
   return s;
 }
 

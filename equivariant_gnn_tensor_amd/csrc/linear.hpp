@@ -27,7 +27,7 @@ struct MatmulShape {
   int tile;        // side of a workgroup's tile
   int grain;       // bytes a lane of the loads straight into LDS (16, 4), or 0: through registers
   int splits, k_split;
-  int stages;      // slices in LDS (more than two: of the 64 x 64 tile)
+  int stages;      // slices in LDS (three: of the 64 x 64 tile of 16 bits)
 };
 // The shape for a product; `sums`: of rows (a weight gradient).  Operands' addresses and strides do not
 // matter to the splits.

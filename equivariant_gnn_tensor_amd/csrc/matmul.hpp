@@ -436,17 +436,14 @@ hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
 
 template <class T>
 hipError_t launch(const MatmulArgs& a, MatmulForm form, const MatmulShape& shape, hipStream_t s) {
-  if constexpr (sizeof(T) == 2)
+  if constexpr (sizeof(T) == 2) {
     if (shape.tile == 256) return launch_tiles<T, 256, 256, 2, 4, 2, 16>(a, form, s);
+    if (shape.tile == 64 && shape.stages == 3) return launch_tiles<T, 64, 64, 2, 2, 3, 16>(a, form, s);
+  }
   if (shape.grain == 16)
-    return shape.tile >= 128   ? launch_tiles<T, 128, 128, 2, 2, 2, 16>(a, form, s)
-           : shape.stages == 5 ? launch_tiles<T, 64, 64, 2, 2, 5, 16>(a, form, s)
-           : shape.stages == 3 ? launch_tiles<T, 64, 64, 2, 2, 3, 16>(a, form, s)
-                               : launch_tiles<T, 64, 64, 2, 2, 2, 16>(a, form, s);
+    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 16>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 16>(a, form, s);
   if (shape.grain == 4)
-    return shape.tile >= 128   ? launch_tiles<T, 128, 128, 2, 2, 2, 4>(a, form, s)
-           : shape.stages >= 3 ? launch_tiles<T, 64, 64, 2, 2, 3, 4>(a, form, s)
-                               : launch_tiles<T, 64, 64, 2, 2, 2, 4>(a, form, s);
+    return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 4>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 4>(a, form, s);
   return shape.tile >= 128 ? launch_tiles<T, 128, 128, 2, 2, 2, 0>(a, form, s) : launch_tiles<T, 64, 64, 2, 2, 2, 0>(a, form, s);
 }
 
