@@ -1241,11 +1241,11 @@ def _c_list(kind, code: str, values):
 
 @functools.lru_cache(maxsize=64)
 def _norm_ws_most(n: int) -> int:
-    """Workspace that is enough for any n tensors: for n large ones, and 2048 partial sums where some of
-    them being empty leaves fewer launches."""
+    """Workspace that is enough for any n tensors: for n large ones, and 6144 partial sums (the most
+    of up to 96 launches), since some of them being empty leaves fewer launches with more workgroups."""
     b = C.c_size_t()
     _check(lib.etpc_grad_norm_workspace_size(n, (C.c_int64 * n)(*[(1 << 46) // max(n, 1 << 16)] * n), b))
-    return max(b.value, 2048 * 8)
+    return max(b.value, 6144 * 8)
 
 
 def _norm_call(grads, ord, norm, ws, stream):

@@ -171,6 +171,13 @@ def test_norm_workspace():
     assert etpc.etpc_grad_norm_workspace_size([1 << 40] * 3) == 8 * 2048
 
 
+@pytest.mark.parametrize("full,empty", [(0, 3), (1, 0), (120, 1), (600, 120), (720, 120), (1080, 130), (11520, 600)])
+def test_norm_scratch(full, empty):
+    """What the binding allocates by the number of tensors alone is enough whichever of them are empty."""
+    sizes = [0] * empty + [1 << 22] * full
+    assert etpc.etpc_grad_norm_workspace_size(sizes) <= etpc._binding._norm_ws_most(full + empty)
+
+
 def test_binding_lists():
     with pytest.raises(ValueError, match="ord"):
         etpc.etpc_grad_norm([torch.zeros(3)], ord=1)
