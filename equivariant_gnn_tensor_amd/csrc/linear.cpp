@@ -62,7 +62,7 @@ size_t product_space(int64_t rows, int64_t k, int64_t cols, int32_t dtype) {
   return splits > 1 ? round256(static_cast<size_t>(splits) * static_cast<size_t>(rows * cols) * sizeof(float)) : 0;
 }
 size_t forward_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
-  return n_in <= narrow::kMost && n_out <= narrow::kMost ? 0 : product_space(rows, n_in, n_out, dtype);
+  return narrow::fits_fwd(rows, n_in, n_out, dtype) ? 0 : product_space(rows, n_in, n_out, dtype);
 }
 
 // A layer's product, split when its shape is.  One or two rows past the last whole tile are left to the
@@ -94,7 +94,7 @@ hipError_t run_product(MatmulArgs a, MatmulForm form, int32_t dtype, void* space
 // The same whatever the layout of w, the addresses and the wanted outputs.
 LinearSpace linear_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype, int32_t act) {
   LinearSpace s{};
-  if (narrow::fits_bwd(n_in, n_out)) {
+  if (narrow::fits_bwd(rows, n_in, n_out, dtype)) {
     s.b_part = round256(static_cast<size_t>(narrow::bwd_groups(rows)) * static_cast<size_t>(n_in * n_out + n_out) * sizeof(float));
     s.bytes = s.b_part;
     return s;
@@ -141,7 +141,7 @@ etpc_status etpc_linear(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dty
   ETPC_TRY(check_apart({{my, n_rows, n_out, size}, {mz, n_rows, n_out, size},
                         {"the workspace", need > 0 ? ws : nullptr, static_cast<int64_t>(need)}},
                        {{mx, n_rows, n_in, size}, operand(mw, size), {mr, n_rows, n_out, size}, ob}));
-  if (n_in <= narrow::kMost && n_out <= narrow::kMost) {
+  if (narrow::fits_fwd(n_rows, n_in, n_out, dtype)) {
     narrow::FwdArgs a{};
     a.x = x, a.w = w, a.b = b, a.res = residual, a.y = y, a.z = z;
     a.xs = x_stride, a.ldw = mw.m.stride, a.ress = residual_stride, a.ys = y_stride, a.zs = z_stride;
@@ -213,7 +213,7 @@ etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, in
                         {mz, n_rows, act != ETPC_ACT_NONE ? n_out : 0, size}}));
   if (!any) return ETPC_OK;
 
-  if (narrow::fits_bwd(n_in, n_out)) {
+  if (narrow::fits_bwd(n_rows, n_in, n_out, dtype)) {
     narrow::BwdArgs a{};
     const bool sums = w_bar != nullptr || b_bar != nullptr;
     a.x = x, a.w = w, a.y_bar = y_bar, a.z = act != ETPC_ACT_NONE ? z : nullptr, a.x_bar = x_bar;

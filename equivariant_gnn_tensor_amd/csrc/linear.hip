@@ -234,6 +234,7 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
                      grain_of(a.b, a.ldb, a.N, a.K, form != MatmulForm::kRowsRows, size));
   const auto tiles = [&](int64_t side) { return ((a.M + side - 1) / side) * ((a.N + side - 1) / side); };
   const int64_t bk = 128 / size, slices = (a.K + bk - 1) / bk;
+  const int64_t narrow = std::min(a.M, a.N);
   int64_t splits = 1;
   if (sums) {
     // One round of the largest tile, two of the others, each workgroup at least 512 rows; where that leaves CUs
@@ -242,7 +243,6 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
     const auto ranges = [&](int64_t side, int64_t least) {
       return std::min(std::max<int64_t>(1, (side == 256 ? 256 : 512) / tiles(side)), std::max<int64_t>(1, a.K / least));
     };
-    const int64_t narrow = std::min(a.M, a.N);
     s.tile = 64;
     if (size == 2 && narrow >= 256 && tiles(256) * ranges(256, 512) >= 192) s.tile = 256;
     else if (narrow > 64 && tiles(128) * ranges(128, 512) >= 192) s.tile = 128;
@@ -250,8 +250,9 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
   } else {
     // The largest tile that leaves no CU idle.  bf16: 16384 x 1024 -> 1024 (256 tiles of 256 x 256) 39.5 us
     // and 44.3 with 128 x 128; 8192 x 1024 -> 1024 (128 of them) 31.8 and 22.9; 2048 x 1024 -> 2048 (256 of
-    // 128 x 128) 15.3 and 18.2 with 64 x 64; 4096 x 2048 -> 512 (128) 26.0 and 20.0.
-    s.tile = size == 2 && tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
+    // 128 x 128) 15.3 and 18.2 with 64 x 64; 4096 x 2048 -> 512 (128) 26.0 and 20.0.  None that a narrow
+    // C would leave half empty (65536 x 512 -> 64 15.1 and 22.7 with 256 x 256, fp32 43.4 and 76.8 with 128 x 128).
+    s.tile = size == 2 && narrow > 128 && tiles(256) >= 256 ? 256 : narrow > 64 && tiles(128) >= 256 ? 128 : 64;
     // Few tiles and a long k: a tile's products take longer than the second launch that adds ranges of k
     // (a slice takes a CU about 0.45 us in fp32, 0.3 in 16 bits; 256 x 4096 -> 256 fp32 24.6 us, 78.6
     // whole; bf16 15.2 and 25.6).

@@ -386,7 +386,6 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
 }
 
 // ---------------------------------------------------------------- launches
-inline int tiles_of(int n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; }
 
 // As many workgroups as are resident, fewer where that gives every wave the same number of tiles
 // (214980 x 64 -> 64 bf16: 24.1 us with four a CU where three are resident, 21.1 with three).
@@ -424,8 +423,7 @@ hipError_t forward(const FwdArgs& a, bool even, hipStream_t s) {
     case 18: return launch_fwd<T, 2, 2>(a, even, s);
     case 20: return launch_fwd<T, 2, 4>(a, even, s);
     case 33: return launch_fwd<T, 4, 1>(a, even, s);
-    case 34: return launch_fwd<T, 4, 2>(a, even, s);
-    default: return launch_fwd<T, 4, 4>(a, even, s);
+    default: return launch_fwd<T, 4, 2>(a, even, s);
   }
 }
 template <class T>

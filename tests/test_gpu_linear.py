@@ -136,3 +136,13 @@ def test_linear(kind, pitch, layout):
 def test_linear_many_rows(kind, rows, n_in, n_out, layout):
     """More tiles than compute units, ranges of rows for the weight gradient, tiles that end outside."""
     run_case(rows, rows, n_in, n_out, kind, "silu", layout, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,n_in,n_out,layout,pitch", [
+    (65537, 64, 64, "io", 0), (65570, 128, 32, "oi", 8), (65600, 32, 128, "io", 5), (65551, 100, 60, "oi", 0),
+    (65569, 60, 100, "io", 8), (65539, 33, 65, "oi", 5), (65568, 127, 64, "io", 0), (65536, 64, 64, "oi", 0),
+    (65537, 128, 128, "io", 0), (66000, 17, 127, "oi", 0), (32769, 64, 64, "oi", 5), (32768, 128, 32, "io", 0)])
+def test_linear_narrow_many_rows(kind, rows, n_in, n_out, layout, pitch):
+    """On either side of where a narrow layer's rows are enough for a kernel that keeps its weights in LDS."""
+    run_case(rows, rows, n_in, n_out, kind, ff.ACTS[1 + (n_in + n_out) % 4], layout, pitch)
