@@ -10,7 +10,8 @@
 //   across: weights contiguous in n.  Eight lanes take 128 bytes of n of one k, a wave eight k and a
 //           workgroup 128; the sums are added over lanes, then over waves in LDS.
 // fp32 sums in a fixed order.  From three rows on the tiles of matmul.hpp are faster (eight rows of 4096 ->
-// 4096 bf16: 56 and 74 us here, along and across, where conversions and multiply-adds count; 14 there).  1 x 1024 -> 1024 fp32 (4 MB of weights, across): 4.6 us.
+// 4096 bf16: 56 and 74 us here, along and across, where conversions and multiply-adds count; 14 there).  1 x 1024 -> 1024
+// fp32 (4 MB of weights, across): 4.6 us.
 #pragma once
 
 #include "activation.hpp"

@@ -1,4 +1,4 @@
-// The dense layer between narrow rows (up to 128 numbers), forward and backward (templates; narrow_*.hip
+// The dense layer between narrow rows (up to 128 numbers, see fits_fwd and fits_bwd), forward and backward (templates; narrow_*.hip
 // hold the instantiations of one element type each).
 //
 //   forward:  z = x w + b, y = act(z) + residual
@@ -15,6 +15,10 @@
 // transposed.  w_bar's and b_bar's sums stay in registers over all of a wave's rows, are added up
 // over the workgroup's waves in LDS and leave one partial sum a workgroup, added in a fixed order
 // by a second launch.
+//
+// 214980 x 64 -> 64 bf16 silu: forward 21.6 us a call (82.6 MB, 3.8 TB/s; half of a wave's cycles are
+// waits), backward 42 (110 MB; 39.5 and the second launch), bound by conversions, slopes and the way
+// through LDS.
 #pragma once
 
 #include <algorithm>
