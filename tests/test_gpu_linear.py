@@ -146,3 +146,11 @@ def test_linear_many_rows(kind, rows, n_in, n_out, layout):
 def test_linear_narrow_many_rows(kind, rows, n_in, n_out, layout, pitch):
     """On either side of where a narrow layer's rows are enough for a kernel that keeps its weights in LDS."""
     run_case(rows, rows, n_in, n_out, kind, ff.ACTS[1 + (n_in + n_out) % 4], layout, pitch)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 300, 2100), (2, 2300, 4200), (1, 130, 8200), (2, 2049, 2048), (1, 17, 515)])
+def test_linear_one_or_two_rows(kind, rows, n_in, n_out):
+    """Either width of a workgroup's outputs, more inputs than one pass holds."""
+    for layout in ("io", "oi"):
+        run_case(rows + n_out, rows, n_in, n_out, kind, "silu", layout, 0)
