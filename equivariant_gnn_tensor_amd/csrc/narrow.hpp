@@ -12,7 +12,10 @@
 //
 // The backward pass is one kernel: z_bar is a fragment for x_bar as it stands; for w_bar, whose
 // contraction runs over rows, it and x go through a few KB of LDS of the wave and are read
-// transposed.  w_bar's and b_bar's sums stay in registers over all of a wave's rows, are added up
+// transposed.  The matrix cores take 16-bit numbers of z_bar, so it goes into both products as the
+// sum of two of them, the rounded one and what that leaves (2^-16 of z_bar in bf16, 2^-22 in fp16): one rounding
+// alone takes w_bar from 0.0017 to 0.0023 off (root mean square, bf16; the rounding of w_bar itself is 0.0017) and
+// saves 1.5 of 40 us.  w_bar's and b_bar's sums stay in registers over all of a wave's rows, are added up
 // over the workgroup's waves in LDS and leave one partial sum a workgroup, added in a fixed order
 // by a second launch.
 //
@@ -227,13 +230,15 @@ constexpr int bwd_threads() {
   return sizeof(T) == 4 ? 256 : 512;
 }
 
-template <class T, int IT, int OT, bool kEven>
+// kSlope: there is an activation, so z_bar is not y_bar.
+template <class T, int IT, int OT, bool kEven, bool kSlope>
 __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int SI = steps<T>(IT), SO = steps<T>(OT), kWaves = bwd_threads<T>() / 64, E = 16 / sizeof(T);
   constexpr int kRows = 32 * IT;
   constexpr int CI = 2 * SI < 8 ? 8 : 2 * SI, CO = 2 * SO < 8 ? 8 : 2 * SO;   // chunks of a row in LDS
-  constexpr int kWeights = slices<T>(OT) * kRows * 128, kTile = 32 * 16 * (CI + CO);
+  constexpr int kParts = sizeof(T) == 2 && kSlope ? 2 : 1;   // numbers that z_bar is the sum of
+  constexpr int kWeights = slices<T>(OT) * kRows * 128, kTile = 32 * 16 * (CI + kParts * CO);
   constexpr int kSums = IT * OT * 32 * 32 + OT * 32;   // numbers of a partial sum (padded)
   constexpr int kTiles = kTile * kWaves, kHalf = kSums * 4 * (kWaves / 2);
   __shared__ __attribute__((aligned(16))) char w[kWeights];
@@ -251,7 +256,7 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
   const auto read = [&](int64_t t) __attribute__((always_inline)) {
     const int64_t r = min(t * 32 + (lane & 31), static_cast<int64_t>(a.rows) - 1);
     next.y_bar.read(a.y_bar, r * a.ybs, a.n_out, h);
-    if (a.z != nullptr) next.z.read(a.z, r * a.zs, a.n_out, h);
+    if (kSlope) next.z.read(a.z, r * a.zs, a.n_out, h);
     if (w_sums) next.x.read(a.x, r * a.xs, a.n_in, h);
   };
   if (tile < tiles) read(tile);
@@ -260,38 +265,90 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
   __syncthreads();
   Acc wb[IT][OT] = {};
   float bb[SO][E] = {};   // sums over this lane's rows of its chunks
+  const int first_lane = lane;
   for (; tile < tiles; tile += step) {
+    // Four tiles of w_bar leave no registers for addresses in LDS, which would be kept and spilled: they are
+    // computed again for each 32 rows (214980 x 64 -> 64 bf16 silu 40 us; 47 with 12 registers spilled).
+    int lane = first_lane;
+    if (sizeof(T) == 2 && IT * OT > 2) asm volatile("" : "+v"(lane));
+    const int h = lane >> 5;
     const Rows now = next;
-    if (tile + step < tiles) read(tile + step);
-    asm volatile("" ::: "memory");   // the weights stay in LDS
+    if (sizeof(T) == 4 && tile + step < tiles) read(tile + step);
+    // A row past the end is the last one again: cleared, as it may hold infinities, and counted as zero.
     const bool row = tile * 32 + (lane & 31) < a.rows;
-    Chunk zb[SO];
+    if (w_sums) {
+#pragma unroll
+      for (int s = 0; s < SI; ++s) *reinterpret_cast<Chunk*>(xt + tile_at<T, CI>(lane & 31, 2 * s + h)) = row ? now.x.c[s] : Chunk{};
+    }
 #pragma unroll
     for (int s = 0; s < SO; ++s) {
-      T e[E], ez[E];
-      float v[E], z[E];
-      __builtin_memcpy(e, &now.y_bar.c[s], 16);
+      const Chunk y = row ? now.y_bar.c[s] : Chunk{};
+      T e[E];
+      float v[E];
+      __builtin_memcpy(e, &y, 16);
 #pragma unroll
-      for (int k = 0; k < E; ++k) v[k] = row ? static_cast<float>(e[k]) : 0.f;   // rows past the end count as zero
-      if (a.z != nullptr) {
-        __builtin_memcpy(ez, &now.z.c[s], 16);
+      for (int k = 0; k < E; ++k) v[k] = static_cast<float>(e[k]);
+      if (kSlope) {
+        const Chunk c = row ? now.z.c[s] : Chunk{};
+        T ez[E];
+        float z[E];
+        __builtin_memcpy(ez, &c, 16);
 #pragma unroll
-        for (int k = 0; k < E; ++k) z[k] = row ? static_cast<float>(ez[k]) : 0.f;
+        for (int k = 0; k < E; ++k) z[k] = static_cast<float>(ez[k]);
         times_slope<sizeof(T) == 4>(v, z, a.act);
       }
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        bb[s][k] += v[k];
-        e[k] = static_cast<T>(v[k]);
+      for (int k = 0; k < E; ++k) bb[s][k] += v[k];
+      if constexpr (kParts == 2) {
+        // The first part is kept finite: the rest alone holds an infinity or a NaN, and what fp16 overflows by.
+        constexpr float kTop = __is_same(T, F16) ? 65504.f : 3.3895314e38f;
+        T rest[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          e[k] = static_cast<T>(__builtin_amdgcn_fmed3f(v[k], -kTop, kTop));
+          rest[k] = static_cast<T>(v[k] - static_cast<float>(e[k]));
+        }
+        Chunk t;
+        __builtin_memcpy(&t, rest, 16);
+        *reinterpret_cast<Chunk*>(zt + 32 * 16 * CO + tile_at<T, CO>(lane & 31, 2 * s + h)) = t;
+      } else if (kSlope) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) e[k] = static_cast<T>(v[k]);
       }
-      __builtin_memcpy(&zb[s], e, 16);
+      Chunk t;
+      __builtin_memcpy(&t, e, 16);
+      *reinterpret_cast<Chunk*>(zt + tile_at<T, CO>(lane & 31, 2 * s + h)) = t;
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (sizeof(T) == 2 && tile + step < tiles) read(tile + step);   // there were no registers for it before
+    asm volatile("" ::: "memory");   // the weights stay in LDS
+    if (a.x_bar != nullptr) {
+      const int64_t m = tile * 32 + (lane & 31);
+      Acc acc[IT] = {};
+#pragma unroll
+      for (int s = 0; s < SO; ++s) {
+        Chunk z[kParts];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) z[p] = *reinterpret_cast<const Chunk*>(zt + p * 32 * 16 * CO + tile_at<T, CO>(lane & 31, 2 * s + h));
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const Chunk f = *reinterpret_cast<const Chunk*>(w + weight_at(kRows, 32 * i + (lane & 31), 2 * s + h));
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) acc[i] = mm::multiply<T>(f, z[p], acc[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {   // stored as they are: turned over like the forward pass 45.6 us, so 38.3
+          const int n = 32 * i + 16 * g + 8 * h;
+          float v[8];
+          eight(acc[i], g, v);
+          if (row && n < a.n_in) store<8, false>(static_cast<T*>(a.x_bar) + m * a.xbs, n, a.n_in, v);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     if (w_sums) {
-      // a row past the end repeats the last one's x, against zeros of z_bar: cleared, as it may hold infinities
-#pragma unroll
-      for (int s = 0; s < SI; ++s) *reinterpret_cast<Chunk*>(xt + tile_at<T, CI>(lane & 31, 2 * s + h)) = row ? now.x.c[s] : Chunk{};
-#pragma unroll
-      for (int s = 0; s < SO; ++s) *reinterpret_cast<Chunk*>(zt + tile_at<T, CO>(lane & 31, 2 * s + h)) = zb[s];
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int s = 0; s < static_cast<int>(sizeof(T)); ++s) {
@@ -299,32 +356,16 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
 #pragma unroll
         for (int i = 0; i < IT; ++i) fx[i] = column_fragment<T, CI>(xt, 32 * i, s, lane);
 #pragma unroll
-        for (int o = 0; o < OT; ++o) fz[o] = column_fragment<T, CO>(zt, 32 * o, s, lane);
+        for (int p = 0; p < kParts; ++p) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
+          for (int o = 0; o < OT; ++o) fz[o] = column_fragment<T, CO>(zt + p * 32 * 16 * CO, 32 * o, s, lane);
 #pragma unroll
-          for (int o = 0; o < OT; ++o) wb[i][o] = mm::multiply<T>(fz[o], fx[i], wb[i][o]);
+          for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int o = 0; o < OT; ++o) wb[i][o] = mm::multiply<T>(fz[o], fx[i], wb[i][o]);
+        }
       }
       __builtin_amdgcn_wave_barrier();
-    }
-    if (a.x_bar != nullptr) {
-      const int64_t m = tile * 32 + (lane & 31);
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        Acc acc = {};
-#pragma unroll
-        for (int s = 0; s < SO; ++s) {
-          const Chunk f = *reinterpret_cast<const Chunk*>(w + weight_at(kRows, 32 * i + (lane & 31), 2 * s + h));
-          acc = mm::multiply<T>(f, zb[s], acc);
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {   // stored as they are: turned over like the forward pass 45.6 us, so 38.3
-          const int n = 32 * i + 16 * g + 8 * h;
-          float v[8];
-          eight(acc, g, v);
-          if (row && n < a.n_in) store<8, false>(static_cast<T*>(a.x_bar) + m * a.xbs, n, a.n_in, v);
-        }
-      }
     }
   }
   if (!sums) return;
@@ -412,8 +453,14 @@ hipError_t launch_fwd(const FwdArgs& a, bool even, hipStream_t s) {
 }
 template <class T, int IT, int OT>
 hipError_t launch_bwd(const BwdArgs& a, bool even, int groups, hipStream_t s) {
-  if (even) bwd_kernel<T, IT, OT, true><<<dim3(groups), dim3(bwd_threads<T>()), 0, s>>>(a);
-  else bwd_kernel<T, IT, OT, false><<<dim3(groups), dim3(bwd_threads<T>()), 0, s>>>(a);
+  const dim3 grid(groups), block(bwd_threads<T>());
+  if (a.z != nullptr) {
+    if (even) bwd_kernel<T, IT, OT, true, true><<<grid, block, 0, s>>>(a);
+    else bwd_kernel<T, IT, OT, false, true><<<grid, block, 0, s>>>(a);
+  } else {
+    if (even) bwd_kernel<T, IT, OT, true, false><<<grid, block, 0, s>>>(a);
+    else bwd_kernel<T, IT, OT, false, false><<<grid, block, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

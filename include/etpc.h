@@ -452,9 +452,10 @@ etpc_status etpc_linear_backward_workspace_size(int64_t n_rows, int64_t n_in, in
                                                 size_t* bytes);
 /* Gradients of <y_bar, y>: with z_bar = y_bar act'(z), x_bar = z_bar w^T, w_bar = x^T z_bar and
  * b_bar = the column sums of z_bar; the residual's is y_bar itself.  x_bar and w_bar have the
- * rows' type (z_bar is rounded to it where it enters their products), b_bar is fp32, summed from
- * z_bar before that.  w_bar's strides are its own.  z may be NULL when act is ETPC_ACT_NONE, x
- * when w_bar is, w when x_bar is; a NULL output is skipped.  Sums over rows have a fixed order. */
+ * rows' type, b_bar is fp32, summed from the unrounded z_bar.  16-bit rows past 64 inputs and 64
+ * outputs (or 128 and 32) round z_bar to their type where it enters the two products.  w_bar's
+ * strides are its own.  z may be NULL when act is ETPC_ACT_NONE, x when w_bar is, w when x_bar is;
+ * a NULL output is skipped.  Sums over rows have a fixed order. */
 etpc_status etpc_linear_backward(int64_t n_rows, int64_t n_in, int64_t n_out, int32_t dtype, const void* x,
                                  int64_t x_stride, const void* w, int64_t w_in_stride, int64_t w_out_stride,
                                  const void* y_bar, int64_t y_bar_stride, const void* z, int64_t z_stride, int32_t act,
