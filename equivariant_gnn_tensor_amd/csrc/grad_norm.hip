@@ -55,8 +55,11 @@ __device__ inline void for_run(const Table& a, F&& f) {
   }
 }
 
+// f(first element, eight numbers) for each vector of a part, zeros past its end.  A thread reads its own
+// elements only, and f may write them (p is not __restrict__): clipping works in place, and the neighbours'
+// are being written by other waves.
 template <class T, class F>
-__device__ inline void for_vectors(const T* __restrict__ p, int64_t n, F&& f) {
+__device__ inline void for_vectors(const T* p, int64_t n, F&& f) {
   int64_t c = 8 * threadIdx.x;
   for (; c + 8 * kThreads * (kUnroll - 1) + 8 <= n; c += 8 * kThreads * kUnroll) {
     float v[kUnroll][8];
@@ -65,10 +68,9 @@ __device__ inline void for_vectors(const T* __restrict__ p, int64_t n, F&& f) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) f(c + i * 8 * kThreads, v[i]);
   }
-  for (; c < n; c += 8 * kThreads) {   // the last vector of a part shorter than eight goes by elements
-    const int64_t at = c + 8 <= n || n < 8 ? c : n - 8;
+  for (; c < n; c += 8 * kThreads) {
     float v[8];
-    load<8, false>(p + at, static_cast<int>(c - at), static_cast<int>(min(n - at, int64_t{8})), v);
+    load_own<8>(p + c, static_cast<int>(min(n - c, int64_t{8})), v);
     f(c, v);
   }
 }
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const double* __restri
 
 template <class T>
 __device__ inline void scale_piece(const T* p, T* out, int64_t n, float by) {
-  // in place: a thread reads a vector before it writes it, and no other thread's
+  // in place: a thread reads a vector before it writes it
   for_vectors(p, n, [&](int64_t c, float (&v)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= by;

@@ -57,6 +57,18 @@ __device__ inline void load(const T* __restrict__ p, int c, int n, float (&v)[N]
   settle<N, kEven, T>(fetch<N, kEven>(p, c, n), c, n, v);
 }
 
+// N elements of which `left` are the thread's own (zeros past them): for calls in place, where the elements
+// before a row's last vector are being written by their own threads.
+template <int N, class T>
+__device__ inline void load_own(const T* p, int left, float (&v)[N]) {
+  if (left >= N) {
+    load<N, true>(p, 0, N, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = k < left ? static_cast<float>(p[k]) : 0.f;
+  }
+}
+
 // Rounds to the element type here, once (to nearest, ties to even).  The end of a row goes
 // out as at most three stores, of four, two and one elements.
 template <int N, bool kEven, class T>

@@ -143,3 +143,22 @@ def test_dense_layouts():
         etpc.etpc_grad_norm([torch.randn(8, 8, device="cuda")[:, :4]])
     with pytest.raises(etpc.EtpcError, match="overlap"):
         etpc.etpc_clip_grad_norm([before[0], before[0]], 1.0)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_ends_in_place(kind):
+    """In place the same bits as into other tensors, wherever the last vector of a tensor ends and whichever wave has it."""
+    etpc = _etpc()
+    rng = np.random.default_rng(13)
+    sizes = [base + end for base in (0, 8, 512, 2040, 2048, 8184) for end in range(8) if base + end]
+    grads = tensors(rng, sizes, [kind], shift=1)
+    before = [g.clone() for g in grads]
+    outs = [torch.zeros_like(g) for g in grads]
+    ref = ff.grad_norm([f64(g) for g in grads])
+    for _ in range(5):
+        for g, b in zip(grads, before):
+            g.copy_(b)
+        check_norm(etpc.etpc_clip_grad_norm(grads, 0.3 * ref, outs=outs), ref)
+        check_norm(etpc.etpc_clip_grad_norm(grads, 0.3 * ref), ref)
+        assert all(torch.equal(g, o) for g, o in zip(grads, outs))
+    check_clipped(grads, before, ref, 0.3 * ref)
