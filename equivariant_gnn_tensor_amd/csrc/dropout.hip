@@ -39,9 +39,11 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const T* x, int64_t x
     const uint32_t vec = left - q * static_cast<uint32_t>(vecs.div);
     const int64_t row = static_cast<int64_t>(row0 + q);
     float v[8];
-    load<8, kEven>(x + row * xs, static_cast<int>(8 * vec), cols, v);
+    const int c = static_cast<int>(8 * vec);
+    if (!kEven && x == y) load_own<8>(x + row * xs + c, cols - c, v);
+    else load<8, kEven>(x + row * xs, c, cols, v);
     if (d.threshold != 0) drop8(v, philox(vec, static_cast<uint32_t>(row), offset, d.seed), d.threshold, d.scale);
-    store<8, kEven>(y + row * ys, static_cast<int>(8 * vec), cols, v);
+    store<8, kEven>(y + row * ys, c, cols, v);
   }
 }
 
@@ -55,7 +57,10 @@ __device__ inline void drop_block(const float* x, float* y, int mul, int c, uint
                                   const DropArgs& d) {
   float v[D][4];
 #pragma unroll
-  for (int m = 0; m < D; ++m) load<4, kEven>(x + m * mul, c, mul, v[m]);
+  for (int m = 0; m < D; ++m) {
+    if (!kEven && x == y) load_own<4>(x + m * mul + c, mul - c, v[m]);
+    else load<4, kEven>(x + m * mul, c, mul, v[m]);
+  }
   const bool keep[4] = {(w0 & 0xFFFFu) >= d.threshold, (w0 >> 16) >= d.threshold, (w1 & 0xFFFFu) >= d.threshold,
                         (w1 >> 16) >= d.threshold};
 #pragma unroll

@@ -92,3 +92,29 @@ def test_join_backward_of_rows_from_odd_elements(kind, cols, odd):
     close(xb, nw.dropout(rx, p, seed, off), scale * (err + U * np.abs(rx)), "x_bar", kind)
     plain = etpc.etpc_layer_norm_backward(h, yb, mean, rstd, w)
     check_backward(*plain, f64(h), f64(yb), f64(mean), f64(rstd), f64(w), kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("cols", [1, 7, 9, 513, 577, 2047, 2049])
+def test_dropout_in_place_is_dropout(kind, cols):
+    """In place the same bits, wherever a row's last vector ends and whichever wave has it."""
+    etpc = _etpc()
+    rng = np.random.default_rng(cols)
+    first = rows(rng, 311, cols, kind, pitch=cols + 2)
+    want = etpc.etpc_dropout(first, 0.3, 5, 6)
+    for _ in range(5):
+        x = first.clone()
+        etpc.etpc_dropout(x, 0.3, 5, 6, y=x)
+        assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("irreps", ["5x0e", "1x0e+3x1o+6x2e", "131x1o+257x0e", "7x3o+1023x0o"])
+def test_irreps_dropout_in_place_is_dropout(irreps):
+    etpc = _etpc()
+    rng = np.random.default_rng(3)
+    first = tensor(rng.standard_normal((211, etpc.etpc_irreps_dims(irreps)["dim"])))
+    want = etpc.etpc_irreps_dropout(irreps, first, 0.3, 5, 6)
+    for _ in range(5):
+        x = first.clone()
+        etpc.etpc_irreps_dropout(irreps, x, 0.3, 5, 6, y=x)
+        assert torch.equal(x, want)
