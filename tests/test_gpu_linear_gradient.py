@@ -7,10 +7,11 @@ products as a rounded number and the rounded rest: off by half a step of the res
 import numpy as np
 import pytest
 import torch
+from scipy import special
 
 from oracle import feedforward as ff
 from tests.gpu_helpers import note
-from tests.test_gpu_linear import DTYPES, HALF, LEAST, U, close, f64, matrix, steps, weights
+from tests.test_gpu_linear import DTYPES, HALF, KINDS, LEAST, U, close, f64, matrix, steps, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,32 @@ def test_narrow_gradient_past_fp16():
         keep = [k for k in range(n_out) if k != 2]
         assert torch.isneginf(w_bar[:, 2]).all() and torch.isfinite(w_bar[:, keep]).all()
         assert torch.isneginf(b_bar[2]) and torch.isfinite(b_bar[keep]).all()
+
+
+def terms(z, act):
+    """Magnitudes that the slope is the sum of: an error relative to them is one that does not come from cancelling."""
+    if act == "tanh":
+        return ff.slope(z, act)
+    if act == "silu":
+        p = special.expit(z)
+        return p + np.abs(z) * p * special.expit(-z)
+    return special.ndtr(z) + np.abs(z) * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "tanh"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_in", [8, 200])
+def test_slopes_far_out(kind, act, n_in):
+    """b_bar of one row is y_bar act'(z), unrounded: relative errors over all of z's useful range, between narrow rows
+    and wider ones.  exp's argument is off by 2 u of itself (2 |z|, |z|, z^2 / 2) and its functions by some u."""
+    etpc = _etpc()
+    z = torch.arange(-96, 97, device="cuda") / 8.0
+    for rows in (1, 40):
+        cols = (z if n_in > 128 else z[::4]).contiguous().to(DTYPES[kind])
+        zs = cols.expand(rows, -1)
+        x = torch.zeros(rows, n_in, dtype=DTYPES[kind], device="cuda")
+        w = torch.zeros(n_in, cols.numel(), dtype=DTYPES[kind], device="cuda")
+        _, _, b_bar = etpc.etpc_linear_backward(x, w, torch.full_like(zs, 0.5).contiguous(), z=zs, act=act)
+        v = f64(cols)
+        bound = U * (32 + 4 * np.abs(v) + 4 * v * v * (act == "gelu")) * terms(v, act) + steps(rows) * np.abs(ff.slope(v, act))
+        close(b_bar / (0.5 * rows), ff.slope(v, act), bound, "slope")
