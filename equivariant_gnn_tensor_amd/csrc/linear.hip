@@ -261,7 +261,7 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
     if (a.M > kFewRows && tiles(64) <= 128 && slices >= (size == 4 ? 12 : 20)) splits = std::min(512 / tiles(64), slices / 4);
   }
   const int64_t each = (slices + splits - 1) / splits * bk;
-  s.k_split = static_cast<int>(std::min<int64_t>(each, (int64_t{1} << 31) - 128));
+  s.k_split = static_cast<int>(std::min<int64_t>(each, a.K));
   s.splits = static_cast<int>((a.K + each - 1) / each);
   if (s.tile == 256 && s.grain != 16) s.tile = 128;
   // A third slice where every CU has all its 64 x 64 tiles at once, three at most, and waits for loads

@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
     int tm, tn;
     place_tile(id - split * per, a.tiles_m, a.tiles_n, tm, tn);
     m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BN;
-    k0 = split * a.k_split, k1 = min(a.K, k0 + a.k_split);
+    k0 = split * a.k_split, k1 = a.K - k0 < a.k_split ? a.K : k0 + a.k_split;
     la.start(static_cast<const T*>(a.a), a.lda, m0, a.M, a.K, k0);
     lb.start(static_cast<const T*>(a.b), a.ldb, n0, a.N, a.K, k0);
     if (kDirect && k1 - k0 < BK) la.end(k1 - k0), lb.end(k1 - k0);
