@@ -280,3 +280,26 @@ def test_offsets_past_32_bits():
     g[-1], g[0] = 4.0, 3.0
     assert float(etpc.etpc_clip_grad_norm([g], 2.5)) == 5.0
     assert float(g[-1]) == 2.0 and float(g[0]) == 1.5
+
+
+def test_most_rows():
+    """2^31 - 1 rows: tile numbers and ends of the ranges of rows within their types (x and y_bar are one row for all)."""
+    etpc = _etpc()
+    rows = (1 << 31) - 1
+    rng = np.random.default_rng(14)
+    note("layer of 2^31 - 1 rows to one output")
+    one, w = matrix(rng, 1, 200, "bf16"), weights(rng, 200, 1, "bf16", "io")
+    y, _ = etpc.etpc_linear(one.expand(rows, 200), w)
+    few = etpc.etpc_linear(one.expand(3, 200), w)[0]
+    assert bool((y == y[0]).all())
+    check_forward(y[-3:], None, f64(one.expand(3, 200)), f64(w), np.zeros(1), None, "none", "bf16")
+    assert torch.equal(y[:3], y[-3:]) and y.shape == (rows, 1) and few.shape == (3, 1)
+    del y
+    note("weight gradient over 2^31 - 1 rows")
+    x = torch.ones(1, 130, dtype=torch.bfloat16, device="cuda").expand(rows, 130)
+    y_bar = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda").expand(rows, 1)
+    w = torch.ones(130, 1, dtype=torch.bfloat16, device="cuda")
+    _, w_bar, b_bar = etpc.etpc_linear_backward(x, w, y_bar, want=("w", "b"))
+    # whole numbers up to 2^24 in a range are exact; the sums of up to 1024 ranges round once each
+    assert float((w_bar.double() / rows - 1).abs().max()) <= 2.0 ** -8 + 1024 * 2.0 ** -24
+    assert abs(float(b_bar) / rows - 1) <= 1024 * 2.0 ** -24
