@@ -65,9 +65,29 @@ size_t forward_space(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
   return narrow::fits_fwd(rows, n_in, n_out, dtype) ? 0 : product_space(rows, n_in, n_out, dtype);
 }
 
-// A layer's product, split when its shape is.  One or two rows past the last whole tile are left to the
-// kernel for few rows where they would cost some CUs one tile more than all others have (4097 x 2047
-// -> 511 fp32: 65 x 8 tiles on 256 CUs are three rounds instead of two; 112 us with them, 96 without; 83 now, of which the last row takes 7).
+// Whether one or two rows past the last whole tile are better left to the kernel for few rows (from three on
+// it is slower than a tile).  They are where some CUs would work one tile longer because of them, for
+// longer than that kernel's launch takes.  fp32 tiles are bound by a CU's matrix cores, so tiles that are resident
+// together count one after another; 16-bit ones overlap.  A slice of a 64 x 64 tile is 0.45 us of a CU in fp32,
+// 0.07 in 16 bits.  150 sizes with a remainder of one or two rows, with and without: 4097 x 2047 -> 511 fp32 80 us
+// and 104, 16386 x 1024 -> 136 77 and 124, 4097 x 512 -> 256 17.5 and 20.9, 8194 x 256 -> 256 18 and 18, 6146 x
+// 136 -> 512 18.6 and 16.6; 8193 x 2048 -> 2048 bf16 70 and 95, 16385 x 256 -> 2048 33 and 37, 16385 x 64 -> 2048 25 and
+// 25, and 8194 x 4096 -> 512, whose tiles are all resident, 60 and 53.
+bool rows_apart(const MatmulArgs& a, const MatmulShape& shape, int32_t dtype) {
+  const int32_t over = a.M % shape.tile;
+  if (over == 0 || over > kFewRows || a.M == over) return false;
+  const int64_t across = (a.N + shape.tile - 1) / shape.tile, down = a.M / shape.tile;
+  const int64_t resident = matmul_resident(shape.tile, shape.stages);
+  const auto rounds = [&](int64_t tiles) {
+    const int64_t all = (tiles + kCus * resident - 1) / (kCus * resident);
+    return dtype != ETPC_F32 ? all : all > 1 ? all * resident : (tiles + kCus - 1) / kCus;
+  };
+  const double side = shape.tile / 64, slices = static_cast<double>(a.K) * static_cast<double>(size_of(dtype)) / 128;
+  const double round = slices * side * side * (dtype == ETPC_F32 ? 0.45 : 0.07);
+  return static_cast<double>(rounds((down + 1) * across) - rounds(down * across)) * round > 4.0;
+}
+
+// A layer's product, split when its shape is.
 hipError_t run_product(MatmulArgs a, MatmulForm form, int32_t dtype, void* space, hipStream_t s) {
   const MatmulShape shape = matmul_shape(a, form, dtype, false);
   if (shape.splits > 1) {
@@ -76,10 +96,8 @@ hipError_t run_product(MatmulArgs a, MatmulForm form, int32_t dtype, void* space
     a.splits = shape.splits;
     return e != hipSuccess ? e : launch_layer_parts(a, dtype, s);
   }
+  if (!rows_apart(a, shape, dtype)) return launch_matmul(a, form, dtype, shape, s);
   const int32_t over = a.M % shape.tile, whole = a.M - over;
-  const int64_t across = (a.N + shape.tile - 1) / shape.tile, down = whole / shape.tile;
-  if (over == 0 || over > kFewRows || whole == 0 || (down * across + 255) / 256 == ((down + 1) * across + 255) / 256)
-    return launch_matmul(a, form, dtype, shape, s);
   const int64_t size = size_of(dtype);
   const auto from = [&](const void* p, int64_t stride) { return p == nullptr ? p : static_cast<const char*>(p) + whole * stride * size; };
   MatmulArgs rest = a;

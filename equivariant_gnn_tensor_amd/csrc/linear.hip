@@ -267,7 +267,7 @@ MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool s
   // A third slice where every CU has all its 64 x 64 tiles at once, three at most, and waits for loads
   // (2048 x 4096 -> 768 bf16 31.3 us; 36.3 with two); fp32 waits for its products (4096 x 2048 -> 512 80
   // us with either).
-  s.stages = s.grain == 16 && size == 2 && tiles(64) * s.splits <= 768 ? 3 : 2;
+  s.stages = s.tile == 64 && s.grain == 16 && size == 2 && tiles(64) * s.splits <= 768 ? 3 : 2;
   return s;
 }
 

@@ -32,6 +32,9 @@ struct MatmulShape {
 // The shape for a product; `sums`: of rows (a weight gradient).  Operands' addresses and strides do not
 // matter to the splits.
 MatmulShape matmul_shape(const MatmulArgs& a, MatmulForm form, int dtype, bool sums);
+constexpr int kCus = 256;
+// Workgroups of a tile of this side that a CU's LDS holds at once.
+constexpr int matmul_resident(int tile, int stages) { return 160 * 1024 / (stages * 128 * 2 * tile); }
 hipError_t launch_matmul(const MatmulArgs& a, MatmulForm form, int dtype, const MatmulShape& shape, hipStream_t s);
 // Up to two rows: C(m, n) with B contiguous along k (`along`) or along n.  launch_matmul takes it.
 constexpr int kFewRows = 2;

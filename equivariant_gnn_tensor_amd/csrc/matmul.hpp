@@ -414,14 +414,13 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_kernel(const MatmulArgs a
 #endif
 }
 
-constexpr int kCus = 256;
-
 template <class T, int BM, int BN, int WM, int WN, int kStages, int kGrain>
 hipError_t launch_tiles(MatmulArgs a, MatmulForm form, hipStream_t s) {
   const int64_t tiles_m = (static_cast<int64_t>(a.M) + BM - 1) / BM, tiles_n = (static_cast<int64_t>(a.N) + BN - 1) / BN;
   const int64_t total = tiles_m * tiles_n * a.splits;
   // as many workgroups as LDS holds at once, each walking its tiles
-  constexpr int resident = 160 * 1024 / (kStages * 128 * (BM + BN));
+  static_assert(BM == BN, "one side");
+  constexpr int resident = matmul_resident(BM, kStages);
   if (total > INT32_MAX - kCus * resident) return hipErrorInvalidValue;   // a workgroup steps past the last tile by that much
   a.tiles_m = static_cast<int32_t>(tiles_m), a.tiles_n = static_cast<int32_t>(tiles_n);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(total, kCus * resident))), block(64 * WM * WN);
