@@ -11,7 +11,7 @@ from scipy import special
 
 from oracle import feedforward as ff
 from tests.gpu_helpers import note
-from tests.test_gpu_linear import DTYPES, HALF, KINDS, LEAST, U, close, f64, matrix, steps, weights
+from tests.test_gpu_linear import DTYPES, HALF, KINDS, LEAST, U, check_backward, close, f64, matrix, steps, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +102,22 @@ def test_slopes_far_out(kind, act, n_in):
         v = f64(cols)
         bound = U * (32 + 4 * np.abs(v) + 4 * v * v * (act == "gelu")) * terms(v, act) + steps(rows) * np.abs(ff.slope(v, act))
         close(b_bar / (0.5 * rows), ff.slope(v, act), bound, "slope")
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("pitch", [0, 3])
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_narrow_gradient(kind, pitch, act):
+    """One, two and four tiles of 32 columns on either side, whole pieces and odd ones, with and without a slope, each
+    output also on its own."""
+    etpc = _etpc()
+    for rows, n_in, n_out in ((300, 32, 32), (1001, 32, 64), (333, 64, 32), (33001, 64, 64), (32800, 128, 32), (77, 61, 31)):
+        note(f"narrow gradient {kind} {act} {rows}x{n_in}->{n_out} pitch={pitch}")
+        rng = np.random.default_rng(rows + pitch)
+        x, w = matrix(rng, rows, n_in, kind, pitch, shift=0.3), weights(rng, n_in, n_out, kind, "oi", pitch)
+        y_bar, z = matrix(rng, rows, n_out, kind, pitch, shift=0.1), matrix(rng, rows, n_out, kind, pitch)
+        z = z if act != "none" else None
+        bars = etpc.etpc_linear_backward(x, w, y_bar, z=z, act=act)
+        check_backward(*bars, f64(x), f64(w), f64(y_bar), None if z is None else f64(z), act, kind)
+        for k, name in enumerate("xwb"):
+            assert torch.equal(etpc.etpc_linear_backward(x, w, y_bar, z=z, act=act, want=(name,))[k], bars[k])
