@@ -32,18 +32,35 @@ struct BwdArgs {
 
 constexpr int kMost = 128;
 inline int tiles_of(int64_t n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; }
-// Forward: a wave that works on 32 rows alone needs many of them, or little work on each, against the tiles of
-// matmul.hpp (us here and there, silu).  64 -> 32: 3000 rows or less alike, 214980 bf16 14.4 and 20.3, fp32
-// 26.5 and 38.3; 64 -> 64 bf16: 65000 rows 10.8 and 9.0, 214980 22.6 and 23.8; 128 -> 32: 20.3 and 24.1,
-// fp32 41.4 and 52.9; 63 -> 63: fp32 59.6 and 121.9, 3000 rows 13.1 and 8.5.  Beyond four tiles of 32 x 32 only
-// where the tiles' loads are not aligned: 128 -> 64 bf16 32.5 and 27.5, 100 -> 60 37.3 and 47.1, 60 -> 100
-// fp32 100.7 and 145.6; 128 -> 128 bf16 61.0 and 37.3.
+// Forward: a wave that works on 32 rows alone needs many of them, or little work on each, against the tiles
+// of matmul.hpp.  Up to two tiles of 32 x 32 always (64 -> 32 silu: 3000 rows or less alike, 214980 bf16 14.4 us
+// and 20.3 with the tiles, fp32 26.5 and 38.3).  With more, rows past what those tiles take in one round (65536
+// in tiles of 128, 81920 in tiles of 64, some more where both load whole pieces; us here and with the tiles):
+//   16 bits, n_out <= 64: 64 -> 64 65000 rows 11.0 and 9.3, 83000 12.2 and 10.7, 90000 12.4 and 12.4, 214980 22.3
+//     and 22.2, 500000 35.9 and 46.0 (short of a round's end the tiles are ahead: 163000 19.8 and 15.3);
+//     90 -> 50 83000 rows 20.0 and 15.8, 100000 21.0 and 26.5;
+//   16 bits, n_out > 64: 33 -> 65 70000 rows 23.3 and 43.2; whole 16-byte pieces on both sides keep the tiles
+//     (32 -> 128 100000 rows 21.4 and 18.1);
+//   fp32, n_in <= 32: 32 -> 128 72000 rows 33.8 and 47.5, 60000 23.8 and 28.6, 40000 21.3 and 18.2;
+//   fp32, four tiles: rows whose outputs end inside 64 bytes, which the tiles write in pieces (62 -> 62 100000 rows
+//     32.9 and 56.3; 60 -> 60 83000 27.3 and 38.0, 70000 27.0 and 28.9; from 33 to 40 outputs alike within 40 %
+//     either way), not others (64 -> 64 150000 rows 35.3 and 29.6; 48 -> 64 100000 25.4 and 27.6, 400000 76.7 and 69.3);
+//   fp32, n_in > 64: whole pieces of x (96 -> 32 100000 rows 23.2 and 30.6; 75 -> 20 36.4 and 37.1, 150000 44.8
+//     and 38.5), not with more than 32 outputs (127 -> 63 150000 rows 82.2 and 74.3);
+//   fp32, eight tiles with n_out > 64: from 73 outputs on that end inside 64 bytes (50 -> 75 83000 rows 52.7 and
+//     65.1; 50 -> 70 100000 66.7 and 53.8, 50 -> 80 59.3 and 42.9).
 inline bool fits_fwd(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
   if (n_in > kMost || n_out > kMost) return false;
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;
   const bool aligned = n_in * size % 16 == 0 && n_out * size % 16 == 0;
   const int tiles = tiles_of(n_in) * tiles_of(n_out);
-  return tiles <= 2 || (rows > 65536 && tiles <= (aligned ? 4 : 8));
+  if (tiles <= 2) return true;
+  if (tiles > 8 || (tiles > 4 && aligned)) return false;
+  if (rows <= (n_out > 64 ? 65536 : n_in > 64 || (size == 2 && aligned) ? 90000 : 81920)) return false;
+  if (dtype != ETPC_F32) return n_out <= 64 || !aligned;
+  if (n_in > 64) return n_out <= 32 && n_in % 4 == 0;
+  if (n_out > 64) return n_in <= 32 || (n_out > 72 && n_out % 16 != 0);
+  return n_out % 16 != 0;
 }
 // Backward: the kernel keeps all of w_bar in a wave's registers, four tiles of 32 x 32, beside two rows'
 // worth of y_bar and z.  Four of them in fp32 take a wave longer than few rows are worth (64 -> 64: 20000 rows

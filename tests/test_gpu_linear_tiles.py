@@ -80,3 +80,14 @@ def test_repeated_rows_on_every_tile(kind, rows, n_in, n_out):
     assert bool((1.01 * exact.abs()[past] >= 65520).all()) and (kind == "f16" or not past.any())
     assert torch.equal(torch.sign(w_bar[past]).double(), torch.sign(exact[past]))
     check_backward(x_bar, torch.where(past, exact, w_bar.double()), b_bar, f64(x), f64(w), f64(y_bar), None, "none", kind)
+
+
+@pytest.mark.parametrize("kind,rows,n_in,n_out,layout,pitch", (
+    for_kinds(90001, 64, 64, "io", 0) + for_kinds(90007, 62, 62, "oi", 5) + for_kinds(81921, 62, 62, "io", 0) + for_kinds(81920, 62, 62, "io", 0)
+    + for_kinds(90033, 128, 32, "oi", 0) + for_kinds(90002, 127, 31, "io", 8) + for_kinds(65537, 32, 128, "io", 0)
+    + for_kinds(65540, 31, 99, "oi", 5) + for_kinds(65600, 50, 75, "io", 0) + for_kinds(65599, 50, 80, "oi", 0)
+    + for_kinds(90020, 90, 50, "io", 8) + for_kinds(90064, 48, 56, "oi", 8) + for_kinds(65536, 31, 99, "io", 0)
+    + for_kinds(65545, 33, 70, "io", 0)))
+def test_narrow_rows_past_a_round_of_tiles(kind, rows, n_in, n_out, layout, pitch):
+    """On either side of each limit past which a narrow layer takes the kernel that keeps its weights in LDS."""
+    run_case(rows, rows, n_in, n_out, kind, "gelu" if n_in % 2 else "tanh", layout, pitch)
