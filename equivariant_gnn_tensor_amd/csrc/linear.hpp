@@ -53,7 +53,7 @@ struct SlopeArgs {
   void* z_bar;          // or null
   float* part;          // or null
   int64_t ybs, zs, zbs;
-  int32_t rows, cols, parts, act;
+  int32_t rows, cols, act;
 };
 int slope_parts(int32_t rows, int32_t cols);
 hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t s);
