@@ -432,8 +432,9 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
 
 // ---------------------------------------------------------------- launches
 
-// As many workgroups as are resident, fewer where that gives every wave the same number of tiles
-// (214980 x 64 -> 64 bf16: 24.1 us with four a CU where three are resident, 21.1 with three).
+// As many workgroups as are resident (64 -> 64 bf16: four a CU, by LDS and by registers).  Fewer, so that every wave
+// has the same number of tiles, leaves loads out at once: 214980 x 64 -> 64 bf16 22.8 us with 840 of 1024, 21.4 with
+// all; 140000 x 17 -> 17 fp32 16.9 and 14.3; 500000 x 60 -> 31 bf16 34.3 and 35.3.
 template <class T, int IT, int OT, bool kEven>
 hipError_t launch_fwd(const FwdArgs& a, hipStream_t s) {
   static const int resident = [] {
@@ -442,8 +443,7 @@ hipError_t launch_fwd(const FwdArgs& a, hipStream_t s) {
     return e == hipSuccess && n > 0 ? 256 * n : 256;
   }();
   const int64_t units = (static_cast<int64_t>(a.rows) + 32 * kFwdThreads / 64 - 1) / (32 * kFwdThreads / 64);
-  const int64_t rounds = (units + resident - 1) / resident;
-  const unsigned groups = static_cast<unsigned>((units + rounds - 1) / rounds);
+  const unsigned groups = static_cast<unsigned>(std::min<int64_t>(units, resident));
   fwd_kernel<T, IT, OT, kEven><<<dim3(groups), dim3(kFwdThreads), 0, s>>>(a);
   return hipGetLastError();
 }

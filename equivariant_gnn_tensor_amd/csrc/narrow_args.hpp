@@ -33,22 +33,22 @@ struct BwdArgs {
 constexpr int kMost = 128;
 inline int tiles_of(int64_t n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; }
 // Forward: a wave that works on 32 rows alone needs many of them, or little work on each, against the tiles
-// of matmul.hpp.  Up to two tiles of 32 x 32 always (64 -> 32 silu: 3000 rows or less alike, 214980 bf16 14.4 us
-// and 20.3 with the tiles, fp32 26.5 and 38.3).  With more, rows past what those tiles take in one round (65536
+// of matmul.hpp.  Up to two tiles of 32 x 32 always (64 -> 32 silu: 3000 rows or less alike, 214980 bf16 13.6 us
+// and 20.5 with the tiles, fp32 26.1 and 39.0).  With more, rows past what those tiles take in one round (65536
 // in tiles of 128, 81920 in tiles of 64, some more where both load whole pieces; us here and with the tiles):
-//   16 bits, n_out <= 64: 64 -> 64 65000 rows 11.0 and 9.3, 83000 12.2 and 10.7, 90000 12.4 and 12.4, 214980 22.3
-//     and 22.2, 500000 35.9 and 46.0 (short of a round's end the tiles are ahead: 163000 19.8 and 15.3);
-//     90 -> 50 83000 rows 20.0 and 15.8, 100000 21.0 and 26.5;
-//   16 bits, n_out > 64: 33 -> 65 70000 rows 23.3 and 43.2; whole 16-byte pieces on both sides keep the tiles
-//     (32 -> 128 100000 rows 21.4 and 18.1);
-//   fp32, n_in <= 32: 32 -> 128 72000 rows 33.8 and 47.5, 60000 23.8 and 28.6, 40000 21.3 and 18.2;
+//   16 bits, n_out <= 64: 64 -> 64 65000 rows 11.2 and 9.1, 83000 12.7 and 10.7, 90000 12.7 and 12.9, 214980 20.7
+//     and 22.7, 500000 36.2 and 47.9 (short of a round's end the tiles are ahead: 163000 18.0 and 16.1);
+//     90 -> 50 83000 rows 17.8 and 16.0, 100000 20.9 and 26.4;
+//   16 bits, n_out > 64: 33 -> 65 70000 rows 20.9 and 42.3; whole 16-byte pieces on both sides keep the tiles
+//     (32 -> 128 100000 rows 21.4 and 18.6);
+//   fp32, n_in <= 32: 32 -> 128 72000 rows 34.4 and 48.3, 60000 24.6 and 29.2, 40000 21.4 and 18.8;
 //   fp32, four tiles: rows whose outputs end inside 64 bytes, which the tiles write in pieces (62 -> 62 100000 rows
-//     32.9 and 56.3; 60 -> 60 83000 27.3 and 38.0, 70000 27.0 and 28.9; from 33 to 40 outputs alike within 40 %
-//     either way), not others (64 -> 64 150000 rows 35.3 and 29.6; 48 -> 64 100000 25.4 and 27.6, 400000 76.7 and 69.3);
-//   fp32, n_in > 64: whole pieces of x (96 -> 32 100000 rows 23.2 and 30.6; 75 -> 20 36.4 and 37.1, 150000 44.8
-//     and 38.5), not with more than 32 outputs (127 -> 63 150000 rows 82.2 and 74.3);
-//   fp32, eight tiles with n_out > 64: from 73 outputs on that end inside 64 bytes (50 -> 75 83000 rows 52.7 and
-//     65.1; 50 -> 70 100000 66.7 and 53.8, 50 -> 80 59.3 and 42.9).
+//     33.3 and 56.3; 60 -> 60 83000 25.2 and 38.4, 70000 24.7 and 28.8; from 33 to 40 outputs alike within 40 %
+//     either way), not others (64 -> 64 150000 rows 33.6 and 29.3; 48 -> 64 100000 26.0 and 27.6, 400000 75.5 and 70.5);
+//   fp32, n_in > 64: whole pieces of x (96 -> 32 100000 rows 24.2 and 31.0; 75 -> 20 36.3 and 37.0, 150000 45.0
+//     and 38.5), not with more than 32 outputs (127 -> 63 150000 rows 82.9 and 74.4);
+//   fp32, eight tiles with n_out > 64: from 73 outputs on that end inside 64 bytes (50 -> 75 83000 rows 52.8 and
+//     64.5; 50 -> 70 100000 67.6 and 54.2, 50 -> 80 60.2 and 42.9).
 inline bool fits_fwd(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
   if (n_in > kMost || n_out > kMost) return false;
   const int64_t size = dtype == ETPC_F32 ? 4 : 2;
