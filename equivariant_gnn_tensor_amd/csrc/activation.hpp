@@ -27,8 +27,8 @@ __device__ inline float logistic(float x) {
 
 // For gelu: the tail Phi(-|z|) of the normal distribution, and e = exp(-z^2 / 2).  With a = |z| / sqrt 2
 // the tail is erfc(a) / 2 = e f(a), and f is 1 / (1 + a / 2) times a polynomial in it, fitted by
-// least squares reweighted towards the smallest relative error (4.7e-8 over 0 <= a <= 16, about 10
-// units of 2^-24 with its evaluation).  It does not cancel like 1 + erf, and takes a third of
+// least squares reweighted towards the smallest relative error (1e-7 over 0 <= a <= 16 with these
+// coefficients, 4e-7 with its evaluation in fp32).  It does not cancel like 1 + erf, and takes a third of
 // the library's erfc.  fp32 rows, bound by their products, take erfc.
 template <bool kWide>
 __device__ inline float normal_tail(float z, float& e) {

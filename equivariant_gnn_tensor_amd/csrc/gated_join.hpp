@@ -15,7 +15,8 @@
 // size reaches.  Backward: 4097 x 2047 fp32 (268 MB) 57 us, 4.7 TB/s, and 6.3 us for the second stage of
 // the column sums.  Its five rows and five column sums a thread are the registers; above 4096 columns
 // (a workgroup of 1024 to a row) four of the sums go to LDS: 8192 x 8192 bf16 243 us, 4.4 TB/s (549
-// with the registers spilled), fp32 504 (919).
+// with the registers spilled), fp32 504 (919; 13 still spilled with a gate).  Forward rows of 8193 to 16384 columns
+// spill 42 registers (fp32 with a gate), 16 (fp32), 14 and 10 (16 bits): 4096 x 16384 fp32 343 us, bf16 174, 3.9 TB/s.
 #pragma once
 
 #include "activation.hpp"

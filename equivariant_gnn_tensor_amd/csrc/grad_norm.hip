@@ -3,7 +3,7 @@
 //   norm = sqrt(sum g^2) or max |g|,  g *= min(1, max_norm / (norm + 1e-6))
 //
 // Memory bound: the gradients are read once for the norm, and read and written once more to be
-// clipped (201 M fp32, 805 MB: the norm 139 us, 5.8 TB/s).  Pointers and sizes travel in the launch's
+// clipped (805 MB: the norm of 201 M fp32 139.6 us, 5.8 TB/s, of 403 M bf16 143).  Pointers and sizes travel in the launch's
 // arguments (no copy to the device, so the calls can be captured).  The tensors are one long row of units, dealt in equal runs to the
 // workgroups: large and small tensors share the chip evenly, and a workgroup looks for its place
 // once.  Squares are exact in 64 bits and their sums neither overflow nor lose small tensors beside

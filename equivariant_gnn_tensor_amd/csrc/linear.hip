@@ -18,7 +18,8 @@ constexpr int64_t kMaxGroups = int64_t{1} << 20;
 // time.  A workgroup keeps its columns' sums in registers over all its rows and leaves one row
 // of them; they are added up in a fixed order afterwards (65408 x 1024 f16 sums alone 30 us, 4.5 TB/s).
 // z_bar is an operand of two products on the matrix cores, so it is rounded to the rows' type (2^-9 of
-// itself in bf16); as two 16-bit numbers, like narrow rows have it, it would double their time.
+// itself in bf16); as two 16-bit numbers, like narrow rows have it, it would double their time (65408 x 1024 ->
+// 4096 bf16 gelu: 920 of 1210 us).
 struct SlopeShape {
   int g;        // threads along a row
   int groups;   // workgroups along a row

@@ -10,18 +10,19 @@
 // rows' while these are worked on.  With the weights' fragment first, a lane gets four adjacent
 // columns of one row; swapping wave halves makes that eight, which are loaded and stored as one.
 //
-// The backward pass is one kernel: z_bar is a fragment for x_bar as it stands; for w_bar, whose
-// contraction runs over rows, it and x go through a few KB of LDS of the wave and are read
-// transposed.  The matrix cores take 16-bit numbers of z_bar, so it goes into both products as the
-// sum of two of them, the rounded one and what that leaves (2^-16 of z_bar in bf16, 2^-22 in fp16): one rounding
-// alone takes w_bar from 0.0017 to 0.0023 off (root mean square, bf16; the rounding of w_bar itself is 0.0017) and
-// saves 1.5 of 40 us.  w_bar's and b_bar's sums stay in registers over all of a wave's rows, are added up
+// The backward pass is one kernel: z_bar and x go through a few KB of LDS of the wave.  x_bar's fragments of
+// z_bar are read back as they were written, w_bar's, whose contraction runs over rows, transposed.  The
+// matrix cores take 16-bit numbers of z_bar, so it goes into both products as the sum of two of them, the
+// rounded one and what that leaves (off by 2^-16 of z_bar in bf16, 2^-22 in fp16): one rounding alone takes the
+// gradients from 0.0017 to 0.0023 off (root mean square, bf16; their own rounding is 0.0017) and saves 2 of 44
+// us.  w_bar's and b_bar's sums stay in registers over all of a wave's rows, are added up
 // over the workgroup's waves in LDS and leave one partial sum a workgroup, added in a fixed order
 // by a second launch.
 //
-// 214980 x 64 -> 64 bf16 silu: forward 21.6 us a call (82.6 MB, 3.8 TB/s; half of a wave's cycles are
-// waits), backward 42 (110 MB; 39.5 and the second launch), bound by conversions, slopes and the way
-// through LDS.
+// 214980 x 64 -> 64 bf16 silu: forward 21 us a call (82.6 MB, 3.9 TB/s; half of a wave's cycles are
+// waits), backward 44 (110 MB; 41.5 and the second launch's 4.7), bound by conversions, slopes and the way
+// through LDS.  16-bit rows that are not whole chunks spill 25 registers backward with 64 -> 64, 21 with 128 -> 32
+// and a slope, 5 without (63 -> 63 silu 80 us).
 #pragma once
 
 #include <algorithm>
@@ -340,7 +341,7 @@ __global__ __launch_bounds__(bwd_threads<T>()) void bwd_kernel(const BwdArgs a) 
 #pragma unroll
       for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {   // stored as they are: turned over like the forward pass 45.6 us, so 38.3
+        for (int g = 0; g < 2; ++g) {   // stored as they are: turned over like the forward pass 45.6 us for 38.3, before z_bar had its rest
           const int n = 32 * i + 16 * g + 8 * h;
           float v[8];
           eight(acc[i], g, v);

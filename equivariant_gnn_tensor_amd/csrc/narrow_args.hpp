@@ -64,7 +64,7 @@ inline bool fits_fwd(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
 }
 // Backward: the kernel keeps all of w_bar in a wave's registers, four tiles of 32 x 32, beside two rows'
 // worth of y_bar and z.  Four of them in fp32 take a wave longer than few rows are worth (64 -> 64: 20000 rows
-// 33.8 us and 30.5 with the products apart, 50000 37.3 and 39.5; bf16 20.2 and 24.3, 22.6 and 30.2).
+// 33.8 us and 30.5 with the products apart, 50000 36.9 and 39.5; bf16 20.8 and 24.3, 22.8 and 30.2).
 inline bool fits_bwd(int64_t rows, int64_t n_in, int64_t n_out, int32_t dtype) {
   if (n_in > kMost || n_out > 64) return false;
   const int tiles = tiles_of(n_in) * tiles_of(n_out);
